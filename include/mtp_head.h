@@ -347,6 +347,152 @@ int mtp_head_quantize_fp8(const uint16_t* w, uint8_t* q, float* row_scale, int32
                           int V, int H, void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * FP4 copies ("glm5next_mtp_head.rs", `head_fp8` doc: a low-precision copy of lm_head used for
+ * drafting only; the pages stop at FP8). A [V, H] BF16 matrix becomes three arrays, with
+ * Hp = mtp_head_fp4_padded(H) (H rounded up to a multiple of 256):
+ *
+ *   q            [V, Hp/2]   uint8  E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; bit 3
+ *                                   is the sign), column 2i in the low half of byte i
+ *   block_scale  [V, Hp/16]  uint8  E4M3 scale of each 16 columns (non-negative)
+ *   row_scale    [V]         fp32
+ *
+ *   row_scale[v]      = fp32( max_k |w[v, k]| / 2688 )                            (2688 = 6 * 448)
+ *   block_scale[v, j] = e4m3( max_{k in block j} |w[v, k]| / (6 row_scale[v]) )
+ *   q[v, k]           = e2m1( w[v, k] / (block_scale[v, k/16] row_scale[v]) )
+ *
+ * where e4m3 and e2m1 round the real quotient once, to nearest even, and saturate; columns from H
+ * to Hp are zeros. An all-zero row (or one so small that row_scale rounds to 0) gives zeros, and so
+ * does an all-zero block. A NaN or Inf weight stores MTP_ERR_NONFINITE in `status` (required here)
+ * and makes that row zeros. 1 <= H <= 131072 (an eh_proj row of the longest head). q and
+ * block_scale must be 16-byte aligned.
+ * mtp_head_dequantize_fp4 writes the BF16 matrix that a copy stands for:
+ *   w[v, k] = bf16( fp32( q * block_scale * row_scale ) ), w [V, H] BF16.
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_fp4_padded(int H); /* 0 for H outside the range */
+
+int mtp_head_quantize_fp4(const uint16_t* w, uint8_t* q, uint8_t* block_scale, float* row_scale,
+                          int32_t* status, int V, int H, void* stream);
+
+int mtp_head_dequantize_fp4(const uint8_t* q, const uint8_t* block_scale, const float* row_scale,
+                            uint16_t* w, int V, int H, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Output stage over an FP4 copy of lm_head: mtp_head_logits_argmax_batched with
+ *   logit_b[v] = row_scale[v] * sum_k block_scale[v, k/16] q[v, k] xhat_b[k],
+ * xhat_b the BF16 output of shared_head.norm as there; the sum in fp32. logits (optional), draft,
+ * status, B (1..16), H, V and eps as there. Two kernels: the normalised rows into the workspace,
+ * then one sweep over the copy.
+ *   workspace   device scratch of at least mtp_head_fp4_workspace_bytes(B, H, V) bytes, its first
+ *               2304 bytes zero-filled once before its first use (the kernels leave them zero). Two
+ *               calls that may run at the same time need different workspaces; one workspace serves
+ *               every B up to the one it was sized for.
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_logits_argmax_fp4(const uint16_t* x, const uint16_t* final_norm_w, const uint8_t* q,
+                               const uint8_t* block_scale, const float* row_scale, float* logits,
+                               int32_t* draft, int32_t* status, void* workspace,
+                               size_t workspace_bytes, int B, int H, int V, float eps, void* stream);
+
+size_t mtp_head_fp4_workspace_bytes(int B, int H, int V); /* 0 for invalid shapes */
+
+/* ------------------------------------------------------------------------------------------
+ * Rows of activations times an FP4 weight matrix, both operands in four bits. The rows of x are
+ * quantised as by mtp_head_quantize_fp4 (into the workspace), then
+ *   y[r, n] = bf16( sum_k value(Q(x))[r, k] * value(q)[n, k] ),   fp32 accumulation,
+ * where value is code * block scale * row scale.
+ *   x [R, K] BF16, q / block_scale / row_scale the FP4 copy of a [N, K] matrix, y [R, N] BF16
+ *   status      optional: MTP_ERR_NONFINITE when a row of x holds a NaN or Inf (its y row is zeros)
+ *   workspace   at least mtp_head_linear_fp4_workspace_bytes(R, N, K) bytes, no initialisation
+ *               needed; calls that may run at the same time need different ones
+ *   1 <= R <= 65536, 1 <= N, 1 <= K <= 131072
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_linear_fp4(const uint16_t* x, const uint8_t* q, const uint8_t* block_scale,
+                        const float* row_scale, uint16_t* y, int32_t* status, void* workspace,
+                        size_t workspace_bytes, int R, int N, int K, void* stream);
+
+size_t mtp_head_linear_fp4_workspace_bytes(int R, int N, int K); /* 0 for invalid shapes */
+
+/* Context-row input stage (mtp_head_context_rows) with an FP4 copy of eh_proj ([H, 2H]): the
+ * normalised concat rows, then mtp_head_linear_fp4 over them. A row whose token is outside [0, V)
+ * is zeros and status (optional) gets MTP_ERR_TOKEN_RANGE. 1 <= R <= 65536 rows (a draft step's
+ * sequences or a prompt's rows alike); H a multiple of 8 (MTP_ERR_NOT_IMPLEMENTED otherwise).
+ * workspace: at least mtp_head_context_fp4_workspace_bytes(R, H) bytes, no initialisation. */
+int mtp_head_context_rows_fp4(const uint16_t* embed, const uint16_t* enorm_w,
+                              const uint16_t* hnorm_w, const uint8_t* eh_q,
+                              const uint8_t* eh_block_scale, const float* eh_row_scale,
+                              const int32_t* tokens, const uint16_t* target_hidden,
+                              uint16_t* x_out, int32_t* status, void* workspace,
+                              size_t workspace_bytes, int R, int H, int V, float eps,
+                              void* stream);
+
+size_t mtp_head_context_fp4_workspace_bytes(int R, int H); /* 0 for invalid shapes */
+
+/* ------------------------------------------------------------------------------------------
+ * Sampling: one token per row of logits from a given uniform random number (the source drafts
+ * greedily, `argmax_bf16`; speculative decoding at a temperature needs drafts drawn from the
+ * drafter's distribution, and that distribution for the acceptance).
+ *
+ *   logits       [R, ld]  fp32 (MTP_LOGITS_FP32) or BF16 (MTP_LOGITS_BF16); ld >= V elements
+ *   temperature  [R] fp32  optional (NULL: 1); 0 takes the largest logit (lowest index of a tie)
+ *   top_k        [R] int32 optional (NULL, <= 0 or >= V: off)
+ *   top_p        [R] fp32  optional (NULL or >= 1: off)
+ *   min_p        [R] fp32  optional (NULL or 0: off)
+ *   u            [R] fp32  in [0, 1); may be NULL when only probs is asked for
+ *   token        [R] int32 optional output
+ *   prob         [R] fp32  optional output: the token's probability in the restricted distribution
+ *   probs        [R, V] fp32 optional output: that distribution
+ *   status       [1] int32 optional; MTP_ERR_ARG if a row's parameters are out of range
+ *                (temperature negative or not finite, top_p negative or NaN, min_p outside [0, 1], u
+ *                outside [0, 1)): that row's token is -1, its prob and probs are 0
+ *
+ * With m = max_i l_i: w_i = exp((l_i - m) / temperature), and 1 where l_i = m (several +Inf share
+ * alike). NaN counts as -Inf; -Inf is never drawn; a row of nothing else gives token -1, prob and
+ * probs 0 (no error). In the order (logit descending, index ascending) the tokens kept are a
+ * prefix: the first top_k; of those, the ones whose preceding mass is less than top_p times the mass
+ * of all of those; of those, the ones with l_i >= m + temperature * ln(min_p). At least one is
+ * kept. The token is the lowest index whose cumulative kept mass, in index order, exceeds u times
+ * the whole. Masses are summed in 64-bit fixed point: results do not vary from run to run.
+ * 1 <= R <= 65536, 1 <= V < 2^31. No workspace.
+ * ---------------------------------------------------------------------------------------- */
+enum { MTP_LOGITS_FP32 = 0, MTP_LOGITS_BF16 = 1 };
+
+int mtp_head_sample(const void* logits, int logits_dtype, int64_t ld, const float* temperature,
+                    const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+                    int32_t* token, float* prob, float* probs, int32_t* status, int R, int V,
+                    void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Acceptance of drafts by rejection sampling: the emitted tokens are distributed as if each had
+ * been drawn from the target.
+ *
+ *   target_probs  [B, D + 1, V] fp32  the target's distribution at each draft position and after
+ *   draft_probs   [B, D, V]     fp32  the distributions that the drafts were drawn from; NULL for
+ *                                     greedy drafts (each distribution is its token alone)
+ *   draft_tokens  [B, D]        int32
+ *   draft_len     [B]           int32 optional: drafts of each sequence, 0..D (NULL: D each)
+ *   u             [B, D + 1]    fp32  uniform in [0, 1): u[b, i] decides draft i, u[b, D] draws the
+ *                                     token after the accepted ones
+ *   tokens        [B, D + 1]    int32 output: the accepted drafts, the drawn token, then -1
+ *   accepted      [B]           int32 output: how many drafts were accepted
+ *   prob          [B]           fp32  optional output: the drawn token's probability in the
+ *                                     distribution that it was drawn from
+ *   status        [1]           int32 optional; see below
+ *
+ * With n = draft_len[b], p_i = target_probs[b, i], q_i = draft_probs[b, i], x_i = draft_tokens[b, i]:
+ * draft i is accepted while u_i q_i(x_i) < p_i(x_i). After a accepted drafts the next token comes from
+ * max(p_a - q_a, 0) when a < n (from p_a itself if that has no mass), from p_n when all are
+ * accepted: the lowest index whose cumulative mass exceeds u_D times the whole. Probabilities are
+ * taken into [0, 1] (NaN as 0) and need not sum to one. A distribution without mass gives token -1
+ * and prob 0. A draft outside [0, V) that is reached is rejected (MTP_ERR_TOKEN_RANGE); a sequence
+ * with draft_len outside 0..D, or u outside [0, 1) at any i < n or at D, gives accepted 0, tokens -1
+ * and prob 0 (MTP_ERR_ARG).
+ * 1 <= B <= 65536, 1 <= D <= 1024, 1 <= V < 2^31. No workspace. `tokens` must not overlap the inputs.
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_verify(const float* target_probs, const float* draft_probs,
+                    const int32_t* draft_tokens, const int32_t* draft_len, const float* u,
+                    int32_t* tokens, int32_t* accepted, float* prob, int32_t* status, int B, int D,
+                    int V, void* stream);
+
+/* ------------------------------------------------------------------------------------------
  * Give-up time of the kernels' stage waits (no counterpart on the source pages, which have no
  * device-side waits: this library's kernels wait on shared-memory barriers for their weight
  * copies and for each other's stages, and every such wait is bounded so that a stalled copy can

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/mtp_head.h"
+#include "checks.h"
 #include "common.cuh"
 #include "internal.h"
 #include "host_back.h"
@@ -21,21 +22,15 @@ using mtp::kMaxB;
 constexpr int kMaxContextRows = 65536;
 constexpr int kMaxPickShards = 65536;  // picks combined by one mtp_head_pick_combine call
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using mtp::aligned;
+using mtp::check_eps;
+using mtp::map_cuda;
 
 int check_shape(int B, int H, int V) {
   if (B < 1 || B > kMaxB) return MTP_ERR_SHAPE;
   if (H < 1 || H > 65536) return MTP_ERR_SHAPE;
   if (V < 1) return MTP_ERR_SHAPE;
   return MTP_OK;
-}
-
-int check_eps(float eps) { return (eps >= 0.0f && !isinf(eps)) ? MTP_OK : MTP_ERR_ARG; }
-
-int map_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return MTP_OK;
-  if (e == cudaErrorNotSupported) return MTP_ERR_NOT_IMPLEMENTED;
-  return MTP_ERR_CUDA;
 }
 
 int validate_input(const uint16_t* embed, const uint16_t* enorm_w, const uint16_t* hnorm_w,

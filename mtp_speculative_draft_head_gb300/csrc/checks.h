@@ -1,0 +1,32 @@
+// Host-side argument checks shared by the C entry points.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/mtp_head.h"
+
+namespace mtp {
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+inline int check_eps(float eps) { return (eps >= 0.0f && !isinf(eps)) ? MTP_OK : MTP_ERR_ARG; }
+
+inline int map_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return MTP_OK;
+  if (e == cudaErrorNotSupported) return MTP_ERR_NOT_IMPLEMENTED;
+  return MTP_ERR_CUDA;
+}
+
+// A C entry point's body: no C++ exception (an allocation or a lock that failed) leaves the library.
+template <class Fn>
+int guarded(Fn&& fn) {
+  try {
+    return fn();
+  } catch (...) {
+    return MTP_ERR_CUDA;
+  }
+}
+
+}  // namespace mtp

@@ -1,0 +1,255 @@
+// The FP4 (E2M1) copy of a BF16 matrix and back ("glm5next_mtp_head.rs", `head_fp8` doc: a
+// low-precision copy of lm_head used for drafting only; here four bits a weight, with a scale per
+// 16 weights and one per row -- the format is in fp4.cuh).
+//
+// The codes without a division per element, as in the FP8 quantiser (quantize.cu): with
+// r = 1 / (s_j rs), formed in fp32, the products |w| r (1 + 2^-21) and |w| r (1 - 2^-21) bracket
+// the real quotient strictly (s_j rs, its reciprocal, the factor and the product round by at most
+// 2^-24 each, together less than 2^-21). The conversion is monotonic, so equal codes of both
+// bracket ends are the code of the quotient; otherwise (a rounding boundary inside the bracket)
+// the quotient is formed in fp64 and handed to the conversion through round-to-odd. fp64 decides
+// every case: w has 8 significant bits, s_j rs 28 and a boundary 3, so a quotient that is not on
+// the boundary differs from it by at least 2^-40 of its size. The block scales go the same way.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace mtp {
+
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr float kUp = 1.0f + 0x1p-21f, kDn = 1.0f - 0x1p-21f;
+constexpr float kSmallRs = 0x1p-100f;  // below: s_j rs or its reciprocal may leave the normal range
+
+// Two E4M3 codes (round to nearest even, satfinite): byte 0 from lo, byte 1 from hi.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Eight E2M1 codes (round to nearest even, satfinite), v[i] in bits 4i..4i+3.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(d)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return d;
+}
+// fp64 -> fp32 by round-to-odd: a following rounding to a few bits is the rounding of q itself.
+__device__ __forceinline__ float to_odd(double q) {
+  float f = __double2float_rz(q);
+  if (static_cast<double>(f) != q) f = __uint_as_float(__float_as_uint(f) | 1u);
+  return f;
+}
+
+// E4M3 code of amax / (6 rs), rs > 0.
+__device__ __forceinline__ uint32_t block_scale_code(float amax, float rs, float r6_up, float r6_dn) {
+  if (rs >= kSmallRs) {
+    const uint32_t two = e4m3x2(__fmul_rn(amax, r6_up), __fmul_rn(amax, r6_dn));
+    if ((two & 0xFFu) == (two >> 8)) return two & 0xFFu;
+  }
+  return e4m3x2(to_odd(static_cast<double>(amax) / (6.0 * static_cast<double>(rs))), 0.0f) & 0xFFu;
+}
+
+// Eight codes of the BF16 pairs u[0..3] for the block scale value s (> 0) and row scale rs.
+__device__ __forceinline__ uint32_t codes8(const uint32_t (&u)[4], float s, float rs, float r_up, float r_dn) {
+  float f[8], a[8];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    f[2 * t] = bf16_lo(u[t]);
+    f[2 * t + 1] = bf16_hi(u[t]);
+  }
+  if (rs >= kSmallRs) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) a[t] = __fmul_rn(f[t], r_up);
+    const uint32_t up = e2m1x8(a);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) a[t] = __fmul_rn(f[t], r_dn);
+    if (up == e2m1x8(a)) return up;
+  }
+  const double d = static_cast<double>(s) * static_cast<double>(rs);  // exact: 4 + 24 bits
+#pragma unroll
+  for (int t = 0; t < 8; ++t) a[t] = to_odd(static_cast<double>(f[t]) / d);
+  return e2m1x8(a);
+}
+
+// max of the two 16-bit halves, lane by lane
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mag_max(uint32_t m, const uint4& u) {
+  m = max_u16x2(m, u.x & 0x7FFF7FFFu);
+  m = max_u16x2(m, u.y & 0x7FFF7FFFu);
+  m = max_u16x2(m, u.z & 0x7FFF7FFFu);
+  return max_u16x2(m, u.w & 0x7FFF7FFFu);
+}
+
+// 16 columns starting at k0 of a row (zeros past k).
+template <bool VEC>
+__device__ __forceinline__ void load16(const uint16_t* row, int k0, int k, uint4& a, uint4& b) {
+  a = b = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (VEC) {  // k % 8 == 0 and 16-byte aligned rows
+    if (k0 < k) a = *reinterpret_cast<const uint4*>(row + k0);
+    if (k0 + 8 < k) b = *reinterpret_cast<const uint4*>(row + k0 + 8);
+  } else {
+    uint32_t u[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const uint32_t lo = k0 + 2 * t < k ? row[k0 + 2 * t] : 0u;
+      const uint32_t hi = k0 + 2 * t + 1 < k ? row[k0 + 2 * t + 1] : 0u;
+      u[t] = lo | (hi << 16);
+    }
+    a = make_uint4(u[0], u[1], u[2], u[3]);
+    b = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+}
+
+// TPR threads of a block (a warp, or the whole block) per row, two passes over it: the magnitude
+// maximum, then 16 columns (one block scale) a thread at a time.
+template <int TPR, bool VEC>
+__global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t* __restrict__ w, uint8_t* __restrict__ q,
+                                                                 uint8_t* __restrict__ bs, float* __restrict__ rs_out,
+                                                                 int32_t* __restrict__ status,
+                                                                 const int32_t* __restrict__ valid, int rows, int k) {
+  __shared__ uint32_t red[kQThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = threadIdx.x % TPR;
+  const int kp = fp4_padded(k), nblk = kp / kFp4Block;
+  pdl_wait_prior_grid();
+  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x) / TPR; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * kQThreads / TPR) {
+    const uint16_t* wr = w + row * k;
+    const bool ok = valid == nullptr || valid[row] != 0;
+    uint32_t m = 0;
+    if (ok)
+      for (int b = t; b * kFp4Block < k; b += TPR) {
+        uint4 u0, u1;
+        load16<VEC>(wr, b * kFp4Block, k, u0, u1);
+        m = mag_max(mag_max(m, u0), u1);
+      }
+    uint32_t mx = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+    if constexpr (TPR > 32) {
+      if (lane == 0) red[warp] = mx;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kQThreads / 32; ++i) mx = max(mx, red[i]);
+      __syncthreads();
+    }
+    float rs = __fdiv_rn(bf16_bits_to_f32(mx), 2688.0f);
+    if (mx >= 0x7F80u) {  // a NaN or Inf in the row
+      if (t == 0) store_status(status, MTP_ERR_NONFINITE);
+      rs = 0.0f;
+    }
+    if (t == 0) rs_out[row] = rs;
+    const float r6 = rs >= kSmallRs ? __frcp_rn(__fmul_rn(6.0f, rs)) : 0.0f;
+    const float r6_up = __fmul_rn(r6, kUp), r6_dn = __fmul_rn(r6, kDn);
+    uint8_t* qr = q + row * (kp / 2);
+    uint8_t* br = bs + row * nblk;
+    for (int b = t; b < nblk; b += TPR) {
+      uint32_t c0 = 0u, c1 = 0u, sc = 0u;
+      if (rs > 0.0f && b * kFp4Block < k) {
+        uint4 u0, u1;
+        load16<VEC>(wr, b * kFp4Block, k, u0, u1);
+        const uint32_t bm = mag_max(mag_max(0u, u0), u1);
+        sc = block_scale_code(bf16_bits_to_f32(max(bm & 0xFFFFu, bm >> 16)), rs, r6_up, r6_dn);
+        if (sc != 0u) {
+          const float s = e4m3_value(sc);
+          const float r = rs >= kSmallRs ? __frcp_rn(__fmul_rn(s, rs)) : 0.0f;
+          const float r_up = __fmul_rn(r, kUp), r_dn = __fmul_rn(r, kDn);
+          c0 = codes8({u0.x, u0.y, u0.z, u0.w}, s, rs, r_up, r_dn);
+          c1 = codes8({u1.x, u1.y, u1.z, u1.w}, s, rs, r_up, r_dn);
+        }
+      }
+      reinterpret_cast<uint2*>(qr)[b] = make_uint2(c0, c1);
+      br[b] = static_cast<uint8_t>(sc);
+    }
+  }
+  pdl_launch_dependents();
+}
+
+// bf16( fp32( code * s_j * rs ) ), 16 columns a thread.
+template <bool VEC>
+__global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const Fp4Matrix m, uint16_t* __restrict__ w, int rows,
+                                                                   int k) {
+  const int kp = fp4_padded(k), nblk = (k + kFp4Block - 1) / kFp4Block;
+  const int64_t total = static_cast<int64_t>(rows) * nblk;
+  pdl_wait_prior_grid();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kQThreads) {
+    const int64_t row = i / nblk;
+    const int b = static_cast<int>(i - row * nblk);
+    const uint2 c = reinterpret_cast<const uint2*>(m.q + row * (kp / 2))[b];
+    const uint32_t s2 = e4m3x2_to_f16x2(m.bs[row * (kp / kFp4Block) + b] * 0x0101u);
+    const float rs = m.rs[row];
+    uint32_t o[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[4];
+      e2m1x8_to_f16x2x4(h == 0 ? c.x : c.y, v);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t p = f16x2_mul(v[t], s2);  // exact
+        o[4 * h + t] = bf16_bits_rn(__fmul_rn(f16_lo(p), rs)) | (bf16_bits_rn(__fmul_rn(f16_hi(p), rs)) << 16);
+      }
+    }
+    uint16_t* dst = w + row * k + b * kFp4Block;
+    if constexpr (VEC) {
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      if (b * kFp4Block + 8 < k) reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+        if (b * kFp4Block + t < k) dst[t] = static_cast<uint16_t>(o[t >> 1] >> (16 * (t & 1)));
+    }
+  }
+  pdl_launch_dependents();
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_quantize(const uint16_t* w, uint8_t* q, uint8_t* bs, float* rs, int32_t* status,
+                                const int32_t* valid, int rows, int k, cudaStream_t stream) {
+  DeviceInfo di;
+  cudaError_t err = device_info(&di);
+  if (err != cudaSuccess) return err;
+  const bool vec = k % 8 == 0;
+  const bool wide = rows < di.sm_count * 8;  // fewer rows than warps in flight: a block per row
+  const void* kern = wide ? (vec ? reinterpret_cast<const void*>(fp4_quantize_kernel<kQThreads, true>)
+                                 : reinterpret_cast<const void*>(fp4_quantize_kernel<kQThreads, false>))
+                          : (vec ? reinterpret_cast<const void*>(fp4_quantize_kernel<32, true>)
+                                 : reinterpret_cast<const void*>(fp4_quantize_kernel<32, false>));
+  const int per_block = wide ? 1 : kQThreads / 32;
+  int64_t blocks = (static_cast<int64_t>(rows) + per_block - 1) / per_block;
+  if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
+  void* args[] = {&w, &q, &bs, &rs, &status, &valid, &rows, &k};
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0, stream, args);
+}
+
+cudaError_t launch_fp4_dequantize(const Fp4Matrix& m, uint16_t* w, int rows, int k, cudaStream_t stream) {
+  DeviceInfo di;
+  cudaError_t err = device_info(&di);
+  if (err != cudaSuccess) return err;
+  const bool vec = k % 8 == 0;
+  const int64_t total = static_cast<int64_t>(rows) * ((k + kFp4Block - 1) / kFp4Block);
+  int64_t blocks = (total + kQThreads - 1) / kQThreads;
+  if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
+  Fp4Matrix mm = m;
+  void* args[] = {&mm, &w, &rows, &k};
+  return launch_pdl(vec ? reinterpret_cast<const void*>(fp4_dequantize_kernel<true>)
+                        : reinterpret_cast<const void*>(fp4_dequantize_kernel<false>),
+                    dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0, stream, args);
+}
+
+}  // namespace mtp

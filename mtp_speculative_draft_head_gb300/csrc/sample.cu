@@ -1,0 +1,826 @@
+// Drafts drawn by sampling, and the acceptance of drafts.
+//
+// sample: one token per row of logits, by inversion of the cumulative distribution. With
+// m = max_i l_i the weight of token i is w_i = exp((l_i - m) / T). Sorted by (logit descending,
+// index ascending), the tokens kept are a prefix of that order: the first top_k; of those, the ones
+// whose preceding mass is below top_p times the mass of all of them; of those, the ones with
+// l_i >= m + T ln(min_p). The token is the lowest index whose cumulative kept mass, in index order,
+// exceeds u times the whole.
+//
+// No sort of the row: a prefix is { i : key_i >= cut } for one 64-bit key (the logit's order bits,
+// then the complement of the index), and the cut is found by histograms. Round 1 bins the row by
+// its distance from the maximum, linearly over the row's range (2048 bins, which spreads a
+// language model's bell-shaped logits better than their exponent bits would); the bin that holds
+// the cut is gathered and sorted when it has at most kGather entries, and is otherwise split by the
+// key's bits, 11 at a time, until it has.
+//
+// Masses are 64-bit fixed-point numbers (2^62 / 2^ceil(log2 V) for a weight of one), so sums do not
+// depend on the order of the atomics or of the threads: the same inputs give the same token
+// whatever the cluster size. Weights are formed in fp32 from an exponent kept as a double-float:
+// relative error ~2^-23, against the 2^-24 of the given random numbers.
+//
+// A cluster of CTAs shares a row. Each keeps its slice in shared memory, so the row is read from
+// HBM once; maxima, histograms and masses are combined through distributed shared memory.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+#include "sample.h"
+
+namespace mtp {
+
+namespace {
+
+constexpr int kT = 512;           // threads per CTA
+constexpr int kW = kT / 32;
+constexpr int kMaxC = 16;         // CTAs per cluster
+constexpr int kBins = 2048;
+constexpr int kGather = 1024;     // candidates sorted at once
+constexpr int kSliceUnit = kT;    // a slice is a multiple of this: every warp owns whole 32-element steps
+
+typedef unsigned long long u64;
+
+// ------------------------------------------------------------------------------- cluster helpers
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of this CTA's shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_peer32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ u64 ld_peer(uint32_t addr) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_peer32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t add_peer32(uint32_t addr, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(addr), "r"(v) : "memory");
+  return r;
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+__device__ __forceinline__ u64 warp_inclusive(u64 v, int lane) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += o;
+  }
+  return v;
+}
+
+// ------------------------------------------------------------------------------- numbers
+// v >= 0 as a fixed-point number with `frac` fraction bits (<= 62), to nearest; v < 2.
+__device__ __forceinline__ u64 to_fixed(float v, int frac) {
+  const uint32_t u = __float_as_uint(v);
+  const int e = static_cast<int>(u >> 23);  // sign bit is 0
+  if (e == 0) return 0ull;                  // below 2^-126
+  const u64 m = (u & 0x7FFFFFu) | 0x800000u;
+  const int sh = e - 150 + frac;  // v = m 2^(e - 150)
+  if (sh >= 0) return m << sh;
+  if (sh < -24) return 0ull;
+  return (m + (1ull << (-sh - 1))) >> -sh;
+}
+
+// floor(u * z) for u in [0, 1).
+__device__ __forceinline__ u64 scale_floor(float u, u64 z) {
+  const uint32_t b = __float_as_uint(u);
+  const int e = static_cast<int>(b >> 23);
+  const u64 m = e == 0 ? (b & 0x7FFFFFu) : ((b & 0x7FFFFFu) | 0x800000u);
+  const int sh = 150 - (e == 0 ? 1 : e);  // u = m 2^-sh, sh >= 24
+  const u64 hi = __umul64hi(m, z), lo = m * z;
+  if (sh >= 128) return 0ull;
+  if (sh >= 64) return hi >> (sh - 64);
+  return (hi << (64 - sh)) | (lo >> sh);
+}
+
+// Whether part < p * whole, for 0 <= p < 1, exactly: part <= floor(p whole) unless p whole is whole.
+__device__ __forceinline__ u64 scale_ceil(float p, u64 z) {
+  const uint32_t b = __float_as_uint(p);
+  const int e = static_cast<int>(b >> 23);
+  const u64 m = e == 0 ? (b & 0x7FFFFFu) : ((b & 0x7FFFFFu) | 0x800000u);
+  const int sh = 150 - (e == 0 ? 1 : e);
+  const u64 hi = __umul64hi(m, z), lo = m * z;
+  if (sh >= 128) return (hi | lo) ? 1ull : 0ull;
+  if (sh >= 64) {
+    const u64 q = hi >> (sh - 64);
+    const u64 rem = (sh == 64 ? 0ull : hi << (128 - sh)) | lo;
+    return q + (rem ? 1ull : 0ull);
+  }
+  const u64 q = (hi << (64 - sh)) | (lo >> sh);
+  return q + ((lo << (64 - sh)) ? 1ull : 0ull);
+}
+
+// Order of floats as unsigned numbers (no NaN); -0 is taken as +0.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  uint32_t u = __float_as_uint(v);
+  if ((u & 0x7FFFFFFFu) == 0u) u = 0u;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// exp(-(m - l) / T) for l <= m: the difference exactly (TwoSum), times log2(e) / T as a double-float,
+// split into a whole power of two and 2^f, |f| <= 1/2, by the exponential series (eight terms:
+// remainder 0.3466^8 / 8! < 2^-27).
+struct Weigh {
+  float m, ch, cl;
+  __device__ __forceinline__ float operator()(float l) const {
+    if (l == m) return 1.0f;
+    float dh, dl;
+    two_sum(m, -l, dh, dl);
+    const float th = __fmul_rn(dh, ch);
+    if (!(th < 120.0f)) return 0.0f;  // below 2^-120 of the maximum's weight (NaN: an infinite distance)
+    const float tl = __fmaf_rn(dh, ch, -th) + __fmaf_rn(dh, cl, __fmul_rn(dl, ch));
+    const float n = rintf(th);
+    const float f = -((th - n) + tl);
+    const float y = f * 0.69314718055994530942f;
+    float p = 1.0f / 5040.0f;
+    p = __fmaf_rn(p, y, 1.0f / 720.0f);
+    p = __fmaf_rn(p, y, 1.0f / 120.0f);
+    p = __fmaf_rn(p, y, 1.0f / 24.0f);
+    p = __fmaf_rn(p, y, 1.0f / 6.0f);
+    p = __fmaf_rn(p, y, 0.5f);
+    p = __fmaf_rn(p, y, 1.0f);
+    p = __fmaf_rn(p, y, 1.0f);
+    return __uint_as_float(__float_as_uint(p) - (static_cast<uint32_t>(static_cast<int>(n)) << 23));
+  }
+};
+
+// ------------------------------------------------------------------------------- shared state
+struct Shared {
+  u64 wsum[kW];            // per-warp masses of this CTA
+  u64 cta[kMaxC];          // every CTA's mass (pushed by its peers)
+  uint32_t cmax[kMaxC];    // every CTA's largest / smallest logit (order bits)
+  uint32_t cmin[kMaxC];
+  uint32_t wmax[kW], wmin[kW];
+  u64 scan[kW];
+  uint32_t scan_n[kW];
+  // the bin that holds the cut: number, entries and mass before it, its entries
+  int hit;
+  uint32_t before_n, hit_n;
+  u64 before_m;
+  uint32_t gathered;       // leader: candidates received
+  u64 cut, cut_mass;       // published by the leader
+};
+// Dynamic shared memory: Shared, the local histogram (u64 mass, u32 count), the cluster's, the
+// gather buffer, then the slice.
+constexpr size_t kHistBytes = kBins * 12;
+constexpr size_t kFixedSmem = (sizeof(Shared) + 127) / 128 * 128 + 2 * kHistBytes + kGather * 8;
+
+struct Hist {
+  u64* mass;
+  uint32_t* n;
+};
+
+// ------------------------------------------------------------------------------- inverse of the cdf
+// The lowest index of the row whose cumulative mass exceeds floor(u z). Every warp owns `seg`
+// consecutive elements (a multiple of 32) of the slice that starts at i0; s.wsum holds this CTA's
+// per-warp masses, s.cta every CTA's. The one warp that finds it calls found(index).
+template <class MassFn, class Found>
+__device__ void locate(const Shared& s, uint32_t rank, u64 target, int64_t i0, int64_t seg, int64_t n, MassFn mass,
+                       Found found) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  u64 before = 0;
+  for (uint32_t r = 0; r < rank; ++r) before += s.cta[r];
+  for (int w = 0; w < warp; ++w) before += s.wsum[w];
+  if (target < before || target - before >= s.wsum[warp]) return;
+  for (int64_t j = i0 + warp * seg; j < i0 + (warp + 1) * seg; j += 32) {
+    const int64_t i = j + lane;
+    const u64 m = i < n ? mass(i) : 0ull;
+    const u64 c = warp_inclusive(m, lane);
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + c > target);
+    if (hit) {
+      if (lane == __ffs(hit) - 1) found(i);
+      return;
+    }
+    before += __shfl_sync(0xffffffffu, c, 31);
+  }
+}
+
+// ------------------------------------------------------------------------------- sampler
+template <bool BF16, bool RES>
+__global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int nc, int64_t slice, int frac) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  Shared& s = *reinterpret_cast<Shared*>(dyn);
+  uint8_t* p = dyn + (sizeof(Shared) + 127) / 128 * 128;
+  Hist loc{reinterpret_cast<u64*>(p), reinterpret_cast<uint32_t*>(p + kBins * 8)};
+  p += kHistBytes;
+  Hist all{reinterpret_cast<u64*>(p), reinterpret_cast<uint32_t*>(p + kBins * 8)};
+  p += kHistBytes;
+  u64* cand = reinterpret_cast<u64*>(p);
+  p += kGather * 8;
+  float* res = reinterpret_cast<float*>(p);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = nc > 1 ? cluster_rank() : 0u;
+  const int64_t row = blockIdx.x / nc;
+  const int64_t V = a.V;
+  const int64_t i0 = rank * slice;                       // this CTA's slice: [i0, i1)
+  const int64_t i1 = i0 + slice < V ? i0 + slice : V;
+  const int64_t seg = slice / kW;                        // elements per warp, a multiple of 32
+  auto sync = [nc]() {
+    if (nc > 1) cluster_sync_all();
+    else __syncthreads();
+  };
+  pdl_wait_prior_grid();
+
+  // ---- the row's parameters
+  float T = a.temperature ? a.temperature[row] : 1.0f;
+  int64_t k = a.top_k ? a.top_k[row] : 0;
+  const float top_p = a.top_p ? a.top_p[row] : 1.0f;
+  const float min_p = a.min_p ? a.min_p[row] : 0.0f;
+  const float u = a.u ? a.u[row] : 0.0f;
+  const bool bad = !(T >= 0.0f && T <= 3.402823466e38f) || !(top_p >= 0.0f) || !(min_p >= 0.0f && min_p <= 1.0f) ||
+                   !(u >= 0.0f && u < 1.0f);
+  if (T == 0.0f) {  // greedy: the first token of the order
+    T = 1.0f;
+    k = 1;
+  }
+
+  auto raw = [&](int64_t i) -> float {
+    float v;
+    if constexpr (BF16)
+      v = bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[row * a.ld + i]);
+    else
+      v = static_cast<const float*>(a.logits)[row * a.ld + i];
+    return v == v ? v : -INFINITY;  // NaN never wins
+  };
+  auto value = [&](int64_t i) -> float {
+    if constexpr (RES) return res[i - i0];
+    return raw(i);
+  };
+
+  // ---- pass 1: the slice into shared memory, its largest and smallest finite-or-+inf logit
+  uint32_t hi = 0u, lo = 0xFFFFFFFFu;  // order bits; 0 is below -inf
+  const uint32_t kNegInf = order_bits(-INFINITY);
+  for (int64_t i = i0 + tid; i < i1; i += kT) {
+    const float v = raw(i);
+    if constexpr (RES) res[i - i0] = v;
+    const uint32_t o = order_bits(v);
+    if (o > kNegInf) {
+      hi = o > hi ? o : hi;
+      lo = o < lo ? o : lo;
+    }
+  }
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (lane == 0) {
+    s.wmax[warp] = hi;
+    s.wmin[warp] = lo;
+  }
+  if (tid == 0) s.gathered = 0u;
+  __syncthreads();
+  if (warp == 0) {
+    hi = __reduce_max_sync(0xffffffffu, lane < kW ? s.wmax[lane] : 0u);
+    lo = __reduce_min_sync(0xffffffffu, lane < kW ? s.wmin[lane] : 0xFFFFFFFFu);
+    if (nc == 1) {
+      if (lane == 0) {
+        s.cmax[0] = hi;
+        s.cmin[0] = lo;
+      }
+    }
+  }
+  if (nc > 1) {
+    cluster_sync_all();  // every CTA of the cluster runs: its shared memory may be written
+    if (warp == 0 && lane < nc) {
+      st_peer32(peer(&s.cmax[rank], lane), hi);
+      st_peer32(peer(&s.cmin[rank], lane), lo);
+    }
+  }
+  sync();
+  uint32_t mx = 0u, mn = 0xFFFFFFFFu;
+  for (int r = 0; r < nc; ++r) {
+    mx = s.cmax[r] > mx ? s.cmax[r] : mx;
+    mn = s.cmin[r] < mn ? s.cmin[r] : mn;
+  }
+  auto from_order = [](uint32_t o) { return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o); };
+
+  if (bad || mx == 0u) {  // uniform over the cluster
+    if (bad && tid == 0 && rank == 0) store_status(a.status, MTP_ERR_ARG);
+    if (tid == 0 && rank == 0) {
+      if (a.token) a.token[row] = -1;
+      if (a.prob) a.prob[row] = 0.0f;
+    }
+    if (a.probs)
+      for (int64_t i = i0 + tid; i < i1; i += kT) a.probs[row * V + i] = 0.0f;
+    return;
+  }
+  const float m = from_order(mx);
+  const bool inf = isinf(m);  // then only the infinite logits have weight
+  const double c = 1.4426950408889634074 / static_cast<double>(T);
+  Weigh weigh;
+  weigh.m = m;
+  weigh.ch = static_cast<float>(c);
+  weigh.cl = isinf(weigh.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(weigh.ch));
+  auto counted = [&](float l) { return inf ? l == m : l > -INFINITY; };
+  auto weight = [&](float l) -> float { return counted(l) ? weigh(l) : 0.0f; };
+  auto key64 = [&](float l, int64_t i) -> u64 {
+    return (static_cast<u64>(order_bits(l)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(i));
+  };
+
+  // ---- the cut: tokens with key >= cut are kept
+  u64 cut = 0ull;
+  const bool use_k = k > 0 && k < V, use_p = top_p < 1.0f;
+  if (use_k || use_p) {
+    const float range = inf ? 0.0f : __fsub_rn(m, from_order(mn));
+    float inv = __fdiv_rn(static_cast<float>(kBins), range);
+    if (!(inv <= 3.0e38f)) inv = 0.0f;  // no range, or none that fp32 holds: one bin
+    if (!(range <= 3.0e38f)) inv = 0.0f;
+    auto bin1 = [&](float l) -> int {
+      if (l == m) return 0;
+      const int b = static_cast<int>(__fmul_rn(__fsub_rn(m, l), inv));
+      return b < kBins - 1 ? b : kBins - 1;
+    };
+    // One histogram round over the elements that `in` selects: bins, cluster sum, and for the
+    // limit (entries, or mass) the bin that holds it.
+    auto histogram = [&](auto in, auto bin) {
+      for (int b = tid; b < kBins; b += kT) {
+        loc.mass[b] = 0ull;
+        loc.n[b] = 0u;
+      }
+      __syncthreads();
+      for (int64_t i = i0 + tid; i < i1; i += kT) {
+        const float l = value(i);
+        if (counted(l) && in(l, i)) {
+          const int b = bin(l, i);
+          atomicAdd(&loc.n[b], 1u);
+          if (use_p) {
+            const u64 w = to_fixed(weight(l), frac);
+            if (w) atomicAdd(&loc.mass[b], w);
+          }
+        }
+      }
+      sync();
+      // every CTA sums one section of the bins over the cluster and hands it to all
+      const int per = kBins / nc;
+      for (int b = rank * per + tid; b < static_cast<int>(rank + 1) * per; b += kT) {
+        u64 w = 0ull;
+        uint32_t n = 0u;
+        for (int r = 0; r < nc; ++r) {
+          w += nc > 1 ? ld_peer(peer(&loc.mass[b], r)) : loc.mass[b];
+          n += nc > 1 ? ld_peer32(peer(&loc.n[b], r)) : loc.n[b];
+        }
+        for (int r = 0; r < nc; ++r) {
+          if (nc > 1) {
+            st_peer(peer(&all.mass[b], r), w);
+            st_peer32(peer(&all.n[b], r), n);
+          } else {
+            all.mass[b] = w;
+            all.n[b] = n;
+          }
+        }
+      }
+      sync();
+    };
+    // The first bin at whose end the running count reaches lim_n (by_mass: the running mass reaches
+    // lim_m), given what precedes bin 0. Sets s.hit, s.before_n, s.before_m, s.hit_n.
+    auto find = [&](bool by_mass, u64 lim, uint32_t base_n, u64 base_m) {
+      constexpr int kPer = kBins / kT;
+      u64 w[kPer], wt = 0ull;
+      uint32_t n[kPer], nt = 0u;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        w[j] = all.mass[tid * kPer + j];
+        n[j] = all.n[tid * kPer + j];
+        wt += w[j];
+        nt += n[j];
+      }
+      const u64 wi = warp_inclusive(wt, lane);
+      const u64 ni = warp_inclusive(nt, lane);
+      if (lane == 31) {
+        s.scan[warp] = wi;
+        s.scan_n[warp] = static_cast<uint32_t>(ni);
+      }
+      if (tid == 0) s.hit = -1;
+      __syncthreads();
+      u64 bw = base_m + wi - wt;
+      u64 bn = base_n + ni - nt;
+      for (int q = 0; q < warp; ++q) {
+        bw += s.scan[q];
+        bn += s.scan_n[q];
+      }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const u64 x0 = by_mass ? bw : bn, x1 = by_mass ? bw + w[j] : bn + n[j];
+        if (x0 < lim && x1 >= lim) {
+          s.hit = tid * kPer + j;
+          s.before_n = static_cast<uint32_t>(bn);
+          s.before_m = bw;
+          s.hit_n = n[j];
+        }
+        bw += w[j];
+        bn += n[j];
+      }
+      __syncthreads();
+    };
+    // The cut for a limit: the key of the entry at which the count (the mass) reaches it; returns the
+    // mass up to and with that entry. The histogram of round 1 is in `all`.
+    auto resolve = [&](bool by_mass, u64 lim, u64& cut_out) -> u64 {
+      find(by_mass, lim, 0u, 0ull);
+      const int b1 = s.hit;
+      if (b1 < 0) {  // the limit lies behind the last entry: all are kept
+        cut_out = 0ull;
+        return ~0ull;
+      }
+      u64 prefix = 0ull;  // bits of the key fixed so far (from the top)
+      int bits = 0;
+      uint32_t bn = s.before_n, n = s.hit_n;
+      u64 bm = s.before_m;
+      auto in_now = [&](float l, int64_t i) {
+        return bin1(l) == b1 && (bits == 0 || (key64(l, i) >> (64 - bits)) == prefix);
+      };
+      while (n > kGather && bits < 64) {
+        const int step = bits + 11 <= 64 ? 11 : 64 - bits;
+        const int sh = 64 - bits - step;
+        __syncthreads();
+        // a larger key comes first: bins by the complement of the digit
+        histogram(in_now, [&](float l, int64_t i) {
+          return static_cast<int>((1u << step) - 1u - (static_cast<uint32_t>(key64(l, i) >> sh) & ((1u << step) - 1u)));
+        });
+        find(by_mass, lim, bn, bm);
+        prefix = (prefix << step) | ((1u << step) - 1u - static_cast<uint32_t>(s.hit));
+        bits += step;
+        bn = s.before_n;
+        bm = s.before_m;
+        n = s.hit_n;
+      }
+      // gather the bin's entries at the leader, sort them, find the cut
+      __syncthreads();
+      for (int64_t i = i0 + tid; i < i1; i += kT) {
+        const float l = value(i);
+        if (counted(l) && in_now(l, i)) {
+          if (nc > 1) {
+            const uint32_t at = add_peer32(peer(&s.gathered, 0), 1u);
+            st_peer(peer(&cand[at], 0), key64(l, i));
+          } else {
+            cand[atomicAdd(&s.gathered, 1u)] = key64(l, i);
+          }
+        }
+      }
+      sync();
+      if (rank == 0) {
+        int size = 32;
+        while (size < static_cast<int>(n)) size <<= 1;
+        for (int j = static_cast<int>(n) + tid; j < size; j += kT) cand[j] = 0ull;
+        __syncthreads();
+        for (int w = 2; w <= size; w <<= 1)  // bitonic, descending
+          for (int d = w >> 1; d > 0; d >>= 1) {
+            for (int t = tid; t < size / 2; t += kT) {
+              const int x = 2 * t - (t & (d - 1)), y = x + d;
+              const bool desc = (x & w) == 0;
+              const u64 ka = cand[x], kb = cand[y];
+              if ((ka < kb) == desc) {
+                cand[x] = kb;
+                cand[y] = ka;
+              }
+            }
+            __syncthreads();
+          }
+        // inclusive masses in order, two entries a thread
+        u64 w2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (2 * tid + j < static_cast<int>(n))
+            w2[j] = use_p ? to_fixed(weight(from_order(static_cast<uint32_t>(cand[2 * tid + j] >> 32))), frac) : 0ull;
+        const u64 inc = warp_inclusive(w2[0] + w2[1], lane);
+        if (lane == 31) s.scan[warp] = inc;
+        __syncthreads();
+        u64 before = bm + inc - w2[0] - w2[1];
+        for (int q = 0; q < warp; ++q) before += s.scan[q];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = 2 * tid + j;
+          if (e < static_cast<int>(n)) {
+            const u64 x0 = by_mass ? before : bn + static_cast<u64>(e), x1 = by_mass ? before + w2[j] : x0 + 1ull;
+            if (x0 < lim && x1 >= lim) {
+              s.cut = cand[e];
+              s.cut_mass = before + w2[j];
+            }
+          }
+          before += w2[j];
+        }
+        if (tid == 0) s.gathered = 0u;
+        __syncthreads();
+        if (nc > 1 && tid < nc) {
+          const u64 cv = s.cut, cm = s.cut_mass;
+          if (tid > 0) {
+            st_peer(peer(&s.cut, tid), cv);
+            st_peer(peer(&s.cut_mass, tid), cm);
+          }
+        }
+      }
+      sync();
+      cut_out = s.cut;
+      return s.cut_mass;
+    };
+
+    histogram([](float, int64_t) { return true; }, [&](float l, int64_t) { return bin1(l); });
+    u64 total = 0ull;  // mass of the tokens that top_k keeps
+    bool have_total = false;
+    if (use_k) {
+      total = resolve(false, static_cast<u64>(k), cut);
+      have_total = total != ~0ull;
+    }
+    if (use_p) {
+      if (!have_total) {
+        u64 t = 0ull;
+        __syncthreads();
+        for (int b = tid; b < kBins; b += kT) t += all.mass[b];
+        t = warp_sum(t);
+        if (lane == 0) s.scan[warp] = t;
+        __syncthreads();
+        total = 0ull;
+        for (int q = 0; q < kW; ++q) total += s.scan[q];
+        __syncthreads();
+      }
+      // kept: preceding mass < top_p * total, so the cut is where the running mass reaches it
+      u64 lim = scale_ceil(top_p, total);
+      if (lim == 0ull) lim = 1ull;  // the first token is always kept
+      u64 cut_p = 0ull;
+      if (use_k && have_total) {
+        // the histogram of round 1 may have been overwritten by the refinement
+        histogram([](float, int64_t) { return true; }, [&](float l, int64_t) { return bin1(l); });
+      }
+      (void)resolve(true, lim, cut_p);
+      cut = cut_p > cut ? cut_p : cut;
+    }
+  }
+  // min_p as a bound on the logit: the smallest float not below m + T ln(min_p)
+  float bound = -INFINITY;
+  if (min_p > 0.0f) {
+    const double t = static_cast<double>(m) + (min_p < 1.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0);
+    bound = static_cast<float>(t);
+    if (static_cast<double>(bound) < t) bound = nextafterf(bound, INFINITY);
+  }
+  auto kept = [&](float l, int64_t i) { return l >= bound && counted(l) && key64(l, i) >= cut; };
+
+  // ---- masses of the kept tokens per warp segment, CTA and row
+  u64 sum = 0ull;
+  for (int64_t j = i0 + warp * seg + lane; j < i0 + (warp + 1) * seg; j += 32)
+    if (j < i1) {
+      const float l = value(j);
+      if (kept(l, j)) sum += to_fixed(weight(l), frac);
+    }
+  sum = warp_sum(sum);
+  if (lane == 0) s.wsum[warp] = sum;
+  __syncthreads();
+  u64 mine = 0ull;
+  for (int q = 0; q < kW; ++q) mine += s.wsum[q];
+  if (tid < nc) {
+    if (nc > 1) st_peer(peer(&s.cta[rank], tid), mine);
+    else s.cta[0] = mine;
+  }
+  sync();  // the last exchange: after it every CTA reads its own shared memory only
+  u64 z = 0ull;
+  for (int r = 0; r < nc; ++r) z += s.cta[r];
+  const float inv_z = static_cast<float>(exp2(static_cast<double>(frac)) / static_cast<double>(z));
+  if (a.token || a.prob)
+    locate(s, rank, scale_floor(u, z), i0, seg, i1,
+           [&](int64_t i) {
+             const float l = value(i);
+             return kept(l, i) ? to_fixed(weight(l), frac) : 0ull;
+           },
+           [&](int64_t i) {
+             if (a.token) a.token[row] = static_cast<int32_t>(i);
+             if (a.prob) a.prob[row] = __fmul_rn(weight(value(i)), inv_z);
+           });
+  if (a.probs)
+    for (int64_t i = i0 + tid; i < i1; i += kT) {
+      const float l = value(i);
+      a.probs[row * V + i] = kept(l, i) ? __fmul_rn(weight(l), inv_z) : 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------------------- acceptance
+// Drafts x_0 .. x_{n-1} of a sequence against the target's distributions p_0 .. p_n and the drafter's
+// q_0 .. q_{n-1}: draft i is accepted while u_i q_i(x_i) < p_i(x_i) (probability min(1, p / q)); the
+// token after the a accepted ones comes from max(p_a - q_a, 0), or from p_n when all are accepted,
+// by inversion with u_D. Emitted tokens are then distributed as the target's. Bound by the read of
+// one row of p and one of q per sequence.
+__global__ void __launch_bounds__(kT, 1) verify_kernel(const VerifyArgs a, int nc, int64_t slice, int frac) {
+  __shared__ Shared s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = nc > 1 ? cluster_rank() : 0u;
+  const int64_t b = blockIdx.x / nc;
+  const int64_t V = a.V, D = a.D;
+  const int64_t i0 = rank * slice, i1 = i0 + slice < V ? i0 + slice : V, seg = slice / kW;
+  pdl_wait_prior_grid();
+  int n = a.draft_len ? a.draft_len[b] : a.D;
+  const float ud = a.u[b * (D + 1) + D];
+  auto unit = [](float u) { return u >= 0.0f && u < 1.0f; };
+  // a sequence with a bad length or random number is refused as a whole (every warp decides for
+  // itself, alike; the return is uniform over the cluster)
+  bool bad = n < 0 || n > a.D || !unit(ud);
+  for (int i = lane; !bad && i < n; i += 32) bad = !unit(a.u[b * (D + 1) + i]);
+  if (__any_sync(0xffffffffu, bad)) {
+    if (rank == 0) {
+      for (int i = tid; i <= a.D; i += kT) a.tokens[b * (D + 1) + i] = -1;
+      if (tid == 0) {
+        a.accepted[b] = 0;
+        if (a.prob) a.prob[b] = 0.0f;
+        store_status(a.status, MTP_ERR_ARG);
+      }
+    }
+    return;
+  }
+  // the acceptance, 32 drafts at a time; a draft outside [0, V) is rejected
+  int acc = 0, rejected_token = -1;
+  bool outside = false;
+  while (acc < n) {
+    const int i = acc + lane;
+    bool ok = false;
+    int32_t x = -1;
+    if (i < n) {
+      x = a.draft_tokens[b * D + i];
+      if (x >= 0 && x < V) {
+        const double u = a.u[b * (D + 1) + i];
+        const double p = a.target_probs[(b * (D + 1) + i) * V + x];
+        const double q = a.draft_probs ? a.draft_probs[(b * D + i) * V + x] : 1.0f;
+        ok = u * q < p;  // the product is exact in fp64
+      }
+    }
+    const uint32_t no = __ballot_sync(0xffffffffu, !ok);
+    const int run = no ? __ffs(no) - 1 : 32;
+    const int left = n - acc;
+    if (run < left && run < 32) {
+      rejected_token = __shfl_sync(0xffffffffu, x, run);
+      outside = rejected_token < 0 || rejected_token >= V;
+      acc += run;
+      break;
+    }
+    acc += run < left ? run : left;
+  }
+  const bool all = acc == n;
+  const float* p = a.target_probs + (b * (D + 1) + acc) * V;
+  const float* q = !all && a.draft_probs ? a.draft_probs + (b * D + acc) * V : nullptr;
+  auto prob01 = [](float v) { return v > 0.0f ? (v < 1.0f ? v : 1.0f) : 0.0f; };
+  bool plain = false;  // the residual is empty: the target's own row
+  auto residual = [&](int64_t i) -> float {
+    const float pv = prob01(p[i]);
+    if (plain || all) return pv;
+    const float qv = q ? q[i] : (i == rejected_token ? 1.0f : 0.0f);
+    return prob01(__fsub_rn(pv, prob01(qv)));
+  };
+  u64 z = 0ull;
+  for (int pass = 0; pass < 2; ++pass) {
+    u64 sum = 0ull;
+    for (int64_t j = i0 + warp * seg + lane; j < i0 + (warp + 1) * seg; j += 32)
+      if (j < i1) sum += to_fixed(residual(j), frac);
+    sum = warp_sum(sum);
+    if (lane == 0) s.wsum[warp] = sum;
+    __syncthreads();
+    u64 mine = 0ull;
+    for (int w = 0; w < kW; ++w) mine += s.wsum[w];
+    if (nc > 1) cluster_sync_all();  // the peers run, and have read the previous pass's masses
+    if (tid < nc) {
+      if (nc > 1) st_peer(peer(&s.cta[rank], tid), mine);
+      else s.cta[0] = mine;
+    }
+    if (nc > 1) cluster_sync_all();
+    else __syncthreads();
+    z = 0ull;
+    for (int r = 0; r < nc; ++r) z += s.cta[r];
+    if (z != 0ull || all || plain) break;
+    plain = true;
+  }
+  if (rank == 0) {
+    for (int i = tid; i <= a.D; i += kT)
+      if (i != acc) a.tokens[b * (D + 1) + i] = i < acc ? a.draft_tokens[b * D + i] : -1;
+    if (tid == 0) {
+      a.accepted[b] = acc;
+      if (outside) store_status(a.status, MTP_ERR_TOKEN_RANGE);
+      if (z == 0ull) {
+        a.tokens[b * (D + 1) + acc] = -1;
+        if (a.prob) a.prob[b] = 0.0f;
+      }
+    }
+  }
+  if (z != 0ull)
+    locate(s, rank, scale_floor(ud, z), i0, seg, i1,
+           [&](int64_t i) { return to_fixed(residual(i), frac); },
+           [&](int64_t i) {
+             a.tokens[b * (D + 1) + acc] = static_cast<int32_t>(i);
+             if (a.prob)
+               a.prob[b] = static_cast<float>(static_cast<double>(residual(i)) * exp2(static_cast<double>(frac)) /
+                                              static_cast<double>(z));
+           });
+}
+
+// ------------------------------------------------------------------------------- host side
+cudaError_t launch_cluster(const void* kernel, unsigned grid, int nc, size_t smem, cudaStream_t stream, void** args) {
+  static std::mutex mu;
+  static bool done[64][8] = {};
+  static const void* kernels[8] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    int slot = 0;
+    while (kernels[slot] != nullptr && kernels[slot] != kernel) ++slot;
+    kernels[slot] = kernel;
+    if (!done[dev][slot]) {
+      DeviceInfo di;
+      err = device_info(&di);
+      if (err != cudaSuccess) return err;
+      err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin);
+      if (err != cudaSuccess) return err;
+      err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (err != cudaSuccess) return err;
+      done[dev][slot] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(nc);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = nc > 1 ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+int64_t slice_of(int64_t V, int nc) { return ((V + nc - 1) / nc + kSliceUnit - 1) / kSliceUnit * kSliceUnit; }
+
+// Fraction bits of a mass: V weights of at most one stay below 2^62 (plus their roundings).
+int mass_bits(int64_t V) {
+  int lg = 0;
+  while ((static_cast<int64_t>(1) << lg) < V) ++lg;
+  return 62 - lg;
+}
+
+// CTAs per row: as many as keep every SM busy (up to kMaxC), and no more than give each warp a step.
+int cluster_size(int64_t rows, int64_t V, int sm_count) {
+  int nc = 1;
+  while (nc < kMaxC && rows * nc * 2 <= sm_count && V > static_cast<int64_t>(nc) * 2 * kSliceUnit) nc *= 2;
+  return nc;
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleArgs& in, cudaStream_t stream) {
+  DeviceInfo di;
+  cudaError_t err = device_info(&di);
+  if (err != cudaSuccess) return err;
+  SampleArgs a = in;
+  int nc = cluster_size(a.R, a.V, di.sm_count);
+  const size_t room = static_cast<size_t>(di.smem_optin) - kFixedSmem;
+  while (nc < kMaxC && static_cast<size_t>(slice_of(a.V, nc)) * 4 > room) nc *= 2;
+  int64_t slice = slice_of(a.V, nc);
+  const bool res = static_cast<size_t>(slice) * 4 <= room;
+  int frac = mass_bits(a.V);
+  const void* kern = a.bf16 ? (res ? reinterpret_cast<const void*>(sample_kernel<true, true>)
+                                   : reinterpret_cast<const void*>(sample_kernel<true, false>))
+                            : (res ? reinterpret_cast<const void*>(sample_kernel<false, true>)
+                                   : reinterpret_cast<const void*>(sample_kernel<false, false>));
+  void* args[] = {&a, &nc, &slice, &frac};
+  return launch_cluster(kern, static_cast<unsigned>(a.R) * nc, nc,
+                        kFixedSmem + (res ? static_cast<size_t>(slice) * 4 : 0), stream, args);
+}
+
+cudaError_t launch_verify(const VerifyArgs& in, cudaStream_t stream) {
+  DeviceInfo di;
+  cudaError_t err = device_info(&di);
+  if (err != cudaSuccess) return err;
+  VerifyArgs a = in;
+  int nc = cluster_size(a.B, a.V, di.sm_count);
+  int64_t slice = slice_of(a.V, nc);
+  int frac = mass_bits(a.V);
+  void* args[] = {&a, &nc, &slice, &frac};
+  return launch_cluster(reinterpret_cast<const void*>(verify_kernel), static_cast<unsigned>(a.B) * nc, nc, 0, stream,
+                        args);
+}
+
+}  // namespace mtp

@@ -32,6 +32,10 @@ class MtpDraftHead:
         self.max_batch = max_batch
         self.lm_head_fp8 = None
         self.row_scale = None
+        self.lm_head_fp4 = None
+        self.eh_proj_fp4 = None
+        self.ws_fp4 = None
+        self.ws_fp4_in = None
         self.ws = _lib.workspace(max_batch, self.H, self.V, self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
@@ -50,6 +54,31 @@ class MtpDraftHead:
             self.lm_head_fp8, self.row_scale = None, None
         return code
 
+    # ------------------------------------------------------------------ FP4 copies
+    def quantize_fp4(self) -> int:
+        """Build the FP4 copies of lm_head and eh_proj, (q, block_scale, row_scale) each; returns the
+        device status (0, or MTP_ERR_NONFINITE when a weight is NaN/Inf -- both are then dropped).
+        eh_proj gets a copy when H is a multiple of 8 (the input stage then runs over it)."""
+        st = torch.zeros(1, dtype=torch.int32, device=self.device)
+        lm = _lib.fp4_empty(self.V, self.H, self.device)
+        _lib.mtp_head_quantize_fp4(self.lm_head, *lm, st)
+        eh = None
+        if self.H % 8 == 0:
+            eh = _lib.fp4_empty(self.H, 2 * self.H, self.device)
+            _lib.mtp_head_quantize_fp4(self.eh_proj, *eh, st)
+        code = int(st.item())
+        self.lm_head_fp4, self.eh_proj_fp4 = (lm, eh) if code == 0 else (None, None)
+        if code == 0 and self.ws_fp4 is None:
+            self.ws_fp4 = _lib.fp4_workspace(self.max_batch, self.H, self.V, self.device)
+            if eh is not None:
+                self.ws_fp4_in = _lib.context_fp4_workspace(self.max_batch, self.H, self.device)
+        return code
+
+    def _fp4(self):
+        if self.lm_head_fp4 is None:
+            raise RuntimeError("no FP4 copy: call quantize_fp4() first")
+        return self.lm_head_fp4
+
     def _head(self, fp8: bool):
         if fp8:
             if self.lm_head_fp8 is None:
@@ -58,29 +87,45 @@ class MtpDraftHead:
         return self.lm_head, None, W_BF16
 
     # ------------------------------------------------------------------ stages
-    def input(self, tokens, hidden, x=None, status=None, stream=None):
+    def input(self, tokens, hidden, x=None, status=None, stream=None, fp4: bool = False):
         B = tokens.numel()
         x = torch.empty((B, self.H), dtype=torch.bfloat16, device=self.device) if x is None else x
+        if fp4:
+            self._fp4()
+            if self.eh_proj_fp4 is not None:
+                _lib.mtp_head_context_rows_fp4(self.embed, self.enorm_w, self.hnorm_w, *self.eh_proj_fp4, tokens,
+                                               hidden, x, self.ws_fp4_in, status, self.eps, stream)
+                return x
         _lib.mtp_head_input_batched(self.embed, self.enorm_w, self.hnorm_w, self.eh_proj, tokens,
                                     hidden, x, status, self.eps, stream)
         return x
 
-    def logits_argmax(self, x, fp8: bool = False, logits=True, draft=None, status=None, stream=None):
+    def logits_argmax(self, x, fp8: bool = False, logits=True, draft=None, status=None, stream=None,
+                      fp4: bool = False):
         B = x.shape[0]
-        W, s, wt = self._head(fp8)
+        if fp8 and fp4:
+            raise ValueError("fp8 and fp4 exclude each other")
+        W, s, wt = (None, None, None) if fp4 else self._head(fp8)
         if logits is True:
             logits = torch.empty((B, self.V), dtype=torch.float32, device=self.device)
         elif logits is False:
             logits = None
         draft = torch.empty(B, dtype=torch.int32, device=self.device) if draft is None else draft
+        if fp4:
+            _lib.mtp_head_logits_argmax_fp4(x, self.final_norm_w, *self._fp4(), logits, draft, self.ws_fp4, status,
+                                            self.eps, stream)
+            return logits, draft
         _lib.mtp_head_logits_argmax_batched(x, self.final_norm_w, W, s, wt, logits, draft, self.ws,
                                             status, self.eps, stream)
         return logits, draft
 
     def forward(self, tokens, hidden, fp8: bool = False, logits=False, x=None, draft=None,
-                status=None, stream=None):
+                status=None, stream=None, fp4: bool = False):
         """One draft step for B sequences (device buffers): returns (x, logits|None, draft)."""
         B = tokens.numel()
+        if fp4:
+            x = self.input(tokens, hidden, x, status, stream, fp4=True)
+            return (x, *self.logits_argmax(x, fp8, logits, draft, status, stream, fp4=True))
         W, s, wt = self._head(fp8)
         x = torch.empty((B, self.H), dtype=torch.bfloat16, device=self.device) if x is None else x
         if logits is True:
@@ -104,6 +149,28 @@ class MtpDraftHead:
                              torch.empty((B, self.H), dtype=torch.bfloat16, device=dev),
                              torch.empty((B, self.H), dtype=torch.bfloat16, device=dev),
                              torch.empty(B, dtype=torch.int32, device=dev), self.ws, status, self.eps, stream)
+
+    # ------------------------------------------------------------------ sampling and acceptance
+    def sample(self, logits, u, temperature=None, top_k=None, top_p=None, min_p=None, probs: bool = True,
+               status=None, stream=None):
+        """One token per row of logits from the uniform numbers u, as mtp_head_sample: returns
+        (token, prob, probs|None). probs is what ``verify`` takes, as the drafter's or the target's."""
+        R, V = logits.shape
+        token = torch.empty(R, dtype=torch.int32, device=logits.device)
+        prob = torch.empty(R, dtype=torch.float32, device=logits.device)
+        dist = torch.empty((R, V), dtype=torch.float32, device=logits.device) if probs else None
+        _lib.mtp_head_sample(logits, u, token, prob, dist, temperature, top_k, top_p, min_p, status, stream)
+        return token, prob, dist
+
+    def verify(self, target_probs, draft_probs, draft_tokens, u, draft_len=None, status=None, stream=None):
+        """Drafts [B, D] against the target's distributions [B, D + 1, V], as mtp_head_verify
+        (draft_probs None for greedy drafts): returns (tokens [B, D + 1], accepted [B])."""
+        B, D = draft_tokens.shape
+        tokens = torch.empty((B, D + 1), dtype=torch.int32, device=target_probs.device)
+        accepted = torch.empty(B, dtype=torch.int32, device=target_probs.device)
+        _lib.mtp_head_verify(target_probs, draft_probs, draft_tokens, u, tokens, accepted, None, draft_len, status,
+                             stream)
+        return tokens, accepted
 
     # ------------------------------------------------------------------ draft chains
     def chain(self, first_tokens, hiddens, fp8: bool = False, graph: bool = True, status=None):
