@@ -27,8 +27,11 @@ struct Fp4Matrix {
 };
 
 // w [rows, k] BF16 (row stride k) -> q, bs, rs. Rows whose valid flag (optional) is 0 become zeros.
+// tile = 0: bs in the layout of a copy. tile > 0: in the order of the linear's operand, for tiles of
+// `tile` rows -- per tile, per 128 rows of it (the last one may be partial), per 64 columns, 512
+// bytes: scale i (0..3) of row r + 32 j (r < 32, j < 4) at 16 r + 4 j + i.
 cudaError_t launch_fp4_quantize(const uint16_t* w, uint8_t* q, uint8_t* bs, float* rs, int32_t* status,
-                                const int32_t* valid, int rows, int k, cudaStream_t stream);
+                                const int32_t* valid, int rows, int k, cudaStream_t stream, int tile = 0);
 cudaError_t launch_fp4_dequantize(const Fp4Matrix& m, uint16_t* w, int rows, int k, cudaStream_t stream);
 
 struct Fp4SweepArgs {

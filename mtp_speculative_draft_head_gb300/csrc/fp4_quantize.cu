@@ -138,7 +138,7 @@ template <int TPR, bool VEC>
 __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t* __restrict__ w, uint8_t* __restrict__ q,
                                                                  uint8_t* __restrict__ bs, float* __restrict__ rs_out,
                                                                  int32_t* __restrict__ status,
-                                                                 const int32_t* __restrict__ valid, int rows, int k) {
+                                                                 const int32_t* __restrict__ valid, int rows, int k, int tile) {
   __shared__ uint32_t red[kQThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = threadIdx.x % TPR;
@@ -175,6 +175,12 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t*
     const float r6_up = __fmul_rn(r6, kUp), r6_dn = __fmul_rn(r6, kDn);
     uint8_t* qr = q + row * (kp / 2);
     uint8_t* br = bs + row * nblk;
+    if (tile > 0) { // the first scale byte of this row in the linear's order (fp4.h)
+      const int64_t tl = row / tile;
+      const int lr = static_cast<int>(row - tl * tile);
+      const int64_t chunk = tl * ((tile + 127) / 128) + lr / 128;
+      br = bs + chunk * (kp / 64) * 512 + (lr & 31) * 16 + ((lr & 127) >> 5) * 4;
+    }
     for (int b = t; b < nblk; b += TPR) {
       uint32_t c0 = 0u, c1 = 0u, sc = 0u;
       if (rs > 0.0f && b * kFp4Block < k) {
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t*
         }
       }
       reinterpret_cast<uint2*>(qr)[b] = make_uint2(c0, c1);
-      br[b] = static_cast<uint8_t>(sc);
+      br[tile > 0 ? (b >> 2) * 512 + (b & 3) : b] = static_cast<uint8_t>(sc);
     }
   }
   pdl_launch_dependents();
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const Fp4Matr
 }  // namespace
 
 cudaError_t launch_fp4_quantize(const uint16_t* w, uint8_t* q, uint8_t* bs, float* rs, int32_t* status,
-                                const int32_t* valid, int rows, int k, cudaStream_t stream) {
+                                const int32_t* valid, int rows, int k, cudaStream_t stream, int tile) {
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
@@ -255,7 +261,7 @@ cudaError_t launch_fp4_quantize(const uint16_t* w, uint8_t* q, uint8_t* bs, floa
   const int per_block = wide ? 1 : kQThreads / 32;
   int64_t blocks = (static_cast<int64_t>(rows) + per_block - 1) / per_block;
   if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
-  void* args[] = {&w, &q, &bs, &rs, &status, &valid, &rows, &k};
+  void* args[] = {&w, &q, &bs, &rs, &status, &valid, &rows, &k, &tile};
   return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0, stream, args);
 }
 

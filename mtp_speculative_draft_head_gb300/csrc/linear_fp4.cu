@@ -1,80 +1,528 @@
 // Rows of activations times an FP4 weight matrix, both in four bits:
 //   y[r, n] = bf16( rs_x[r] rs_w[n] sum_k (s_x code_x)[r, k] (s_w code_w)[n, k] )
-// The rows of x are quantised on the way (fp4_quantize.cu) into the workspace.
+//
+// Kernels:
+//  1. the rows of x are quantised (fp4_quantize.cu) into the workspace, their block scales already
+//     in the order in which tensor memory wants them;
+//  2. linear_fp4_kernel: the product on the fifth-generation tensor cores with the block scales
+//     applied by the MMA itself (tcgen05.mma kind::mxf4nvf4, one E4M3 scale per 16 codes of either
+//     operand, fp32 accumulation); the row scales multiply in the epilogue.
+//
+// The weights are the MMA's M operand (128 rows a tile) and the activation rows its N operand (16 to
+// 224 a tile): one row of activations costs an eighth of a 128-row tile instead of filling one, so
+// the same kernel serves a draft step's few sequences, bound by the read of the weights, and a
+// prompt's thousands of rows, bound by the tensor cores. Codes arrive by 2-D TMA (256 codes = 128
+// bytes a row and stage, 128-byte swizzle). The weights' scales are rows of 16 bytes a stage in the
+// copy's plain layout; one warp loads them and stores the four words of a row into the four
+// 32 x 16-byte blocks that tcgen05.cp spreads over tensor memory (the scales of rows r, r + 32,
+// r + 64, r + 96 side by side). The activations' scales are written in that order by the quantiser
+// and come by one bulk copy a stage.
+//
+// Schedules. Many rows: a persistent grid, one CTA per SM, two accumulators in tensor memory, so a
+// tile's epilogue runs under the next tile's MMAs. Few rows (less than a wave of tiles): the k range
+// is split over a cluster of 2 to 8 CTAs, whose fp32 partial sums meet in the first CTA's shared
+// memory and are added in k order.
+//
+// Warp roles: 0 TMA producer, 1 tensor-memory allocation and MMA issue, 2 weight scales, 4..7
+// epilogue (warp w reads TMEM lanes 32 (w % 4) ..). Every wait is bounded, as in context.cu.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "common.cuh"
-#include "fp4_dot.cuh"
+#include "fp4.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace mtp {
 
 namespace {
 
+constexpr int kLM = 128;          // weight rows per tile
+constexpr int kLK = 256;          // codes per stage: four MMAs of 64
+constexpr int kLThreads = 256;
+constexpr int kABytes = kLM * kLK / 2;       // 16 KB of weight codes per stage
+constexpr int kSfChunk = 4 * 512;            // scales of 128 rows x 256 codes: four 512-byte blocks
+constexpr int kMaxSplits = 8;
+constexpr uint32_t kTmemCols = 512;
+
+template <int NT>
+struct LTile {
+  static constexpr int kChunks = (NT + 127) / 128;             // 128-row scale blocks of the activations
+  static constexpr int kBBytes = NT * kLK / 2;
+  static constexpr int kStageBytes = kABytes + kBBytes + kSfChunk * (1 + kChunks);
+  static constexpr int kFit = (200 * 1024) / kStageBytes;
+  static constexpr int kStages = kFit < 9 ? kFit : 9;
+  static constexpr uint32_t kSfaCol = 2 * NT;                  // after the two accumulators
+  static constexpr uint32_t kSfbCol = kSfaCol + 16;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 4) * 8 + 16;
+  static_assert(NT % 16 == 0 && NT <= 256, "N of an M = 128 MMA");
+  static_assert(kSfbCol + 16 * kChunks <= kTmemCols, "tensor memory");
+};
+
+struct LinearSched {
+  int nt;       // activation rows per tile
+  int mt;       // weight tiles
+  int tiles;    // all tiles; tile t: weight tile t % mt, activation tile t / mt
+  int nkb;      // stages per tile
+  int splits;   // CTAs per tile (a cluster along k); 1: persistent
+};
+
+struct LinearParams {
+  const uint8_t* w_bs;   // [N, kp / 16]
+  const float* w_rs;     // [N]
+  const uint8_t* x_sf;   // workspace: [tiles of nt][chunks][kp / 64][512]
+  const float* x_rs;     // workspace: [R]
+  uint16_t* y;           // [R, N]
+  int32_t* status;
+  int R, N, kp;
+};
+
+// ------------------------------------------------------------------------------- PTX
+// Instruction descriptor, kind::mxf4nvf4: E2M1 A and B, both K-major, E4M3 scales, M x N, K = 64.
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// 32 rows of 16 bytes (512 contiguous bytes of shared memory) to four TMEM columns, repeated in all
+// four 32-lane quarters.
+__device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint32_t smem) {
+  // no swizzle, groups of eight 16-byte rows 128 bytes apart, descriptor version 1
+  const uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+                     (static_cast<uint64_t>(1) << 46);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------------------------- kernel
+template <int NT, bool SPLIT>
+__global__ void __launch_bounds__(kLThreads, 1)
+    linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                      const LinearParams p, const LinearSched c) {
+  using TL = LTile<NT>;
+  constexpr int kStages = TL::kStages, kChunks = TL::kChunks;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * TL::kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;     // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // this CTA's tiles t0, t0 + step, ... and its stages kb0 .. kb0 + nkb of each
+  const uint32_t rank = SPLIT ? cta_rank() : 0u;
+  const int t0 = SPLIT ? static_cast<int>(blockIdx.x) / c.splits : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? c.tiles : static_cast<int>(gridDim.x);
+  const int kb0 = SPLIT ? static_cast<int>(rank) * c.nkb / c.splits : 0;
+  const int nkb = (SPLIT ? (static_cast<int>(rank) + 1) * c.nkb / c.splits : c.nkb) - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&full[i]), 2);  // the producer and the scale warp
+      mbar_init(smem_addr(&empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&acc_full[i]), 1);
+      mbar_init(smem_addr(&acc_empty[i]), 4);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmemCols);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  auto aborted = [&] { return *reinterpret_cast<volatile int*>(&abort_flag) != 0; };
+  auto give_up = [&] {
+    store_status(p.status, MTP_ERR_TIMEOUT);
+    atomicExch(&abort_flag, 1);
+  };
+
+  // The epilogue's row scales of a tile's activation rows: lane l holds those of rows l, l + 32, ...
+  // (loaded before the accumulator is waited for; read one by one between the stores, each cost the
+  // epilogue an L2 round trip: 44 us a tile).
+  constexpr int kRx = (NT + 31) / 32;
+  auto load_rx = [&](float (&rx)[kRx], int r0) {
+#pragma unroll
+    for (int j = 0; j < kRx; ++j) rx[j] = r0 + 32 * j + lane < p.R ? __ldcg(p.x_rs + r0 + 32 * j + lane) : 0.0f;
+  };
+  auto store_y = [&](int r0, int col, int row, float v, float rw, const float (&rx)[kRx]) {
+    const float s = __shfl_sync(0xffffffffu, rx[col >> 5], col & 31);
+    if (r0 + col < p.R && row < p.N)
+      p.y[static_cast<size_t>(r0 + col) * p.N + row] = static_cast<uint16_t>(bf16_bits_rn(__fmul_rn(__fmul_rn(v, rw), s)));
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      uint64_t pol_w, pol_x;
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol_w));
+      asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
+      const int ntiles = t0 < c.tiles ? (c.tiles - t0 + step - 1) / step : 0;
+      const int total = ntiles * nkb;
+      auto load_w = [&](int i) {
+        const int t = t0 + (i / nkb) * step, kb = kb0 + i % nkb;
+        const uint32_t bar = smem_addr(&full[i % kStages]);
+        mbar_arrive_expect_tx(bar, kABytes + TL::kBBytes + kSfChunk * kChunks);
+        tma_load_2d(smem_addr(smem + (i % kStages) * TL::kStageBytes), &tm_w, kb * (kLK / 2), (t % c.mt) * kLM, bar, pol_w);
+      };
+      auto load_x = [&](int i) {
+        const int t = t0 + (i / nkb) * step, kb = kb0 + i % nkb, xt = t / c.mt;
+        const uint32_t bar = smem_addr(&full[i % kStages]);
+        const uint32_t st = smem_addr(smem + (i % kStages) * TL::kStageBytes);
+        tma_load_2d(st + kABytes, &tm_x, kb * (kLK / 2), xt * NT, bar, pol_x);
+        for (int ch = 0; ch < kChunks; ++ch)
+          bulk_copy_g2s(st + kABytes + TL::kBBytes + kSfChunk * (1 + ch),
+                        p.x_sf + ((static_cast<size_t>(xt) * kChunks + ch) * (p.kp / 64) + kb * 4) * 512, kSfChunk, bar,
+                        pol_x);
+      };
+      // the weights do not depend on the kernel before (the quantiser): the first stages' weight
+      // codes are in flight before the wait for it
+      const int pre = total < kStages ? total : kStages;
+      for (int i = 0; i < pre; ++i) load_w(i);
+      pdl_wait_prior_grid();
+      for (int i = 0; i < pre; ++i) load_x(i);
+      int issued = pre;
+      for (int i = pre; i < total; ++i) {
+        if (aborted() || !mbar_wait_bounded(smem_addr(&empty[i % kStages]), static_cast<uint32_t>((i / kStages - 1) & 1))) {
+          give_up();
+          break;
+        }
+        load_w(i);
+        load_x(i);
+        ++issued;
+      }
+      // every copy issued must land before the CTA's shared memory goes away (normally the MMA thread
+      // has seen them all; after a timeout the scale warp's arrival may be missing, and the wait ends
+      // by its limit)
+      for (int i = issued - kStages < 0 ? 0 : issued - kStages; i < issued; ++i)
+        (void)mbar_wait_bounded(smem_addr(&full[i % kStages]), static_cast<uint32_t>((i / kStages) & 1));
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_fp4(kLM, NT);
+      int i = 0, n = 0;
+      bool ok = true;
+      for (int t = t0; t < c.tiles && ok; t += step, ++n) {
+        const int buf = n & 1;
+        // this accumulator's previous tile must have left tensor memory
+        if (n >= 2 && !mbar_wait_bounded(smem_addr(&acc_empty[buf]), static_cast<uint32_t>((n / 2 - 1) & 1))) {
+          give_up();
+          ok = false;
+        }
+        tmem_fence_after_sync();
+        for (int kb = 0; kb < nkb && ok; ++kb, ++i) {
+          const int s = i % kStages;
+          if (aborted() || !mbar_wait_bounded(smem_addr(&full[s]), static_cast<uint32_t>((i / kStages) & 1))) {
+            give_up();
+            ok = false;
+            break;
+          }
+          tmem_fence_after_sync();
+          const uint32_t st = smem_addr(smem + s * TL::kStageBytes);
+          const uint32_t sf = st + kABytes + TL::kBBytes;
+          const uint64_t da = umma_desc_sw128(st), db = umma_desc_sw128(st + kABytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // 64 codes = 32 bytes along the swizzle row
+            const uint32_t sfa = tmem + TL::kSfaCol + 4 * k, sfb = tmem + TL::kSfbCol + 4 * kChunks * k;
+            tmem_copy_sf(sfa, sf + 512 * k);
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) tmem_copy_sf(sfb + 4 * ch, sf + kSfChunk * (1 + ch) + 512 * k);
+            umma_fp4(tmem + static_cast<uint32_t>(buf * NT), da + 2 * k, db + 2 * k, idesc, sfa, sfb, (kb | k) != 0 ? 1u : 0u);
+          }
+          umma_commit(smem_addr(&empty[s]));  // the stage is free once these have read it
+        }
+        umma_commit(smem_addr(&acc_full[buf]));
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ weight scales
+    // Lane r holds the 16 scale bytes of rows r, r + 32, r + 64, r + 96 of the tile for one stage:
+    // word k of a row belongs to MMA k. Loads run kAhead stages ahead of the stores.
+    constexpr int kAhead = 3;
+    const int ntiles = t0 < c.tiles ? (c.tiles - t0 + step - 1) / step : 0;
+    const int total = ntiles * nkb;
+    uint4 v[kAhead][4];
+    auto fetch = [&](int i, uint4 (&d)[4]) {
+      const int t = t0 + (i / nkb) * step, kb = kb0 + i % nkb;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = (t % c.mt) * kLM + 32 * j + lane;
+        d[j] = i < total && row < p.N
+                   ? __ldg(reinterpret_cast<const uint4*>(p.w_bs + static_cast<size_t>(row) * (p.kp / 16)) + kb)
+                   : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) fetch(a, v[a]);
+    bool ok = true;
+    for (int i0 = 0; i0 < total && ok; i0 += kAhead) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int i = i0 + a;
+        if (i < total && ok) {
+          if (i >= kStages &&
+              (aborted() || !__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[i % kStages]),
+                                                                       static_cast<uint32_t>((i / kStages - 1) & 1))))) {
+            ok = false;
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(smem + (i % kStages) * TL::kStageBytes + kABytes + TL::kBBytes) + lane;
+            dst[0] = make_uint4(v[a][0].x, v[a][1].x, v[a][2].x, v[a][3].x);
+            dst[32] = make_uint4(v[a][0].y, v[a][1].y, v[a][2].y, v[a][3].y);
+            dst[64] = make_uint4(v[a][0].z, v[a][1].z, v[a][2].z, v[a][3].z);
+            dst[96] = make_uint4(v[a][0].w, v[a][1].w, v[a][2].w, v[a][3].w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&full[i % kStages]));
+            fetch(i + kAhead, v[a]);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up();
+    __syncwarp();
+  } else if (warp >= 4 && !SPLIT) {
+    // ------------------------------------------------------------------ epilogue
+    const int q = warp & 3;
+    pdl_wait_prior_grid();  // x_rs comes from the quantiser
+    int n = 0;
+    for (int t = t0; t < c.tiles; t += step, ++n) {
+      const int buf = n & 1;
+      const int row = (t % c.mt) * kLM + 32 * q + lane, r0 = (t / c.mt) * NT;
+      const float rw = row < p.N ? __ldg(p.w_rs + row) : 0.0f;
+      float rx[kRx];
+      load_rx(rx, r0);
+      const bool done = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_full[buf]), static_cast<uint32_t>((n / 2) & 1)));
+      tmem_fence_after_sync();
+      if (!done || aborted()) {
+        if (lane == 0) give_up();
+        break;
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < NT; c0 += 16) {
+        if (r0 + c0 < p.R) {
+          uint32_t v[16];
+          tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf * NT + c0), v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) store_y(r0, c0 + e, row, __uint_as_float(v[e]), rw, rx);
+        }
+      }
+      tmem_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&acc_empty[buf]));
+    }
+  }
+
+  if constexpr (SPLIT) {
+    // ------------------------------------------------------------------ joining the k ranges
+    // The MMAs of every CTA of the cluster are done after the first barrier, so the first CTA's ring
+    // is free for the others' partial sums: slot (rank - 1)[column][128 rows].
+    const int q = warp & 3;
+    const bool epi = warp >= 4;
+    float* slots = reinterpret_cast<float*>(smem);
+    bool done = true;
+    if (epi) {
+      pdl_wait_prior_grid();
+      done = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_full[0]), 0));
+      tmem_fence_after_sync();
+      if (!done && lane == 0) give_up();
+    }
+    __syncthreads();
+    cluster_barrier();
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    if (epi && rank != 0) {
+      uint32_t dst;
+      const float* mine = slots + static_cast<size_t>(rank - 1) * NT * kLM + 32 * q + lane;
+      asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_addr(mine)));
+#pragma unroll 1
+      for (int c0 = 0; c0 < NT; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(lane_base + c0, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + (c0 + e) * kLM * 4), "r"(v[e]) : "memory");
+      }
+    }
+    cluster_barrier();
+    if (epi && rank == 0 && !aborted()) {
+      const int row = (t0 % c.mt) * kLM + 32 * q + lane, r0 = (t0 / c.mt) * NT;
+      const float rw = row < p.N ? __ldg(p.w_rs + row) : 0.0f;
+      float rx[kRx];
+      load_rx(rx, r0);
+#pragma unroll
+      for (int c0 = 0; c0 < NT; c0 += 16) {
+        if (r0 + c0 < p.R) {
+          uint32_t v[16];
+          tmem_ld16(lane_base + c0, v);
+          float s[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(v[e]);
+          for (int k = 1; k < c.splits; ++k)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              s[e] = __fadd_rn(s[e], slots[(static_cast<size_t>(k - 1) * NT + c0 + e) * kLM + 32 * q + lane]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) store_y(r0, c0 + e, row, s[e], rw, rx);
+        }
+      }
+    }
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    // after a timeout the epilogue may have stopped early: tensor memory is released only once the
+    // MMAs issued into it are done (normally this returns at once)
+    if (lane == 0 && aborted())
+      for (int b = 0; b < 2; ++b) {
+        (void)mbar_wait_bounded(smem_addr(&acc_full[b]), 0);
+        (void)mbar_wait_bounded(smem_addr(&acc_full[b]), 1);
+      }
+    __syncwarp();
+    tmem_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  pdl_launch_dependents();
+}
+
+// ------------------------------------------------------------------------------- schedule
+// Few rows (up to one tile of them): the smallest N tile, and k split over clusters until the weight
+// tiles fill the SMs. More: the N tile whose waves cost the least (a wave's time goes with N).
+LinearSched make_sched(int R, int N, int kp, int sm_count) {
+  LinearSched c{};
+  c.mt = (N + kLM - 1) / kLM;
+  c.nkb = kp / kLK;
+  c.splits = 1;
+  static const int kTiles[] = {16, 32, 64, 128, 192, 224};
+  double best = 1e30;
+  for (int nt : kTiles) {
+    if (R > 128 && nt < 64) continue;  // (the workspace holds the scale blocks of no smaller tiles)
+    const int64_t tiles = static_cast<int64_t>(c.mt) * ((R + nt - 1) / nt);
+    int splits = 1;
+    while (splits < kMaxSplits && splits < c.nkb && tiles * (splits + 1) <= sm_count &&
+           static_cast<size_t>(splits) * nt * kLM * 4 <= 160 * 1024)
+      ++splits;
+    const int64_t waves = (tiles * splits + sm_count - 1) / sm_count;
+    const int kbs = (c.nkb + splits - 1) / splits;
+    // per stage: the MMAs (N 16 columns at a time), or the copy of 128 + nt rows of codes
+    const double cost = static_cast<double>(waves) * (kbs * (nt > 96 ? nt : 96 + nt / 16) + 400.0) + nt;
+    if (cost < best) {
+      best = cost;
+      c.nt = nt;
+      c.tiles = static_cast<int>(tiles);
+      c.splits = splits;
+    }
+  }
+  return c;
+}
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct LinearWs {
   uint8_t* q;
-  uint8_t* bs;
+  uint8_t* sf;
   float* rs;
-  uint16_t* xh;
 };
+// Workspace: codes [R, kp / 2], block scales, row scales [R]. The block scales take whole 128-row
+// blocks per activation tile; the size allows for the tile that needs the most of them.
 size_t bind(LinearWs* w, uint8_t* p, int R, int K) {
-  const size_t kp = fp4_padded(K), rp = (static_cast<size_t>(R) + 7) / 8 * 8;
+  const size_t kp = fp4_padded(K);
   uint8_t* p0 = p;
   w->q = p;
-  p += round256(R * kp / 2);
-  w->bs = p;
-  p += round256(R * kp / 16);
+  p += round256(static_cast<size_t>(R) * kp / 2);
   w->rs = reinterpret_cast<float*>(p);
   p += round256(static_cast<size_t>(R) * 4);
-  w->xh = reinterpret_cast<uint16_t*>(p);
-  p += rp * kp * 2;
+  w->sf = p;
+  const size_t blocks = R <= 128 ? 8 : (static_cast<size_t>(R) + 63) / 64 + 2;  // see make_sched
+  p += blocks * (kp / 64) * 512;
   return static_cast<size_t>(p - p0);
 }
 
-// code * s of the quantised activations in f16 (exact); rows past R become zeros.
-__global__ void __launch_bounds__(256) fp4_expand_kernel(const Fp4Matrix m, uint16_t* xh, int R, int rp, int kp) {
-  const int64_t total = static_cast<int64_t>(rp) * (kp / 8);
-  pdl_wait_prior_grid();
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t row = i / (kp / 8);
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if (row < R) {
-      const uint32_t s2 = e4m3x2_to_f16x2(m.bs[i / 2] * 0x0101u);
-      e2m1x8_to_f16x2x4(reinterpret_cast<const uint32_t*>(m.q)[i], v);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) v[t] = f16x2_mul(v[t], s2);
+template <int NT, bool SPLIT>
+cudaError_t launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const LinearParams& p, const LinearSched& c,
+                        int sm_count, cudaStream_t stream) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  const void* kernel = reinterpret_cast<const void*>(linear_fp4_kernel<NT, SPLIT>);
+  constexpr size_t smem = LTile<NT>::kSmem;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (err != cudaSuccess) return err;
+      done[dev] = true;
     }
-    reinterpret_cast<uint4*>(xh)[i] = make_uint4(v[0], v[1], v[2], v[3]);
   }
-  pdl_launch_dependents();
+  CUtensorMap w = tw, x = tx;
+  LinearParams pp = p;
+  LinearSched cc = c;
+  void* args[] = {&w, &x, &pp, &cc};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? c.tiles * c.splits : (c.tiles < sm_count ? c.tiles : sm_count)));
+  cfg.blockDim = dim3(kLThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(c.splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = SPLIT ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-constexpr int kWarpsPerCta = 8;
+template <int NT>
+cudaError_t launch_nt(const CUtensorMap& tw, const CUtensorMap& tx, const LinearParams& p, const LinearSched& c,
+                      int sm_count, cudaStream_t stream) {
+  return c.splits > 1 ? launch_tile<NT, true>(tw, tx, p, c, sm_count, stream)
+                      : launch_tile<NT, false>(tw, tx, p, c, sm_count, stream);
+}
 
-__global__ void __launch_bounds__(kWarpsPerCta * 32) linear_fp4_kernel(const Fp4Matrix w, const uint16_t* xh,
-                                                                       const float* rs_x, uint16_t* y, int R, int N,
-                                                                       int kp) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  pdl_wait_prior_grid();
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kWarpsPerCta + warp) * 16;
-  const int t0 = blockIdx.y * 8;
-  if (r0 < N) {
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    fp4_dot_16x8(w.q, w.bs, r0, N, kp, xh + static_cast<size_t>(t0) * kp, d);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + 2 * t4 + (i & 1);
-      const int64_t n = r0 + g + 8 * (i >> 1);
-      if (t < R && n < N)
-        y[static_cast<int64_t>(t) * N + n] =
-            static_cast<uint16_t>(bf16_bits_rn(__fmul_rn(__fmul_rn(d[i], w.rs[n]), rs_x[t])));
-    }
-  }
-  pdl_launch_dependents();
+bool code_map(CUtensorMap* tm, const uint8_t* base, int rows, int kp, int box_rows, TmapEncodeFn enc) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kp / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kp / 2)};
+  const cuuint32_t box[2] = {kLK / 2, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -88,23 +536,25 @@ cudaError_t launch_linear_fp4(const Fp4LinearArgs& a, cudaStream_t stream) {
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
+  const TmapEncodeFn enc = tensor_map_encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
   LinearWs w;
   bind(&w, a.ws, a.R, a.K);
-  err = launch_fp4_quantize(a.x, w.q, w.bs, w.rs, a.status, a.valid, a.R, a.K, stream);
+  const int kp = fp4_padded(a.K);
+  const LinearSched c = make_sched(a.R, a.N, kp, di.sm_count);
+  CUtensorMap tw, tx;
+  if (!code_map(&tw, a.w.q, a.N, kp, kLM, enc) || !code_map(&tx, w.q, a.R, kp, c.nt, enc)) return cudaErrorNotSupported;
+  err = launch_fp4_quantize(a.x, w.q, w.sf, w.rs, a.status, a.valid, a.R, a.K, stream, c.nt);
   if (err != cudaSuccess) return err;
-  int kp = fp4_padded(a.K), R = a.R, N = a.N, rp = (a.R + 7) / 8 * 8;
-  {
-    Fp4Matrix m{w.q, w.bs, w.rs};
-    void* args[] = {&m, &w.xh, &R, &rp, &kp};
-    err = launch_pdl(reinterpret_cast<const void*>(fp4_expand_kernel), dim3(4 * di.sm_count), dim3(256), 0, stream, args);
-    if (err != cudaSuccess) return err;
+  const LinearParams p{a.w.bs, a.w.rs, w.sf, w.rs, a.y, a.status, a.R, a.N, kp};
+  switch (c.nt) {
+    case 16: return launch_nt<16>(tw, tx, p, c, di.sm_count, stream);
+    case 32: return launch_nt<32>(tw, tx, p, c, di.sm_count, stream);
+    case 64: return launch_nt<64>(tw, tx, p, c, di.sm_count, stream);
+    case 128: return launch_nt<128>(tw, tx, p, c, di.sm_count, stream);
+    case 192: return launch_nt<192>(tw, tx, p, c, di.sm_count, stream);
+    default: return launch_nt<224>(tw, tx, p, c, di.sm_count, stream);
   }
-  Fp4Matrix m = a.w;
-  uint16_t* y = a.y;
-  void* args[] = {&m, &w.xh, &w.rs, &y, &R, &N, &kp};
-  return launch_pdl(reinterpret_cast<const void*>(linear_fp4_kernel),
-                    dim3((N + kWarpsPerCta * 16 - 1) / (kWarpsPerCta * 16), rp / 8), dim3(kWarpsPerCta * 32), 0, stream,
-                    args);
 }
 
 }  // namespace mtp
