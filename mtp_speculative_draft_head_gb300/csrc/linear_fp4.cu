@@ -23,8 +23,8 @@
 // is split over a cluster of 2 to 8 CTAs, whose fp32 partial sums meet in the first CTA's shared
 // memory and are added in k order.
 //
-// Warp roles: 0 TMA producer, 1 tensor-memory allocation and MMA issue, 2 weight scales, 4..7
-// epilogue (warp w reads TMEM lanes 32 (w % 4) ..). Every wait is bounded, as in context.cu.
+// Warp roles: 0 weight codes, 1 tensor-memory allocation and MMA issue, 2 weight scales, 3
+// activation codes and scales, 4..7 epilogue (warp w reads TMEM lanes 32 (w % 4) ..). Every wait is bounded, as in context.cu.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -92,13 +92,46 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// 32 rows of 16 bytes (512 contiguous bytes of shared memory) to four TMEM columns, repeated in all
-// four 32-lane quarters.
-__device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint32_t smem) {
-  // no swizzle, groups of eight 16-byte rows 128 bytes apart, descriptor version 1
-  const uint64_t d = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
-                     (static_cast<uint64_t>(1) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// Descriptor of 32 rows of 16 bytes (512 contiguous bytes of shared memory): no swizzle, groups of
+// eight 16-byte rows 128 bytes apart, descriptor version 1.
+__device__ __forceinline__ uint64_t sf_desc(uint32_t smem) {
+  return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+// Those rows to four TMEM columns, repeated in all four 32-lane quarters.
+__device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// A position in the ring of stages: slot and the parity of its current round.
+template <int STAGES>
+struct Ring {
+  uint32_t s = 0, ph = 0, used = 0;
+  __device__ __forceinline__ void next() {
+    ++used;
+    if (++s == STAGES) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+// The copies of a producer's last stages land before the CTA's shared memory goes away (normally the
+// MMA warp has seen them all; after a timeout another role's arrival may be missing, and the waits
+// end by their limit).
+template <int STAGES>
+__device__ __forceinline__ void drain(Ring<STAGES> r, uint64_t* full) {
+  for (uint32_t i = 0; i < STAGES && i < r.used; ++i) {
+    if (r.s == 0) {
+      r.s = STAGES;
+      r.ph ^= 1u;
+    }
+    --r.s;
+    (void)mbar_wait_bounded(smem_addr(&full[r.s]), r.ph);
+  }
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -145,7 +178,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&full[i]), 2);  // the producer and the scale warp
+      mbar_init(smem_addr(&full[i]), 3);  // the two producers and the scale warp
       mbar_init(smem_addr(&empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -154,6 +187,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
     }
     abort_flag = 0;
     fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_x)) : "memory");
   }
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmemCols);
   tmem_fence_before_sync();
@@ -180,138 +215,151 @@ __global__ void __launch_bounds__(kLThreads, 1)
       p.y[static_cast<size_t>(r0 + col) * p.N + row] = static_cast<uint16_t>(bf16_bits_rn(__fmul_rn(__fmul_rn(v, rw), s)));
   };
 
+  // The roles below run as whole warps on warp-uniform values, with one elected lane issuing: a copy or
+  // an MMA issued from a single-lane branch pays for moving each operand to the uniform registers,
+  // ~300 cycles a stage in each role (about 1,100 cycles a stage in all against 320 of MMAs).
   if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      uint64_t pol_w, pol_x;
-      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol_w));
-      asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
-      const int ntiles = t0 < c.tiles ? (c.tiles - t0 + step - 1) / step : 0;
-      const int total = ntiles * nkb;
-      auto load_w = [&](int i) {
-        const int t = t0 + (i / nkb) * step, kb = kb0 + i % nkb;
-        const uint32_t bar = smem_addr(&full[i % kStages]);
-        mbar_arrive_expect_tx(bar, kABytes + TL::kBBytes + kSfChunk * kChunks);
-        tma_load_2d(smem_addr(smem + (i % kStages) * TL::kStageBytes), &tm_w, kb * (kLK / 2), (t % c.mt) * kLM, bar, pol_w);
-      };
-      auto load_x = [&](int i) {
-        const int t = t0 + (i / nkb) * step, kb = kb0 + i % nkb, xt = t / c.mt;
-        const uint32_t bar = smem_addr(&full[i % kStages]);
-        const uint32_t st = smem_addr(smem + (i % kStages) * TL::kStageBytes);
-        tma_load_2d(st + kABytes, &tm_x, kb * (kLK / 2), xt * NT, bar, pol_x);
-        for (int ch = 0; ch < kChunks; ++ch)
-          bulk_copy_g2s(st + kABytes + TL::kBBytes + kSfChunk * (1 + ch),
-                        p.x_sf + ((static_cast<size_t>(xt) * kChunks + ch) * (p.kp / 64) + kb * 4) * 512, kSfChunk, bar,
-                        pol_x);
-      };
-      // the weights do not depend on the kernel before (the quantiser): the first stages' weight
-      // codes are in flight before the wait for it
-      const int pre = total < kStages ? total : kStages;
-      for (int i = 0; i < pre; ++i) load_w(i);
-      pdl_wait_prior_grid();
-      for (int i = 0; i < pre; ++i) load_x(i);
-      int issued = pre;
-      for (int i = pre; i < total; ++i) {
-        if (aborted() || !mbar_wait_bounded(smem_addr(&empty[i % kStages]), static_cast<uint32_t>((i / kStages - 1) & 1))) {
-          give_up();
-          break;
+    // ------------------------------------------------------------------ weight codes
+    // They do not depend on the kernel before (the quantiser): the ring fills while it runs.
+    const bool lead = elect_one();
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    Ring<kStages> r;
+    bool ok = true;
+    for (int t = t0; t < c.tiles && ok; t += step) {
+      const int row = (t % c.mt) * kLM;
+      for (int kb = kb0; kb < kb0 + nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
+        if (!ok) break;
+        if (lead) {
+          const uint32_t bar = smem_addr(&full[r.s]);
+          mbar_arrive_expect_tx(bar, kABytes);
+          tma_load_2d(smem_addr(smem) + r.s * TL::kStageBytes, &tm_w, kb * (kLK / 2), row, bar, pol);
         }
-        load_w(i);
-        load_x(i);
-        ++issued;
+        r.next();
       }
-      // every copy issued must land before the CTA's shared memory goes away (normally the MMA thread
-      // has seen them all; after a timeout the scale warp's arrival may be missing, and the wait ends
-      // by its limit)
-      for (int i = issued - kStages < 0 ? 0 : issued - kStages; i < issued; ++i)
-        (void)mbar_wait_bounded(smem_addr(&full[i % kStages]), static_cast<uint32_t>((i / kStages) & 1));
     }
-    __syncwarp();
+    if (!ok && lane == 0) give_up();
+    drain(r, full);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ activation codes and scales
+    const bool lead = elect_one();
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+    pdl_wait_prior_grid();  // the quantiser's
+    Ring<kStages> r;
+    bool ok = true;
+    for (int t = t0; t < c.tiles && ok; t += step) {
+      const int xt = t / c.mt;
+      const uint8_t* sf = p.x_sf + (static_cast<size_t>(xt) * kChunks * (p.kp / 64) + kb0 * 4) * 512;
+      for (int kb = kb0; kb < kb0 + nkb; ++kb, sf += kSfChunk) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
+        if (!ok) break;
+        if (lead) {
+          const uint32_t bar = smem_addr(&full[r.s]);
+          const uint32_t st = smem_addr(smem) + r.s * TL::kStageBytes + kABytes;
+          mbar_arrive_expect_tx(bar, TL::kBBytes + kSfChunk * kChunks);
+          tma_load_2d(st, &tm_x, kb * (kLK / 2), xt * NT, bar, pol);
+#pragma unroll
+          for (int ch = 0; ch < kChunks; ++ch)
+            bulk_copy_g2s(st + TL::kBBytes + kSfChunk * (1 + ch), sf + static_cast<size_t>(ch) * (p.kp / 64) * 512, kSfChunk,
+                          bar, pol);
+        }
+        r.next();
+      }
+    }
+    if (!ok && lane == 0) give_up();
+    drain(r, full);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_fp4(kLM, NT);
-      int i = 0, n = 0;
-      bool ok = true;
-      for (int t = t0; t < c.tiles && ok; t += step, ++n) {
-        const int buf = n & 1;
-        // this accumulator's previous tile must have left tensor memory
-        if (n >= 2 && !mbar_wait_bounded(smem_addr(&acc_empty[buf]), static_cast<uint32_t>((n / 2 - 1) & 1))) {
-          give_up();
-          ok = false;
-        }
+    constexpr uint32_t idesc = idesc_fp4(kLM, NT);
+    const bool lead = elect_one();
+    Ring<kStages> r;
+    bool ok = true;
+    int n = 0;
+    for (int t = t0; t < c.tiles && ok; t += step, ++n) {
+      const int buf = n & 1;
+      // this accumulator's previous tile must have left tensor memory
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_empty[buf]), static_cast<uint32_t>(((n >> 1) & 1) ^ 1)));
+      tmem_fence_after_sync();
+      const uint32_t acc = tmem + static_cast<uint32_t>(buf * NT);
+      for (int kb = 0; kb < nkb && ok; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&full[r.s]), r.ph));
+        if (!ok) break;
         tmem_fence_after_sync();
-        for (int kb = 0; kb < nkb && ok; ++kb, ++i) {
-          const int s = i % kStages;
-          if (aborted() || !mbar_wait_bounded(smem_addr(&full[s]), static_cast<uint32_t>((i / kStages) & 1))) {
-            give_up();
-            ok = false;
-            break;
-          }
-          tmem_fence_after_sync();
-          const uint32_t st = smem_addr(smem + s * TL::kStageBytes);
+        if (lead) {
+          const uint32_t st = smem_addr(smem) + r.s * TL::kStageBytes;
           const uint32_t sf = st + kABytes + TL::kBBytes;
-          const uint64_t da = umma_desc_sw128(st), db = umma_desc_sw128(st + kABytes);
+          const uint64_t da = umma_desc_sw128(st), db = umma_desc_sw128(st + kABytes), ds = sf_desc(sf);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // 64 codes = 32 bytes along the swizzle row
             const uint32_t sfa = tmem + TL::kSfaCol + 4 * k, sfb = tmem + TL::kSfbCol + 4 * kChunks * k;
-            tmem_copy_sf(sfa, sf + 512 * k);
+            tmem_copy_sf(sfa, ds + 32 * k);
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) tmem_copy_sf(sfb + 4 * ch, sf + kSfChunk * (1 + ch) + 512 * k);
-            umma_fp4(tmem + static_cast<uint32_t>(buf * NT), da + 2 * k, db + 2 * k, idesc, sfa, sfb, (kb | k) != 0 ? 1u : 0u);
+            for (int ch = 0; ch < kChunks; ++ch) tmem_copy_sf(sfb + 4 * ch, ds + (kSfChunk / 16) * (1 + ch) + 32 * k);
+            umma_fp4(acc, da + 2 * k, db + 2 * k, idesc, sfa, sfb, (kb | k) != 0 ? 1u : 0u);
           }
-          umma_commit(smem_addr(&empty[s]));  // the stage is free once these have read it
+          umma_commit(smem_addr(&empty[r.s]));  // the stage is free once these have read it
         }
-        umma_commit(smem_addr(&acc_full[buf]));
+        r.next();
       }
+      if (lead) umma_commit(smem_addr(&acc_full[buf]));
+      __syncwarp();
     }
-    __syncwarp();
+    if (!ok && lane == 0) give_up();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ weight scales
     // Lane r holds the 16 scale bytes of rows r, r + 32, r + 64, r + 96 of the tile for one stage:
     // word k of a row belongs to MMA k. Loads run kAhead stages ahead of the stores.
-    constexpr int kAhead = 3;
-    const int ntiles = t0 < c.tiles ? (c.tiles - t0 + step - 1) / step : 0;
-    const int total = ntiles * nkb;
+    constexpr int kAhead = 4;
     uint4 v[kAhead][4];
-    auto fetch = [&](int i, uint4 (&d)[4]) {
-      const int t = t0 + (i / nkb) * step, kb = kb0 + i % nkb;
+    int ft = t0, fkb = kb0;  // the next stage to fetch
+    const uint8_t* rows[4];
+    auto seek = [&] {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int row = (t % c.mt) * kLM + 32 * j + lane;
-        d[j] = i < total && row < p.N
-                   ? __ldg(reinterpret_cast<const uint4*>(p.w_bs + static_cast<size_t>(row) * (p.kp / 16)) + kb)
-                   : make_uint4(0u, 0u, 0u, 0u);
+        const int row = (ft % c.mt) * kLM + 32 * j + lane;
+        rows[j] = ft < c.tiles && row < p.N ? p.w_bs + static_cast<size_t>(row) * (p.kp / 16) : nullptr;
       }
     };
+    auto fetch = [&](uint4 (&d)[4]) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) fetch(a, v[a]);
+      for (int j = 0; j < 4; ++j)
+        d[j] = rows[j] != nullptr ? __ldg(reinterpret_cast<const uint4*>(rows[j]) + fkb) : make_uint4(0u, 0u, 0u, 0u);
+      if (++fkb == kb0 + nkb) {
+        fkb = kb0;
+        ft += step;
+        seek();
+      }
+    };
+    seek();
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) fetch(v[a]);
+    Ring<kStages> r;
     bool ok = true;
-    for (int i0 = 0; i0 < total && ok; i0 += kAhead) {
+    int left = t0 < c.tiles ? ((c.tiles - t0 + step - 1) / step) * nkb : 0;
+    while (left > 0 && ok) {
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        const int i = i0 + a;
-        if (i < total && ok) {
-          if (i >= kStages &&
-              (aborted() || !__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[i % kStages]),
-                                                                       static_cast<uint32_t>((i / kStages - 1) & 1))))) {
-            ok = false;
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(smem + (i % kStages) * TL::kStageBytes + kABytes + TL::kBBytes) + lane;
+        if (left > 0 && ok) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
+          if (ok) {
+            uint4* dst = reinterpret_cast<uint4*>(smem + r.s * TL::kStageBytes + kABytes + TL::kBBytes) + lane;
             dst[0] = make_uint4(v[a][0].x, v[a][1].x, v[a][2].x, v[a][3].x);
             dst[32] = make_uint4(v[a][0].y, v[a][1].y, v[a][2].y, v[a][3].y);
             dst[64] = make_uint4(v[a][0].z, v[a][1].z, v[a][2].z, v[a][3].z);
             dst[96] = make_uint4(v[a][0].w, v[a][1].w, v[a][2].w, v[a][3].w);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&full[i % kStages]));
-            fetch(i + kAhead, v[a]);
+            if (lane == 0) mbar_arrive(smem_addr(&full[r.s]));
+            r.next();
+            fetch(v[a]);
           }
+          --left;
         }
       }
     }
     if (!ok && lane == 0) give_up();
-    __syncwarp();
   } else if (warp >= 4 && !SPLIT) {
     // ------------------------------------------------------------------ epilogue
     const int q = warp & 3;
