@@ -144,6 +144,9 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t*
   const int t = threadIdx.x % TPR;
   const int kp = fp4_padded(k), nblk = kp / kFp4Block;
   pdl_wait_prior_grid();
+  // The next kernel may launch at once (what it reads before its own wait, a linear's weights, was
+  // written before this grid's wait ended).
+  pdl_launch_dependents();
   for (int64_t row = (static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x) / TPR; row < rows;
        row += static_cast<int64_t>(gridDim.x) * kQThreads / TPR) {
     const uint16_t* wr = w + row * k;
@@ -200,7 +203,6 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t*
       br[tile > 0 ? (b >> 2) * 512 + (b & 3) : b] = static_cast<uint8_t>(sc);
     }
   }
-  pdl_launch_dependents();
 }
 
 // bf16( fp32( code * s_j * rs ) ), 16 columns (one block scale) a thread. Idx: 32 bits when they
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const Fp4Matr
     }
     if (total - i <= step) break;  // the next index would pass the end (and may not fit Idx)
   }
-  pdl_launch_dependents();
+  // (no early launch: a sweep that follows may read w, as its lm_head, before its own wait)
 }
 
 }  // namespace

@@ -52,11 +52,11 @@ struct LTile {
   static constexpr int kChunks = (NT + 127) / 128;             // 128-row scale blocks of the activations
   static constexpr int kBBytes = NT * kLK / 2;
   static constexpr int kStageBytes = kABytes + kBBytes + kSfChunk * (1 + kChunks);
-  static constexpr int kFit = (200 * 1024) / kStageBytes;
+  static constexpr int kFit = (206 * 1024) / kStageBytes;
   static constexpr int kStages = kFit < 9 ? kFit : 9;
   static constexpr uint32_t kSfaCol = 2 * NT;                  // after the two accumulators
   static constexpr uint32_t kSfbCol = kSfaCol + 16;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 4) * 8 + 16;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 4) * 8 + 16 + 4 * NT * 4;
   static_assert(NT % 16 == 0 && NT <= 256, "N of an M = 128 MMA");
   static_assert(kSfbCol + 16 * kChunks <= kTmemCols, "tensor memory");
 };
@@ -67,6 +67,7 @@ struct LinearSched {
   int tiles;    // all tiles; tile t: weight tile t % mt, activation tile t / mt
   int nkb;      // stages per tile
   int splits;   // CTAs per tile (a cluster along k); 1: persistent
+  bool pair;    // persistent in pairs: a tile is two neighbouring weight tiles, mt counts those
 };
 
 struct LinearParams {
@@ -106,6 +107,28 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
+}
+// Copies to the same place in both CTAs of a pair, each completing on its own CTA's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_copy_pair(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4, %5;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(pol)
+      : "memory");
+}
+// Arrive on the barrier at this place in both CTAs of a pair when this thread's MMAs so far are done.
+__device__ __forceinline__ void umma_commit_pair(uint32_t mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 // A position in the ring of stages: slot and the parity of its current round.
 template <int STAGES>
@@ -153,7 +176,7 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // ------------------------------------------------------------------------------- kernel
-template <int NT, bool SPLIT>
+template <int NT, bool SPLIT, bool PAIR>
 __global__ void __launch_bounds__(kLThreads, 1)
     linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const LinearParams p, const LinearSched c) {
@@ -166,20 +189,23 @@ __global__ void __launch_bounds__(kLThreads, 1)
   uint64_t* acc_full = empty + kStages;   // [2]
   uint64_t* acc_empty = acc_full + 2;     // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  float* rx_all = reinterpret_cast<float*>(tmem_slot + 4);  // [4][NT]
   __shared__ int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this CTA's tiles t0, t0 + step, ... and its stages kb0 .. kb0 + nkb of each
-  const uint32_t rank = SPLIT ? cta_rank() : 0u;
-  const int t0 = SPLIT ? static_cast<int>(blockIdx.x) / c.splits : static_cast<int>(blockIdx.x);
-  const int step = SPLIT ? c.tiles : static_cast<int>(gridDim.x);
+  const uint32_t rank = SPLIT || PAIR ? cta_rank() : 0u;
+  const int t0 = SPLIT ? static_cast<int>(blockIdx.x) / c.splits : static_cast<int>(blockIdx.x) >> (PAIR ? 1 : 0);
+  const int step = SPLIT ? c.tiles : static_cast<int>(gridDim.x) >> (PAIR ? 1 : 0);
+  // first weight row and activation tile of tile t (a pair's CTAs take neighbouring weight tiles)
+  auto tile_row = [&](int t) { return (t % c.mt * (PAIR ? 2 : 1) + (PAIR ? static_cast<int>(rank) : 0)) * kLM; };
   const int kb0 = SPLIT ? static_cast<int>(rank) * c.nkb / c.splits : 0;
   const int nkb = (SPLIT ? (static_cast<int>(rank) + 1) * c.nkb / c.splits : c.nkb) - kb0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&full[i]), 3);  // the two producers and the scale warp
-      mbar_init(smem_addr(&empty[i]), 1);
+      mbar_init(smem_addr(&empty[i]), PAIR ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&acc_full[i]), 1);
@@ -193,6 +219,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmemCols);
   tmem_fence_before_sync();
   __syncthreads();
+  if constexpr (PAIR) cluster_barrier();  // the pair's barriers are ready for each other's arrivals
   tmem_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   auto aborted = [&] { return *reinterpret_cast<volatile int*>(&abort_flag) != 0; };
@@ -201,18 +228,41 @@ __global__ void __launch_bounds__(kLThreads, 1)
     atomicExch(&abort_flag, 1);
   };
 
-  // The epilogue's row scales of a tile's activation rows: lane l holds those of rows l, l + 32, ...
-  // (loaded before the accumulator is waited for; read one by one between the stores, each cost the
-  // epilogue an L2 round trip: 44 us a tile).
-  constexpr int kRx = (NT + 31) / 32;
-  auto load_rx = [&](float (&rx)[kRx], int r0) {
-#pragma unroll
-    for (int j = 0; j < kRx; ++j) rx[j] = r0 + 32 * j + lane < p.R ? __ldcg(p.x_rs + r0 + 32 * j + lane) : 0.0f;
+  // The row scales of a tile's activation rows, per epilogue warp in shared memory (loaded before the
+  // accumulator is waited for: read one by one between the stores, each cost an L2 round trip, 44 us a
+  // tile).
+  auto load_rx = [&](float* rx, int r0) {
+    for (int j = lane; j < NT; j += 32) rx[j] = r0 + j < p.R ? __ldcg(p.x_rs + r0 + j) : 0.0f;
+    __syncwarp();
   };
-  auto store_y = [&](int r0, int col, int row, float v, float rw, const float (&rx)[kRx]) {
-    const float s = __shfl_sync(0xffffffffu, rx[col >> 5], col & 31);
-    if (r0 + col < p.R && row < p.N)
-      p.y[static_cast<size_t>(r0 + col) * p.N + row] = static_cast<uint16_t>(bf16_bits_rn(__fmul_rn(__fmul_rn(v, rw), s)));
+  // Sixteen columns of y from this lane's accumulator row: neighbouring lanes swap halves, so that an
+  // even lane holds its own and the next weight row for one activation row, an odd lane for the next
+  // one, and a warp stores 2 x 64 bytes at a time (N odd: 2-byte stores).
+  auto store16 = [&](int r0, int c0, int row, const float (&v)[16], float rw, const float* rx) {
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 s = reinterpret_cast<const float2*>(rx + c0)[e];
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+          : "=r"(o[e])
+          : "f"(__fmul_rn(__fmul_rn(v[2 * e + 1], rw), s.y)), "f"(__fmul_rn(__fmul_rn(v[2 * e], rw), s.x)));
+    }
+    if ((p.N & 1) == 0) {
+      const int odd = lane & 1;
+      uint16_t* dst = p.y + static_cast<size_t>(r0 + c0 + odd) * p.N + (row - odd);
+      const bool in = row < p.N;  // N is even: the pair is inside or outside as a whole
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t w = __shfl_xor_sync(0xffffffffu, o[e], 1);
+        const uint32_t d = odd ? __byte_perm(w, o[e], 0x7632) : __byte_perm(o[e], w, 0x5410);
+        if (in && r0 + c0 + 2 * e + odd < p.R) *reinterpret_cast<uint32_t*>(dst + static_cast<size_t>(2 * e) * p.N) = d;
+      }
+    } else if (row < p.N) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (r0 + c0 + e < p.R)
+          p.y[static_cast<size_t>(r0 + c0 + e) * p.N + row] = static_cast<uint16_t>(o[e >> 1] >> (16 * (e & 1)));
+    }
   };
 
   // The roles below run as whole warps on warp-uniform values, with one elected lane issuing: a copy or
@@ -227,7 +277,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     Ring<kStages> r;
     bool ok = true;
     for (int t = t0; t < c.tiles && ok; t += step) {
-      const int row = (t % c.mt) * kLM;
+      const int row = tile_row(t);
       for (int kb = kb0; kb < kb0 + nkb; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
         if (!ok) break;
@@ -259,11 +309,21 @@ __global__ void __launch_bounds__(kLThreads, 1)
           const uint32_t bar = smem_addr(&full[r.s]);
           const uint32_t st = smem_addr(smem) + r.s * TL::kStageBytes + kABytes;
           mbar_arrive_expect_tx(bar, TL::kBBytes + kSfChunk * kChunks);
-          tma_load_2d(st, &tm_x, kb * (kLK / 2), xt * NT, bar, pol);
+          if constexpr (PAIR) {
+            // each CTA of the pair fetches half of the rows and of the scales for both
+            tma_load_2d_pair(st + rank * (TL::kBBytes / 2), &tm_x, kb * (kLK / 2), xt * NT + static_cast<int>(rank) * (NT / 2),
+                             bar, pol);
+            constexpr uint32_t kHalf = kSfChunk * kChunks / 2;  // of the chunks' scales taken in a row
+            const int ch = static_cast<int>(rank * kHalf) / kSfChunk;
+            bulk_copy_pair(st + TL::kBBytes + kSfChunk + rank * kHalf,
+                           sf + static_cast<size_t>(ch) * (p.kp / 64) * 512 + rank * kHalf % kSfChunk, kHalf, bar, pol);
+          } else {
+            tma_load_2d(st, &tm_x, kb * (kLK / 2), xt * NT, bar, pol);
 #pragma unroll
-          for (int ch = 0; ch < kChunks; ++ch)
-            bulk_copy_g2s(st + TL::kBBytes + kSfChunk * (1 + ch), sf + static_cast<size_t>(ch) * (p.kp / 64) * 512, kSfChunk,
-                          bar, pol);
+            for (int ch = 0; ch < kChunks; ++ch)
+              bulk_copy_g2s(st + TL::kBBytes + kSfChunk * (1 + ch), sf + static_cast<size_t>(ch) * (p.kp / 64) * 512,
+                            kSfChunk, bar, pol);
+          }
         }
         r.next();
       }
@@ -299,7 +359,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
             for (int ch = 0; ch < kChunks; ++ch) tmem_copy_sf(sfb + 4 * ch, ds + (kSfChunk / 16) * (1 + ch) + 32 * k);
             umma_fp4(acc, da + 2 * k, db + 2 * k, idesc, sfa, sfb, (kb | k) != 0 ? 1u : 0u);
           }
-          umma_commit(smem_addr(&empty[r.s]));  // the stage is free once these have read it
+          // the stage is free once these have read it (a pair fills the stages of both: both say so)
+          if constexpr (PAIR) umma_commit_pair(smem_addr(&empty[r.s]));
+          else umma_commit(smem_addr(&empty[r.s]));
         }
         r.next();
       }
@@ -310,52 +372,57 @@ __global__ void __launch_bounds__(kLThreads, 1)
   } else if (warp == 2) {
     // ------------------------------------------------------------------ weight scales
     // Lane r holds the 16 scale bytes of rows r, r + 32, r + 64, r + 96 of the tile for one stage:
-    // word k of a row belongs to MMA k. Loads run kAhead stages ahead of the stores.
-    constexpr int kAhead = 4;
-    uint4 v[kAhead][4];
+    // word k of a row belongs to MMA k. Four stages (64 bytes a row, two whole sectors) are loaded at a
+    // time, one group ahead of the stores; a group ends with its tile.
+    constexpr int kGroup = 4;
+    uint4 v[2][kGroup][4];
     int ft = t0, fkb = kb0;  // the next stage to fetch
-    const uint8_t* rows[4];
-    auto seek = [&] {
+    auto fetch = [&](uint4 (&d)[kGroup][4]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int row = (ft % c.mt) * kLM + 32 * j + lane;
-        rows[j] = ft < c.tiles && row < p.N ? p.w_bs + static_cast<size_t>(row) * (p.kp / 16) : nullptr;
-      }
-    };
-    auto fetch = [&](uint4 (&d)[4]) {
+        const int row = tile_row(ft) + 32 * j + lane;
+        const uint4* src = reinterpret_cast<const uint4*>(p.w_bs + static_cast<size_t>(row) * (p.kp / 16)) + fkb;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        d[j] = rows[j] != nullptr ? __ldg(reinterpret_cast<const uint4*>(rows[j]) + fkb) : make_uint4(0u, 0u, 0u, 0u);
-      if (++fkb == kb0 + nkb) {
+        for (int g = 0; g < kGroup; ++g)
+          d[g][j] = ft < c.tiles && row < p.N && fkb + g < kb0 + nkb ? __ldg(src + g) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      fkb += kGroup;
+      if (fkb >= kb0 + nkb) {
         fkb = kb0;
         ft += step;
-        seek();
       }
     };
-    seek();
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) fetch(v[a]);
+    fetch(v[0]);
     Ring<kStages> r;
     bool ok = true;
-    int left = t0 < c.tiles ? ((c.tiles - t0 + step - 1) / step) * nkb : 0;
-    while (left > 0 && ok) {
+    auto put = [&](const uint4 (&d)[4]) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
+      if (ok) {
+        uint4* dst = reinterpret_cast<uint4*>(smem + r.s * TL::kStageBytes + kABytes + TL::kBBytes) + lane;
+        dst[0] = make_uint4(d[0].x, d[1].x, d[2].x, d[3].x);
+        dst[32] = make_uint4(d[0].y, d[1].y, d[2].y, d[3].y);
+        dst[64] = make_uint4(d[0].z, d[1].z, d[2].z, d[3].z);
+        dst[96] = make_uint4(d[0].w, d[1].w, d[2].w, d[3].w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&full[r.s]));
+        r.next();
+      }
+    };
+    int t = t0, kb = 0;
+    while (t < c.tiles && ok) {
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        if (left > 0 && ok) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
-          if (ok) {
-            uint4* dst = reinterpret_cast<uint4*>(smem + r.s * TL::kStageBytes + kABytes + TL::kBBytes) + lane;
-            dst[0] = make_uint4(v[a][0].x, v[a][1].x, v[a][2].x, v[a][3].x);
-            dst[32] = make_uint4(v[a][0].y, v[a][1].y, v[a][2].y, v[a][3].y);
-            dst[64] = make_uint4(v[a][0].z, v[a][1].z, v[a][2].z, v[a][3].z);
-            dst[96] = make_uint4(v[a][0].w, v[a][1].w, v[a][2].w, v[a][3].w);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&full[r.s]));
-            r.next();
-            fetch(v[a]);
+      for (int h = 0; h < 2; ++h) {
+        if (t < c.tiles && ok) {
+          fetch(v[h ^ 1]);
+#pragma unroll
+          for (int g = 0; g < kGroup; ++g)
+            if (kb + g < nkb && ok) put(v[h][g]);
+          kb += kGroup;
+          if (kb >= nkb) {
+            kb = 0;
+            t += step;
           }
-          --left;
         }
       }
     }
@@ -367,9 +434,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
     int n = 0;
     for (int t = t0; t < c.tiles; t += step, ++n) {
       const int buf = n & 1;
-      const int row = (t % c.mt) * kLM + 32 * q + lane, r0 = (t / c.mt) * NT;
+      const int row = tile_row(t) + 32 * q + lane, r0 = (t / c.mt) * NT;
       const float rw = row < p.N ? __ldg(p.w_rs + row) : 0.0f;
-      float rx[kRx];
+      float* rx = rx_all + q * NT;
       load_rx(rx, r0);
       const bool done = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_full[buf]), static_cast<uint32_t>((n / 2) & 1)));
       tmem_fence_after_sync();
@@ -382,8 +449,10 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (r0 + c0 < p.R) {
           uint32_t v[16];
           tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(buf * NT + c0), v);
+          float s[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) store_y(r0, c0 + e, row, __uint_as_float(v[e]), rw, rx);
+          for (int e = 0; e < 16; ++e) s[e] = __uint_as_float(v[e]);
+          store16(r0, c0, row, s, rw, rx);
         }
       }
       tmem_fence_before_sync();
@@ -424,9 +493,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
     }
     cluster_barrier();
     if (epi && rank == 0 && !aborted()) {
-      const int row = (t0 % c.mt) * kLM + 32 * q + lane, r0 = (t0 / c.mt) * NT;
+      const int row = tile_row(t0) + 32 * q + lane, r0 = (t0 / c.mt) * NT;
       const float rw = row < p.N ? __ldg(p.w_rs + row) : 0.0f;
-      float rx[kRx];
+      float* rx = rx_all + q * NT;
       load_rx(rx, r0);
 #pragma unroll
       for (int c0 = 0; c0 < NT; c0 += 16) {
@@ -440,14 +509,14 @@ __global__ void __launch_bounds__(kLThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               s[e] = __fadd_rn(s[e], slots[(static_cast<size_t>(k - 1) * NT + c0 + e) * kLM + 32 * q + lane]);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) store_y(r0, c0 + e, row, s[e], rw, rx);
+          store16(r0, c0, row, s, rw, rx);
         }
       }
     }
   }
   tmem_fence_before_sync();
   __syncthreads();
+  if constexpr (PAIR) cluster_barrier();  // neither CTA leaves while the other may still write to it
   if (warp == 1) {
     // after a timeout the epilogue may have stopped early: tensor memory is released only once the
     // MMAs issued into it are done (normally this returns at once)
@@ -491,6 +560,13 @@ LinearSched make_sched(int R, int N, int kp, int sm_count) {
       c.splits = splits;
     }
   }
+  // Whole tiles on a full grid run in pairs of CTAs that share the activations' copies: without, the
+  // operands' way from L2 to the SMs is the bound (23 TB/s over all).
+  c.pair = c.splits == 1 && c.nt >= 128 && c.tiles >= sm_count;
+  if (c.pair) {
+    c.tiles = c.tiles / c.mt * ((c.mt + 1) / 2);
+    c.mt = (c.mt + 1) / 2;
+  }
   return c;
 }
 
@@ -516,12 +592,12 @@ size_t bind(LinearWs* w, uint8_t* p, int R, int K) {
   return static_cast<size_t>(p - p0);
 }
 
-template <int NT, bool SPLIT>
+template <int NT, bool SPLIT, bool PAIR>
 cudaError_t launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const LinearParams& p, const LinearSched& c,
                         int sm_count, cudaStream_t stream) {
   static std::mutex mu;
   static bool done[64] = {};
-  const void* kernel = reinterpret_cast<const void*>(linear_fp4_kernel<NT, SPLIT>);
+  const void* kernel = reinterpret_cast<const void*>(linear_fp4_kernel<NT, SPLIT, PAIR>);
   constexpr size_t smem = LTile<NT>::kSmem;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -540,7 +616,9 @@ cudaError_t launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const Line
   LinearSched cc = c;
   void* args[] = {&w, &x, &pp, &cc};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? c.tiles * c.splits : (c.tiles < sm_count ? c.tiles : sm_count)));
+  const int places = PAIR ? sm_count / 2 : sm_count;
+  const int cluster = SPLIT ? c.splits : (PAIR ? 2 : 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((SPLIT || c.tiles < places ? c.tiles : places) * cluster));
   cfg.blockDim = dim3(kLThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -548,19 +626,21 @@ cudaError_t launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const Line
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(c.splits);
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = SPLIT ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
 template <int NT>
 cudaError_t launch_nt(const CUtensorMap& tw, const CUtensorMap& tx, const LinearParams& p, const LinearSched& c,
                       int sm_count, cudaStream_t stream) {
-  return c.splits > 1 ? launch_tile<NT, true>(tw, tx, p, c, sm_count, stream)
-                      : launch_tile<NT, false>(tw, tx, p, c, sm_count, stream);
+  if (c.splits > 1) return launch_tile<NT, true, false>(tw, tx, p, c, sm_count, stream);
+  if constexpr (NT >= 128)
+    if (c.pair) return launch_tile<NT, false, true>(tw, tx, p, c, sm_count, stream);
+  return launch_tile<NT, false, false>(tw, tx, p, c, sm_count, stream);
 }
 
 bool code_map(CUtensorMap* tm, const uint8_t* base, int rows, int kp, int box_rows, TmapEncodeFn enc) {
@@ -591,7 +671,7 @@ cudaError_t launch_linear_fp4(const Fp4LinearArgs& a, cudaStream_t stream) {
   const int kp = fp4_padded(a.K);
   const LinearSched c = make_sched(a.R, a.N, kp, di.sm_count);
   CUtensorMap tw, tx;
-  if (!code_map(&tw, a.w.q, a.N, kp, kLM, enc) || !code_map(&tx, w.q, a.R, kp, c.nt, enc)) return cudaErrorNotSupported;
+  if (!code_map(&tw, a.w.q, a.N, kp, kLM, enc) || !code_map(&tx, w.q, a.R, kp, c.pair ? c.nt / 2 : c.nt, enc)) return cudaErrorNotSupported;
   err = launch_fp4_quantize(a.x, w.q, w.sf, w.rs, a.status, a.valid, a.R, a.K, stream, c.nt);
   if (err != cudaSuccess) return err;
   const LinearParams p{a.w.bs, a.w.rs, w.sf, w.rs, a.y, a.status, a.R, a.N, kp};
