@@ -220,6 +220,27 @@ def test_sweep_nan_sequence_drafts_minus_one():
     assert not ws[:2304].any()
 
 
+@pytest.mark.parametrize("B", [1, 16])
+@pytest.mark.parametrize("limit", [0, 200])
+def test_sweep_wait_limit(B, limit):
+    """Stage waits cut short report MTP_ERR_TIMEOUT or finish; the workspace serves the next call."""
+    x, fw, w4 = sweep_inputs(B, 2048, 30000, 17)
+    lg, d, ws = run_sweep(x, fw, w4)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    l2, d2 = torch.zeros_like(lg), torch.zeros_like(d)
+    prev = m.mtp_head_set_wait_limit_ns(limit)
+    try:
+        m.mtp_head_logits_argmax_fp4(x, fw, *w4, l2, d2, ws, st, eps=EPS)
+        torch.cuda.synchronize()
+    finally:
+        m.mtp_head_set_wait_limit_ns(prev)
+    code = int(st.item())
+    assert code == m.ERR_TIMEOUT if limit == 0 else code in (0, m.ERR_TIMEOUT)
+    assert not ws[:2304].any()
+    l3, d3, _ = run_sweep(x, fw, w4, ws=ws)
+    assert torch.equal(l3, lg) and torch.equal(d3, d)
+
+
 def test_sweep_graph_and_streams():
     """Two captured graphs with workspaces of their own, replayed on different streams together, and a
     call on a side stream: the bits of the plain call."""
