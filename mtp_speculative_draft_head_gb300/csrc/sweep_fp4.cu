@@ -40,8 +40,14 @@ constexpr int kXhatOffset = kWsBytes + 256;
 constexpr int kStageK = 512;  // codes per row and stage
 __host__ __device__ constexpr int stage_padded(int h) { return (h + kStageK - 1) / kStageK * kStageK; }
 
-// Small enough (with 32 registers a thread) to sit on an SM beside a sweep CTA.
 constexpr int kNormThreads = 320;
+
+// A load that stays in front of what follows.
+__device__ __forceinline__ uint4 ld_now(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
 
 // xhat_b = shared_head.norm(x_b) in BF16 (the exact rounding of the other kernels), stored as f16
 // times a power of two that puts the largest element just under 2^15: exact down to 2^-29 of it,
@@ -58,7 +64,23 @@ __global__ void __launch_bounds__(kNormThreads) fp4_xhat_kernel(const Fp4SweepAr
     return reinterpret_cast<uint4*>(a.ws + kXhatOffset) + (static_cast<size_t>(v >> 2) * nt + (b >> 3)) * 32 + (b & 7) * 4 + (v & 3);
   };
   pdl_wait_prior_grid();
-  // The sweep may launch at once: it reads the copy before its own wait (written, if it was, before this
+  // This row's first pieces are asked for before the sweep's weight stream can get in front of them.
+  constexpr int kHeld = 3;
+  uint4 hx[kHeld], hw[kHeld];
+  const bool vec = H % 8 == 0;  // rows of whole 16-byte pieces are read a piece at a time
+  const uint16_t* x = a.x + static_cast<size_t>(b < a.B ? b : 0) * H;
+  const uint4* xv = reinterpret_cast<const uint4*>(x);
+  const uint4* wv = reinterpret_cast<const uint4*>(a.final_norm_w);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int v = tid + i * kNormThreads;
+    hx[i] = hw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (vec && b < a.B && v < H / 8) {
+      hx[i] = ld_now(xv + v);
+      hw[i] = ld_now(wv + v);
+    }
+  }
+  // The sweep may launch now: it reads the copy before its own wait (written, if it was, before this
   // grid's wait ended), and the activations after it.
   pdl_launch_dependents();
   if (b >= a.B) {
@@ -66,28 +88,42 @@ __global__ void __launch_bounds__(kNormThreads) fp4_xhat_kernel(const Fp4SweepAr
     if (tid == 0) reinterpret_cast<float*>(a.ws + kUnscaleOffset)[b] = 0.0f;
     return;
   }
-  const uint16_t* x = a.x + static_cast<size_t>(b) * H;
-  // sum of squares (double-float) and max |x w| of the row times sc, a power of two: 1, or what brings
-  // the row near one when its squares leave the fp32 range
+  // sum of squares (double-float), max |x w| and max |x| of the row times sc, a power of two: 1, or what
+  // brings the row near one when its squares leave the fp32 range
   float sc = 1.0f;
   auto sums = [&](float& biggest) {
-    DF acc{0.0f, 0.0f};
+    DF2 acc{0ull, 0ull};
     float mx = 0.0f, mv = 0.0f;
-    for (int k = tid; k < H; k += kNormThreads) {
-      const float v = __fmul_rn(bf16_bits_to_f32(x[k]), sc);
-      df_add(acc, __fmul_rn(v, v));
-      mx = fmaxf(mx, fabsf(__fmul_rn(v, bf16_bits_to_f32(a.final_norm_w[k]))));
-      mv = fmaxf(mv, fabsf(v));
+    auto add = [&](float v0, float v1, float w0, float w1) {
+      v0 = __fmul_rn(v0, sc);
+      v1 = __fmul_rn(v1, sc);
+      const uint64_t v = f2_pack(v0, v1);
+      df2_add(acc, f2_mul(v, v));
+      mx = fmaxf(mx, fmaxf(fabsf(__fmul_rn(v0, w0)), fabsf(__fmul_rn(v1, w1))));
+      mv = fmaxf(mv, fmaxf(fabsf(v0), fabsf(v1)));
+    };
+    auto add8 = [&](const uint4& q, const uint4& wq) {
+      const uint32_t u[4] = {q.x, q.y, q.z, q.w}, w4[4] = {wq.x, wq.y, wq.z, wq.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add(bf16_lo(u[i]), bf16_hi(u[i]), bf16_lo(w4[i]), bf16_hi(w4[i]));
+    };
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) add8(hx[i], hw[i]);  // (zeros past the row)
+      for (int v = tid + kHeld * kNormThreads; v < H / 8; v += kNormThreads) add8(xv[v], wv[v]);
+    } else {
+      for (int k = tid; k < H; k += kNormThreads) add(bf16_bits_to_f32(x[k]), 0.0f, bf16_bits_to_f32(a.final_norm_w[k]), 0.0f);
     }
+    DF sum = df_add(df2_x(acc), df2_y(acc));
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
-      acc = df_add(acc, shfl_xor_df(acc, m));
+      sum = df_add(sum, shfl_xor_df(sum, m));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
       mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, m));
     }
     __syncthreads();  // the previous call's partials are read
     if (lane == 0) {
-      part[warp] = acc;
+      part[warp] = sum;
       pmax[warp] = mx;
       pval[warp] = mv;
     }
@@ -127,30 +163,45 @@ __global__ void __launch_bounds__(kNormThreads) fp4_xhat_kernel(const Fp4SweepAr
   }
   __syncthreads();
   const float rh = fac[0], rl = fac[1], xs = fac[2];
+#pragma unroll 1
   for (int v = tid; v < kp / 8; v += kNormThreads) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float y[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = 8 * v + 2 * i + j;
-        y[j] = 0.0f;
-        if (k < H)
-          y[j] = __fmul_rn(bf16_bits_to_f32(bf16_scaled_rne(
-                               __fmul_rn(__fmul_rn(bf16_bits_to_f32(x[k]), sc), bf16_bits_to_f32(a.final_norm_w[k])), rh, rl)),
-                           xs);
+    uint32_t xu[4] = {0u, 0u, 0u, 0u}, wu[4] = {0u, 0u, 0u, 0u};
+    if (vec) {
+      if (8 * v < H) {
+        const uint4 q = xv[v], wq = wv[v];  // from L1
+        xu[0] = q.x, xu[1] = q.y, xu[2] = q.z, xu[3] = q.w;
+        wu[0] = wq.x, wu[1] = wq.y, wu[2] = wq.z, wu[3] = wq.w;
       }
-      o[i] = f16x2_bits(y[0], y[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (8 * v + i < H) {
+          xu[i >> 1] |= static_cast<uint32_t>(x[8 * v + i]) << (16 * (i & 1));
+          wu[i >> 1] |= static_cast<uint32_t>(a.final_norm_w[8 * v + i]) << (16 * (i & 1));
+        }
     }
+    uint32_t o[4];
+    if (sc == 1.0f) {
+      const float wf[8] = {bf16_lo(wu[0]), bf16_hi(wu[0]), bf16_lo(wu[1]), bf16_hi(wu[1]),
+                           bf16_lo(wu[2]), bf16_hi(wu[2]), bf16_lo(wu[3]), bf16_hi(wu[3])};
+      const uint4 y = bf16x8_scaled_rne(xu, wf, rh, rl);
+      o[0] = y.x, o[1] = y.y, o[2] = y.z, o[3] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = bf16_scaled_rne(__fmul_rn(__fmul_rn(bf16_lo(xu[i]), sc), bf16_lo(wu[i])), rh, rl) |
+               (bf16_scaled_rne(__fmul_rn(__fmul_rn(bf16_hi(xu[i]), sc), bf16_hi(wu[i])), rh, rl) << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f16x2_bits(__fmul_rn(bf16_lo(o[i]), xs), __fmul_rn(bf16_hi(o[i]), xs));
     *piece(v) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
 constexpr int kRows = 128;             // rows per tile
-constexpr int kConsumers = 8;          // warps
+constexpr int kConsumers = 16;         // warps: four row quarters x four column quarters
+constexpr int kMT = kRows / 4 / 16;    // 16-row MMA tiles per warp
 constexpr int kSThreads = (kConsumers + 2) * 32;
-constexpr int kGroup = 2;              // row tiles that share an activation stage
 constexpr int kCodeBytes = kRows * kStageK / 2;    // 32 KB: two swizzled boxes of 128 bytes a row
 constexpr int kScaleBytes = kRows * kStageK / 16;  // 4 KB
 constexpr int kStageBytes = kCodeBytes + kScaleBytes;
@@ -160,9 +211,9 @@ struct SweepCfg {
   static constexpr int kStages = NT == 1 ? 5 : 4;
   static constexpr int kXBytes = NT * (kStageK / 32) * 512;  // activations of a stage
   static constexpr int kXStages = 3;
-  static constexpr int kPartBytes = 2 * 4 * 3 * 32 * NT * 16;  // [half][MMA tile][other quarter][lane][NT] float4
+  static constexpr int kPartBytes = 4 * 8 * NT * kRows * 4;  // [column quarter][sequence][row] fp32
   static constexpr size_t kSmem =
-      1024 + static_cast<size_t>(kStages) * kStageBytes + kXStages * kXBytes + kPartBytes + 2 * (kStages + kXStages) * 8 + kConsumers * 8 * NT * sizeof(ArgBest);
+      1024 + static_cast<size_t>(kStages) * kStageBytes + kXStages * kXBytes + kPartBytes + 2 * (kStages + kXStages) * 8 + kConsumers * 2 * NT * sizeof(ArgBest);
   static_assert(kSmem <= 226 * 1024, "shared memory");
 };
 
@@ -177,6 +228,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// A load that stays where it is written (an ordinary one was moved to its use, after the column loop,
+// and every tile then waited ~3,000 cycles for it).
+__device__ __forceinline__ float ldg_now(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 // Whether ok holds for every consumer thread (named barrier 1).
 __device__ __forceinline__ bool consumers_all(bool ok) {
   uint32_t r;
@@ -196,12 +254,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* xring = smem + C::kStages * kStageBytes;
-  float4* part = reinterpret_cast<float4*>(xring + C::kXStages * C::kXBytes);
+  float* part = reinterpret_cast<float*>(xring + C::kXStages * C::kXBytes);
   uint64_t* afull = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(part) + C::kPartBytes);
   uint64_t* aempty = afull + C::kStages;
   uint64_t* xfull = aempty + C::kStages;
   uint64_t* xempty = xfull + C::kXStages;
-  ArgBest* wbest = reinterpret_cast<ArgBest*>(xempty + C::kXStages);  // [warp][8 NT]
+  ArgBest* wbest = reinterpret_cast<ArgBest*>(xempty + C::kXStages);  // [warp][2 NT]
   __shared__ int is_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,7 +282,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_s)) : "memory");
   }
-  for (int i = threadIdx.x; i < kConsumers * 8 * NT; i += kSThreads) wbest[i] = ArgBest{0.0f, -1};
   __syncthreads();
 
   if (warp == kConsumers) {
@@ -237,27 +294,23 @@ __global__ void __launch_bounds__(kSThreads, 1)
     int slot = 0, issued = 0;
     uint32_t ph = 1;
     bool ok = true;
-    for (int gt = t0; gt < t1 && ok; gt += kGroup) {
-      const int nt = t1 - gt < kGroup ? t1 - gt : kGroup;
-      for (int kp = 0; kp < KP && ok; ++kp) {
-        for (int j = 0; j < nt; ++j) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&aempty[slot]), ph, wait_ns));
-          if (!ok) break;
-          if (lead) {
-            const uint32_t bar = smem_addr(&afull[slot]);
-            const uint32_t dst = smem_addr(smem) + slot * kStageBytes;
-            const int row = (gt + j) * kRows;
-            mbar_arrive_expect_tx(bar, kStageBytes);
-            // (past the end of a row both boxes are zeros)
-            tma_load_2d(dst, &tm_q, kp * (kStageK / 2), row, bar, pol);
-            tma_load_2d(dst + kCodeBytes / 2, &tm_q, kp * (kStageK / 2) + 128, row, bar, pol);
-            tma_load_2d(dst + kCodeBytes, &tm_s, kp * (kStageK / 16), row, bar, pol_s);
-          }
-          ++issued;
-          if (++slot == C::kStages) {
-            slot = 0;
-            ph ^= 1u;
-          }
+    for (int t = t0; t < t1 && ok; ++t) {
+      for (int kp = 0; kp < KP; ++kp) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&aempty[slot]), ph, wait_ns));
+        if (!ok) break;
+        if (lead) {
+          const uint32_t bar = smem_addr(&afull[slot]);
+          const uint32_t dst = smem_addr(smem) + slot * kStageBytes;
+          mbar_arrive_expect_tx(bar, kStageBytes);
+          // (past the end of a row the second box is zeros)
+          tma_load_2d(dst, &tm_q, kp * (kStageK / 2), t * kRows, bar, pol);
+          tma_load_2d(dst + kCodeBytes / 2, &tm_q, kp * (kStageK / 2) + 128, t * kRows, bar, pol);
+          tma_load_2d(dst + kCodeBytes, &tm_s, kp * (kStageK / 16), t * kRows, bar, pol_s);
+        }
+        ++issued;
+        if (++slot == C::kStages) {
+          slot = 0;
+          ph ^= 1u;
         }
       }
     }
@@ -274,7 +327,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     int slot = 0, issued = 0;
     uint32_t ph = 1;
     bool ok = true;
-    for (int gt = t0; gt < t1 && ok; gt += kGroup) {
+    for (int t = t0; t < t1 && ok; ++t) {
       for (int kp = 0; kp < KP; ++kp) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&xempty[slot]), ph, wait_ns));
         if (!ok) break;
@@ -297,180 +350,159 @@ __global__ void __launch_bounds__(kSThreads, 1)
   } else {
     // ------------------------------------------------------------------ consumers
     const int g = lane >> 2, t4 = lane & 3;
-    const int half = warp >> 2, quarter = warp & 3;
+    const int rq = warp >> 2, quarter = warp & 3;  // rows 32 rq .., columns 128 quarter .. of a stage
     // this warp's 64 bytes of a row's codes: box quarter / 2, 16-byte chunks 4 (quarter % 2) ..
     const uint32_t box = static_cast<uint32_t>(quarter >> 1) * (kCodeBytes / 2);
     const int chunk0 = 4 * (quarter & 1);
     const uint32_t pick = (t4 >> 1) ? 0x5531u : 0x4420u;  // bytes 2 c + (t4 / 2) of a word, c = 0, 1
-    ArgBest best[NT][2];
+    // In the epilogue a thread finishes row `er` of the tile for sequences eq, eq + 4, ...
+    const int er = threadIdx.x & (kRows - 1), eq = threadIdx.x / kRows;
+    ArgBest best[2 * NT];
+    float us[2 * NT];  // unscale factors of those sequences
 #pragma unroll
-    for (int jn = 0; jn < NT; ++jn) best[jn][0] = best[jn][1] = ArgBest{0.0f, -1};
+    for (int i = 0; i < 2 * NT; ++i) best[i] = ArgBest{0.0f, -1};
     int aslot = 0, xslot = 0;
     uint32_t ap = 0, xp = 0;
     bool ok = true;
     bool waited = false;
-    for (int gt = t0; gt < t1; gt += kGroup) {
-      const int ntile = t1 - gt < kGroup ? t1 - gt : kGroup;
-      float acc[kGroup][4][NT][4];
+    for (int t = t0; t < t1; ++t) {
+      float acc[kMT][NT][4];
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
+      for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int jn = 0; jn < NT; ++jn) acc[mt][jn][0] = acc[mt][jn][1] = acc[mt][jn][2] = acc[mt][jn][3] = 0.0f;
+      const int64_t row = static_cast<int64_t>(t) * kRows + er;
+      float rs = 0.0f;  // the row scale, ahead of the epilogue
+      if (row < V) rs = ldg_now(a.w.rs + row);
+      for (int kp = 0; kp < KP; ++kp) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&xfull[xslot]), xp, wait_ns) &&
+                                         mbar_wait_bounded(smem_addr(&afull[aslot]), ap, wait_ns));
+        if (!ok) break;
+        const uint32_t st = smem_addr(smem) + aslot * kStageBytes;
+        const uint32_t xs = smem_addr(xring) + xslot * C::kXBytes + (4 * quarter * NT * 32 + lane) * 16;
+        uint32_t sc[kMT][2][2];  // f16 scale pairs of rows g, g + 8: chunks 0, 1 and 2, 3
 #pragma unroll
-          for (int jn = 0; jn < NT; ++jn) acc[j][mt][jn][0] = acc[j][mt][jn][1] = acc[j][mt][jn][2] = acc[j][mt][jn][3] = 0.0f;
-      for (int kp = 0; kp < KP && ok; ++kp) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&xfull[xslot]), xp, wait_ns))) {
-          ok = false;
-          break;
-        }
-        uint4 x[4][NT];  // B fragments of this warp's 128 columns: two k16 steps a chunk
+        for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w0, w1;
+            lds_v2(w0, w1, st + kCodeBytes + (32 * rq + 16 * mt + g + 8 * h) * (kStageK / 16) + 8 * quarter);
+            sc[mt][h][0] = e4m3x2_to_f16x2(__byte_perm(w0, 0u, pick));
+            sc[mt][h][1] = e4m3x2_to_f16x2(__byte_perm(w1, 0u, pick));
+          }
+        float c4[kMT][NT][4];
 #pragma unroll
-          for (int jn = 0; jn < NT; ++jn)
-            x[c][jn] = lds128(smem_addr(xring) + xslot * C::kXBytes + (((4 * quarter + c) * NT + jn) * 32 + lane) * 16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&xempty[xslot]));
-        if (++xslot == C::kXStages) {
-          xslot = 0;
-          xp ^= 1u;
-        }
+        for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          if (j < ntile && ok) {
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&afull[aslot]), ap, wait_ns))) {
-              ok = false;
-            } else {
-              const uint32_t st = smem_addr(smem) + aslot * kStageBytes;
+          for (int jn = 0; jn < NT; ++jn) c4[mt][jn][0] = c4[mt][jn][1] = c4[mt][jn][2] = c4[mt][jn][3] = 0.0f;
 #pragma unroll
-              for (int mt = 0; mt < 4; ++mt) {
-                const int r0 = 64 * half + 16 * mt;
-                uint32_t sc[2][2];  // f16 scale pairs of rows g, g + 8: chunks 0, 1 and 2, 3
+        for (int cc = 0; cc < 4; cc += 2) {
+          uint32_t r[kMT][4];  // rows g, g + 8 of chunk cc, then of chunk cc + 1
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint32_t w0, w1;
-                  lds_v2(w0, w1, st + kCodeBytes + (r0 + g + 8 * h) * (kStageK / 16) + 8 * quarter);
-                  sc[h][0] = e4m3x2_to_f16x2(__byte_perm(w0, 0u, pick));
-                  sc[h][1] = e4m3x2_to_f16x2(__byte_perm(w1, 0u, pick));
-                }
-                float c4[NT][4];
+          for (int mt = 0; mt < kMT; ++mt)
+            ldmatrix_x4(r[mt], st + box + swz(32 * rq + 16 * mt + (lane & 15), chunk0 + cc + (lane >> 4)));
 #pragma unroll
-                for (int jn = 0; jn < NT; ++jn) c4[jn][0] = c4[jn][1] = c4[jn][2] = c4[jn][3] = 0.0f;
+          for (int i = 0; i < 2; ++i) {
+            uint4 x[NT];  // B fragments of the chunk's two k16 steps
 #pragma unroll
-                for (int cc = 0; cc < 4; cc += 2) {
-                  uint32_t r[4];  // rows g, g + 8 of chunk cc, then of chunk cc + 1
-                  ldmatrix_x4(r, st + box + swz(r0 + (lane & 15), chunk0 + cc + (lane >> 4)));
+            for (int jn = 0; jn < NT; ++jn) x[jn] = lds128(xs + ((cc + i) * NT + jn) * 512);
 #pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    uint32_t va[4], vb[4];
-                    e2m1x8_to_f16x2x4(r[2 * i], va);
-                    e2m1x8_to_f16x2x4(r[2 * i + 1], vb);
-                    const uint32_t sa = __byte_perm(sc[0][cc >> 1], 0u, i == 0 ? 0x1010u : 0x3232u);
-                    const uint32_t sb = __byte_perm(sc[1][cc >> 1], 0u, i == 0 ? 0x1010u : 0x3232u);
+            for (int mt = 0; mt < kMT; ++mt) {
+              uint32_t va[4], vb[4];
+              e2m1x8_to_f16x2x4(r[mt][2 * i], va);
+              e2m1x8_to_f16x2x4(r[mt][2 * i + 1], vb);
+              const uint32_t sa = __byte_perm(sc[mt][0][cc >> 1], 0u, i == 0 ? 0x1010u : 0x3232u);
+              const uint32_t sb = __byte_perm(sc[mt][1][cc >> 1], 0u, i == 0 ? 0x1010u : 0x3232u);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                      const uint32_t f[4] = {f16x2_mul(va[2 * h], sa), f16x2_mul(vb[2 * h], sb),
-                                             f16x2_mul(va[2 * h + 1], sa), f16x2_mul(vb[2 * h + 1], sb)};
-#pragma unroll
-                      for (int jn = 0; jn < NT; ++jn)
-                        mma_f16(c4[jn], f, h == 0 ? x[cc + i][jn].x : x[cc + i][jn].z,
-                                h == 0 ? x[cc + i][jn].y : x[cc + i][jn].w);
-                    }
-                  }
-                }
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t f[4] = {f16x2_mul(va[2 * h], sa), f16x2_mul(vb[2 * h], sb),
+                                       f16x2_mul(va[2 * h + 1], sa), f16x2_mul(vb[2 * h + 1], sb)};
 #pragma unroll
                 for (int jn = 0; jn < NT; ++jn)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) acc[j][mt][jn][i] = __fadd_rn(acc[j][mt][jn][i], c4[jn][i]);
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_addr(&aempty[aslot]));
-              if (++aslot == C::kStages) {
-                aslot = 0;
-                ap ^= 1u;
+                  mma_f16(c4[mt][jn], f, h == 0 ? x[jn].x : x[jn].z, h == 0 ? x[jn].y : x[jn].w);
               }
             }
           }
         }
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int jn = 0; jn < NT; ++jn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[mt][jn][i] = __fadd_rn(acc[mt][jn][i], c4[mt][jn][i]);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&aempty[aslot]));
+          mbar_arrive(smem_addr(&xempty[xslot]));
+        }
+        if (++aslot == C::kStages) {
+          aslot = 0;
+          ap ^= 1u;
+        }
+        if (++xslot == C::kXStages) {
+          xslot = 0;
+          xp ^= 1u;
+        }
       }
-      // a consumer that gave up takes the others with it, so that all meet at the barriers below
+      // a consumer that gave up takes the others with it, so that all meet at the barriers below (and the
+      // previous tile's partial sums have been read)
       ok = consumers_all(ok);
       if (!ok) break;
       if (!waited) {
         pdl_wait_prior_grid();  // the unscale factors come from the preceding kernel
         waited = true;
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) us[i] = __ldcg(reinterpret_cast<const float*>(a.ws + kUnscaleOffset) + eq + 4 * i);
       }
-      // ---- the quarters' sums of each tile: a warp finishes the MMA tile of its quarter's number
+      // ---- the column quarters' sums, rows swizzled by the sequence so that neither the fragments'
+      // stores nor the rows' loads conflict. The epilogue is short and its stores are whole 128-byte
+      // lines: straight from the fragments (unrolled, 32 bytes of a row at a time, on a quarter of the
+      // warps) it held the stages back for 7,500 cycles a tile at 16 sequences.
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        if (j < ntile) {  // the same for every consumer
-          named_barrier_sync(1, kConsumers * 32);  // the previous tile's sums are read
+      for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
-            if (mt != quarter)
+        for (int jn = 0; jn < NT; ++jn)
 #pragma unroll
-              for (int jn = 0; jn < NT; ++jn)
-                part[(((half * 4 + mt) * 3 + (quarter < mt ? quarter : quarter - 1)) * 32 + lane) * NT + jn] =
-                    make_float4(acc[j][mt][jn][0], acc[j][mt][jn][1], acc[j][mt][jn][2], acc[j][mt][jn][3]);
-          named_barrier_sync(1, kConsumers * 32);
-          const int64_t rbase = static_cast<int64_t>(gt + j) * kRows + 64 * half + 16 * quarter + g;
-          float rs[2];
-          rs[0] = rbase < V ? __ldg(a.w.rs + rbase) : 0.0f;
-          rs[1] = rbase + 8 < V ? __ldg(a.w.rs + rbase + 8) : 0.0f;
+          for (int i = 0; i < 4; ++i)
+            part[((quarter * 8 * NT + 8 * jn + 2 * t4 + (i & 1)) * kRows) + ((32 * rq + 16 * mt + g + 8 * (i >> 1)) ^ (t4 << 3))] =
+                acc[mt][jn][i];
+      named_barrier_sync(1, kConsumers * 32);
 #pragma unroll
-          for (int jn = 0; jn < NT; ++jn) {
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < 2 * NT; ++i) {
+        const int n = eq + 4 * i;
+        if (n < a.B && row < V) {
+          const float* src = part + n * kRows + (er ^ (((n >> 1) & 3) << 3));
+          float s = src[0];
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-              if (mt == quarter)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = acc[j][mt][jn][i];
-#pragma unroll
-            for (int o = 0; o < 3; ++o) {
-              const float4 v = part[(((half * 4 + quarter) * 3 + o) * 32 + lane) * NT + jn];
-              s[0] = __fadd_rn(s[0], v.x);
-              s[1] = __fadd_rn(s[1], v.y);
-              s[2] = __fadd_rn(s[2], v.z);
-              s[3] = __fadd_rn(s[3], v.w);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int n = 8 * jn + 2 * t4 + (i & 1);
-              const int64_t row = rbase + 8 * (i >> 1);
-              if (n < a.B && row < V) {
-                const float us = __ldcg(reinterpret_cast<const float*>(a.ws + kUnscaleOffset) + n);
-                const float v = __fmul_rn(__fmul_rn(s[i], us), rs[i >> 1]);
-                if (a.logits != nullptr) a.logits[static_cast<int64_t>(n) * V + row] = v;
-                arg_update(best[jn][i & 1], v, static_cast<int32_t>(row));
-              }
-            }
-          }
+          for (int q = 1; q < 4; ++q) s = __fadd_rn(s, src[q * 8 * NT * kRows]);
+          const float v = __fmul_rn(__fmul_rn(s, us[i]), rs);
+          if (a.logits != nullptr) __stcs(a.logits + static_cast<int64_t>(n) * V + row, v);
+          // rows come in ascending order: a later one wins only by a larger value
+          if (v > best[i].v || (best[i].i < 0 && v == v)) best[i] = ArgBest{v, static_cast<int32_t>(row)};
         }
       }
     }
     if (!ok && lane == 0) store_status(a.status, MTP_ERR_TIMEOUT);
-    // combine lanes that hold the same sequences (same t4), then publish per warp
+    // the warp's best of its rows, per sequence
 #pragma unroll
-    for (int jn = 0; jn < NT; ++jn)
+    for (int i = 0; i < 2 * NT; ++i) {
+      ArgBest b = best[i];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        ArgBest b = best[jn][hh];
-#pragma unroll
-        for (int m = 4; m < 32; m <<= 1) {
-          const float v = __shfl_xor_sync(0xffffffffu, b.v, m);
-          const int32_t i = __shfl_xor_sync(0xffffffffu, b.i, m);
-          if (i >= 0) arg_update(b, v, i);
-        }
-        const int n = 8 * jn + 2 * t4 + hh;
-        if (g == 0 && n < a.B) wbest[warp * 8 * NT + n] = b;
+      for (int m = 16; m > 0; m >>= 1) {
+        const float v = __shfl_xor_sync(0xffffffffu, b.v, m);
+        const int32_t j = __shfl_xor_sync(0xffffffffu, b.i, m);
+        if (j >= 0) arg_update(b, v, j);
       }
+      if (lane == 0) wbest[warp * 2 * NT + i] = b;
+    }
   }
   __syncthreads();
   pdl_wait_prior_grid();  // the workspace may still be read by the kernel before (no-op if done)
   if (threadIdx.x < a.B) {
     ArgBest c{0.0f, -1};
-    for (int w = 0; w < kConsumers; ++w) {
-      const ArgBest o = wbest[w * 8 * NT + threadIdx.x];
+    const int eq = threadIdx.x & 3;  // the four warps that held this sequence
+    for (int w = 4 * eq; w < 4 * eq + 4; ++w) {
+      const ArgBest o = wbest[w * 2 * NT + (threadIdx.x >> 2)];
       if (o.i >= 0) arg_update(c, o.v, o.i);
     }
     pick_publish(a.ws, threadIdx.x, c.v, c.i, 0);
