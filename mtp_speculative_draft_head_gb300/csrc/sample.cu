@@ -9,18 +9,21 @@
 //
 // No sort of the row: a prefix is { i : key_i >= cut } for one 64-bit key (the logit's order bits,
 // then the complement of the index), and the cut is found by histograms. Round 1 bins the row by
-// its distance from the maximum, linearly over the row's range (2048 bins, which spreads a
-// language model's bell-shaped logits better than their exponent bits would); the bin that holds
-// the cut is gathered and sorted when it has at most kGather entries, and is otherwise split by the
-// key's bits, 11 at a time, until it has.
+// its distance from the maximum, linearly over the distances at which a weight is more than nothing
+// (2048 bins; entries further down, masked ones among them, are left out of it). With a top_k whose
+// bin ends within kGather entries -- the usual case -- these are gathered and sorted by one CTA, which
+// finishes the row on the sorted list: no weight is formed for any other entry. Otherwise the bins
+// carry masses too; the bin that holds the cut is gathered and sorted when it has at most kGather
+// entries, and split by the key's bits, 11 at a time, until it has.
 //
 // Masses are 64-bit fixed-point numbers (2^62 / 2^ceil(log2 V) for a weight of one), so sums do not
 // depend on the order of the atomics or of the threads: the same inputs give the same token
 // whatever the cluster size. Weights are formed in fp32 from an exponent kept as a double-float:
 // relative error ~2^-23, against the 2^-24 of the given random numbers.
 //
-// A cluster of CTAs shares a row. Each keeps its slice in shared memory, so the row is read from
-// HBM once; maxima, histograms and masses are combined through distributed shared memory.
+// A cluster of CTAs shares a row; maxima, histograms and masses are combined through distributed
+// shared memory. A slice is kept in shared memory where it fits beside the histograms, and is read
+// again, from L2 mostly, where it does not (many rows).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -137,6 +140,15 @@ __device__ __forceinline__ u64 scale_ceil(float p, u64 z) {
   return q + ((lo << (64 - sh)) ? 1ull : 0ull);
 }
 
+// A 64-bit sum in shared memory by 32-bit atomics (a 64-bit one is a compare-and-swap loop there): the
+// low half's old value tells the carry, the high half is touched only when there is something to add.
+__device__ __forceinline__ void add64(uint32_t* halves, u64 v) {
+  const uint32_t lo = static_cast<uint32_t>(v);
+  uint32_t hi = static_cast<uint32_t>(v >> 32);
+  if (lo != 0u && atomicAdd(halves, lo) > ~lo) ++hi;
+  if (hi != 0u) atomicAdd(halves + 1, hi);
+}
+
 // Order of floats as unsigned numbers (no NaN); -0 is taken as +0.
 __device__ __forceinline__ uint32_t order_bits(float v) {
   uint32_t u = __float_as_uint(v);
@@ -223,8 +235,24 @@ __device__ void locate(const Shared& s, uint32_t rank, u64 target, int64_t i0, i
 }
 
 // ------------------------------------------------------------------------------- sampler
+// Bitonic sort, descending, of `size` (a power of two) 64-bit keys by the whole block.
+__device__ void sort_desc(u64* key, int size) {
+  for (int w = 2; w <= size; w <<= 1)
+    for (int d = w >> 1; d > 0; d >>= 1) {
+      for (int t = threadIdx.x; t < size / 2; t += kT) {
+        const int x = 2 * t - (t & (d - 1)), y = x + d;
+        const u64 ka = key[x], kb = key[y];
+        if ((ka < kb) == ((x & w) == 0)) {
+          key[x] = kb;
+          key[y] = ka;
+        }
+      }
+      __syncthreads();
+    }
+}
+
 template <bool BF16, bool RES>
-__global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int nc, int64_t slice, int frac) {
+__global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int nc, int64_t slice, int frac) {
   extern __shared__ __align__(128) uint8_t dyn[];
   Shared& s = *reinterpret_cast<Shared*>(dyn);
   uint8_t* p = dyn + (sizeof(Shared) + 127) / 128 * 128;
@@ -247,6 +275,11 @@ __global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int n
     if (nc > 1) cluster_sync_all();
     else __syncthreads();
   };
+  for (int b = tid; b < kBins; b += kT) {
+    loc.mass[b] = 0ull;
+    loc.n[b] = 0u;
+  }
+  if (tid == 0) s.gathered = 0u;
   pdl_wait_prior_grid();
 
   // ---- the row's parameters
@@ -262,54 +295,61 @@ __global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int n
     k = 1;
   }
 
+  const char* base = static_cast<const char*>(a.logits) + row * a.ld * (BF16 ? 2 : 4);
   auto raw = [&](int64_t i) -> float {
     float v;
-    if constexpr (BF16)
-      v = bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[row * a.ld + i]);
-    else
-      v = static_cast<const float*>(a.logits)[row * a.ld + i];
+    if constexpr (BF16) v = bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(base) + i));
+    else v = __ldg(reinterpret_cast<const float*>(base) + i);
     return v == v ? v : -INFINITY;  // NaN never wins
   };
   auto value = [&](int64_t i) -> float {
     if constexpr (RES) return res[i - i0];
-    return raw(i);
+    else return raw(i);
+  };
+  // fn(logit, index) over this thread's elements, kBatch loads in flight. Whole warps call fn: past the
+  // end of the slice with -inf, which counts for nothing.
+  constexpr int kBatch = 8;
+  auto each = [&](auto get, auto fn) {
+    for (int64_t i = i0 + tid; i - lane < i1; i += kBatch * kT) {
+      float v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) v[j] = i + j * kT < i1 ? get(i + j * kT) : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i + j * kT - lane < i1) fn(v[j], i + j * kT);
+    }
   };
 
   // ---- pass 1: the slice into shared memory, its largest and smallest finite-or-+inf logit
   uint32_t hi = 0u, lo = 0xFFFFFFFFu;  // order bits; 0 is below -inf
   const uint32_t kNegInf = order_bits(-INFINITY);
-  for (int64_t i = i0 + tid; i < i1; i += kT) {
-    const float v = raw(i);
+  each(raw, [&](float v, int64_t i) {
     if constexpr (RES) res[i - i0] = v;
     const uint32_t o = order_bits(v);
     if (o > kNegInf) {
       hi = o > hi ? o : hi;
       lo = o < lo ? o : lo;
     }
-  }
+  });
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
   if (lane == 0) {
     s.wmax[warp] = hi;
     s.wmin[warp] = lo;
   }
-  if (tid == 0) s.gathered = 0u;
-  __syncthreads();
+  if (nc > 1) cluster_sync_all();  // (also: every CTA of the cluster runs, its shared memory may be written)
+  else __syncthreads();
   if (warp == 0) {
     hi = __reduce_max_sync(0xffffffffu, lane < kW ? s.wmax[lane] : 0u);
     lo = __reduce_min_sync(0xffffffffu, lane < kW ? s.wmin[lane] : 0xFFFFFFFFu);
-    if (nc == 1) {
-      if (lane == 0) {
+    if (lane < nc) {
+      if (nc > 1) {
+        st_peer32(peer(&s.cmax[rank], lane), hi);
+        st_peer32(peer(&s.cmin[rank], lane), lo);
+      } else {
         s.cmax[0] = hi;
         s.cmin[0] = lo;
       }
-    }
-  }
-  if (nc > 1) {
-    cluster_sync_all();  // every CTA of the cluster runs: its shared memory may be written
-    if (warp == 0 && lane < nc) {
-      st_peer32(peer(&s.cmax[rank], lane), hi);
-      st_peer32(peer(&s.cmin[rank], lane), lo);
     }
   }
   sync();
@@ -327,54 +367,62 @@ __global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int n
       if (a.prob) a.prob[row] = 0.0f;
     }
     if (a.probs)
-      for (int64_t i = i0 + tid; i < i1; i += kT) a.probs[row * V + i] = 0.0f;
+      for (int64_t i = i0 + tid; i < i1; i += kT) __stcs(a.probs + row * V + i, 0.0f);
     return;
   }
   const float m = from_order(mx);
   const bool inf = isinf(m);  // then only the infinite logits have weight
-  const double c = 1.4426950408889634074 / static_cast<double>(T);
   Weigh weigh;
-  weigh.m = m;
-  weigh.ch = static_cast<float>(c);
-  weigh.cl = isinf(weigh.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(weigh.ch));
+  {
+    const double c = 1.4426950408889634074 / static_cast<double>(T);
+    weigh.m = m;
+    weigh.ch = static_cast<float>(c);
+    weigh.cl = isinf(weigh.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(weigh.ch));
+  }
   auto counted = [&](float l) { return inf ? l == m : l > -INFINITY; };
   auto weight = [&](float l) -> float { return counted(l) ? weigh(l) : 0.0f; };
   auto key64 = [&](float l, int64_t i) -> u64 {
     return (static_cast<u64>(order_bits(l)) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(i));
   };
+  // min_p as a bound on the logit: the smallest float not below m + T ln(min_p)
+  float bound = -INFINITY;
+  if (min_p > 0.0f) {
+    const double t = static_cast<double>(m) + (min_p < 1.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0);
+    bound = static_cast<float>(t);
+    if (static_cast<double>(bound) < t) bound = nextafterf(bound, INFINITY);
+  }
 
   // ---- the cut: tokens with key >= cut are kept
   u64 cut = 0ull;
   const bool use_k = k > 0 && k < V, use_p = top_p < 1.0f;
   if (use_k || use_p) {
+    // Distances at which a weight still counts for something: below 2^-(frac + 2) of the maximum's it
+    // rounds to no mass. The bins divide them (or the row's range where that is less).
+    float reach = __fmul_rn(T, 0.6931472f * static_cast<float>(frac + 2));
     const float range = inf ? 0.0f : __fsub_rn(m, from_order(mn));
-    float inv = __fdiv_rn(static_cast<float>(kBins), range);
-    if (!(inv <= 3.0e38f)) inv = 0.0f;  // no range, or none that fp32 holds: one bin
-    if (!(range <= 3.0e38f)) inv = 0.0f;
+    reach = range < reach ? range : reach;
+    float inv = __fdiv_rn(static_cast<float>(kBins), reach);
+    if (!(inv <= 3.0e38f) || !(reach <= 3.0e38f)) inv = 0.0f;  // nothing to divide, or not in fp32: one bin
+    auto live = [&](float l) { return counted(l) && (l == m || __fsub_rn(m, l) <= reach); };
     auto bin1 = [&](float l) -> int {
       if (l == m) return 0;
       const int b = static_cast<int>(__fmul_rn(__fsub_rn(m, l), inv));
       return b < kBins - 1 ? b : kBins - 1;
     };
-    // One histogram round over the elements that `in` selects: bins, cluster sum, and for the
-    // limit (entries, or mass) the bin that holds it.
-    auto histogram = [&](auto in, auto bin) {
-      for (int b = tid; b < kBins; b += kT) {
-        loc.mass[b] = 0ull;
-        loc.n[b] = 0u;
-      }
-      __syncthreads();
-      for (int64_t i = i0 + tid; i < i1; i += kT) {
-        const float l = value(i);
-        if (counted(l) && in(l, i)) {
-          const int b = bin(l, i);
+    // One histogram round over the elements that `in` selects: bins of entries (and, with_mass, of
+    // masses), summed over the cluster into `all`. loc is left zero.
+    auto histogram = [&](bool with_mass, auto in, auto bin) {
+      each(value, [&](float l, int64_t i) {
+        const bool on = in(l, i);
+        const int b = on ? bin(l, i) : -1;
+        // a whole warp in one bin (equal or far-away logits) adds once
+        if (__all_sync(0xffffffffu, b == __shfl_sync(0xffffffffu, b, 0))) {
+          if (on && lane == 0) atomicAdd(&loc.n[b], 32u);
+        } else if (on) {
           atomicAdd(&loc.n[b], 1u);
-          if (use_p) {
-            const u64 w = to_fixed(weight(l), frac);
-            if (w) atomicAdd(&loc.mass[b], w);
-          }
         }
-      }
+        if (with_mass && on) add64(reinterpret_cast<uint32_t*>(&loc.mass[b]), to_fixed(weigh(l), frac));
+      });
       sync();
       // every CTA sums one section of the bins over the cluster and hands it to all
       const int per = kBins / nc;
@@ -382,39 +430,44 @@ __global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int n
         u64 w = 0ull;
         uint32_t n = 0u;
         for (int r = 0; r < nc; ++r) {
-          w += nc > 1 ? ld_peer(peer(&loc.mass[b], r)) : loc.mass[b];
           n += nc > 1 ? ld_peer32(peer(&loc.n[b], r)) : loc.n[b];
+          if (with_mass) w += nc > 1 ? ld_peer(peer(&loc.mass[b], r)) : loc.mass[b];
         }
         for (int r = 0; r < nc; ++r) {
           if (nc > 1) {
-            st_peer(peer(&all.mass[b], r), w);
             st_peer32(peer(&all.n[b], r), n);
+            if (with_mass) st_peer(peer(&all.mass[b], r), w);
           } else {
-            all.mass[b] = w;
             all.n[b] = n;
+            all.mass[b] = w;
           }
         }
       }
       sync();
+      for (int b = tid; b < kBins; b += kT) {
+        loc.mass[b] = 0ull;
+        loc.n[b] = 0u;
+      }
     };
-    // The first bin at whose end the running count reaches lim_n (by_mass: the running mass reaches
-    // lim_m), given what precedes bin 0. Sets s.hit, s.before_n, s.before_m, s.hit_n.
+    // The first bin at whose end the running count (by_mass: the running mass) reaches lim, given what
+    // precedes bin 0. Sets s.hit (-1: none), s.before_n, s.before_m, s.hit_n.
     auto find = [&](bool by_mass, u64 lim, uint32_t base_n, u64 base_m) {
       constexpr int kPer = kBins / kT;
       u64 w[kPer], wt = 0ull;
       uint32_t n[kPer], nt = 0u;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        w[j] = all.mass[tid * kPer + j];
+        w[j] = by_mass ? all.mass[tid * kPer + j] : 0ull;
         n[j] = all.n[tid * kPer + j];
         wt += w[j];
         nt += n[j];
       }
       const u64 wi = warp_inclusive(wt, lane);
-      const u64 ni = warp_inclusive(nt, lane);
+      const uint32_t ni = static_cast<uint32_t>(warp_inclusive(nt, lane));
+      __syncthreads();
       if (lane == 31) {
         s.scan[warp] = wi;
-        s.scan_n[warp] = static_cast<uint32_t>(ni);
+        s.scan_n[warp] = ni;
       }
       if (tid == 0) s.hit = -1;
       __syncthreads();
@@ -438,42 +491,10 @@ __global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int n
       }
       __syncthreads();
     };
-    // The cut for a limit: the key of the entry at which the count (the mass) reaches it; returns the
-    // mass up to and with that entry. The histogram of round 1 is in `all`.
-    auto resolve = [&](bool by_mass, u64 lim, u64& cut_out) -> u64 {
-      find(by_mass, lim, 0u, 0ull);
-      const int b1 = s.hit;
-      if (b1 < 0) {  // the limit lies behind the last entry: all are kept
-        cut_out = 0ull;
-        return ~0ull;
-      }
-      u64 prefix = 0ull;  // bits of the key fixed so far (from the top)
-      int bits = 0;
-      uint32_t bn = s.before_n, n = s.hit_n;
-      u64 bm = s.before_m;
-      auto in_now = [&](float l, int64_t i) {
-        return bin1(l) == b1 && (bits == 0 || (key64(l, i) >> (64 - bits)) == prefix);
-      };
-      while (n > kGather && bits < 64) {
-        const int step = bits + 11 <= 64 ? 11 : 64 - bits;
-        const int sh = 64 - bits - step;
-        __syncthreads();
-        // a larger key comes first: bins by the complement of the digit
-        histogram(in_now, [&](float l, int64_t i) {
-          return static_cast<int>((1u << step) - 1u - (static_cast<uint32_t>(key64(l, i) >> sh) & ((1u << step) - 1u)));
-        });
-        find(by_mass, lim, bn, bm);
-        prefix = (prefix << step) | ((1u << step) - 1u - static_cast<uint32_t>(s.hit));
-        bits += step;
-        bn = s.before_n;
-        bm = s.before_m;
-        n = s.hit_n;
-      }
-      // gather the bin's entries at the leader, sort them, find the cut
-      __syncthreads();
-      for (int64_t i = i0 + tid; i < i1; i += kT) {
-        const float l = value(i);
-        if (counted(l) && in_now(l, i)) {
+    // The entries that `in` selects (n of them, at most kGather) to the first CTA's list.
+    auto gather = [&](auto in) {
+      each(value, [&](float l, int64_t i) {
+        if (in(l, i)) {
           if (nc > 1) {
             const uint32_t at = add_peer32(peer(&s.gathered, 0), 1u);
             st_peer(peer(&cand[at], 0), key64(l, i));
@@ -481,111 +502,247 @@ __global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int n
             cand[atomicAdd(&s.gathered, 1u)] = key64(l, i);
           }
         }
-      }
+      });
       sync();
-      if (rank == 0) {
-        int size = 32;
-        while (size < static_cast<int>(n)) size <<= 1;
-        for (int j = static_cast<int>(n) + tid; j < size; j += kT) cand[j] = 0ull;
-        __syncthreads();
-        for (int w = 2; w <= size; w <<= 1)  // bitonic, descending
-          for (int d = w >> 1; d > 0; d >>= 1) {
-            for (int t = tid; t < size / 2; t += kT) {
-              const int x = 2 * t - (t & (d - 1)), y = x + d;
-              const bool desc = (x & w) == 0;
-              const u64 ka = cand[x], kb = cand[y];
-              if ((ka < kb) == desc) {
-                cand[x] = kb;
-                cand[y] = ka;
-              }
-            }
-            __syncthreads();
-          }
-        // inclusive masses in order, two entries a thread
-        u64 w2[2] = {0ull, 0ull};
+    };
+    // (first CTA) the list sorted, descending, and its entries' running masses in `list_mass`, from `base`
+    u64* list_mass = all.mass;  // [kGather]; the histogram is not needed any more when this is used
+    auto sort_list = [&](int n, bool with_mass, u64 base_m) {
+      int size = 32;
+      while (size < n) size <<= 1;
+      for (int j = n + tid; j < size; j += kT) cand[j] = 0ull;
+      __syncthreads();
+      sort_desc(cand, size);
+      u64 w2[2] = {0ull, 0ull};  // two entries a thread
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (2 * tid + j < static_cast<int>(n))
-            w2[j] = use_p ? to_fixed(weight(from_order(static_cast<uint32_t>(cand[2 * tid + j] >> 32))), frac) : 0ull;
-        const u64 inc = warp_inclusive(w2[0] + w2[1], lane);
-        if (lane == 31) s.scan[warp] = inc;
-        __syncthreads();
-        u64 before = bm + inc - w2[0] - w2[1];
-        for (int q = 0; q < warp; ++q) before += s.scan[q];
+      for (int j = 0; j < 2; ++j)
+        if (with_mass && 2 * tid + j < n) w2[j] = to_fixed(weight(from_order(static_cast<uint32_t>(cand[2 * tid + j] >> 32))), frac);
+      const u64 inc = warp_inclusive(w2[0] + w2[1], lane);
+      if (lane == 31) s.scan[warp] = inc;
+      __syncthreads();
+      u64 before = base_m + inc - w2[0] - w2[1];
+      for (int q = 0; q < warp; ++q) before += s.scan[q];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        before += w2[j];
+        if (2 * tid + j < kGather) list_mass[2 * tid + j] = before;
+      }
+      __syncthreads();
+    };
+
+    const bool mass1 = !use_k;  // masses wait until the count shows that they are needed
+    histogram(mass1, [&](float l, int64_t) { return live(l); }, [&](float l, int64_t) { return bin1(l); });
+    if (use_k) {
+      find(false, static_cast<u64>(k), 0u, 0ull);
+      const int b1 = s.hit;
+      const uint32_t n = s.before_n + s.hit_n;
+      if (b1 >= 0 && n <= kGather) {
+        // ---- the whole row on one sorted list
+        if (a.probs)
+          for (int64_t i = i0 + tid; i < i1; i += kT) __stcs(a.probs + row * V + i, 0.0f);
+        gather([&](float l, int64_t) { return live(l) && bin1(l) <= b1; });
+        if (rank != 0) return;
+        sort_list(static_cast<int>(n), true, 0ull);
+        // kept: the first k; of those, preceding mass < top_p * theirs; of those, logit >= bound
+        const u64 lim = use_p ? scale_ceil(top_p, list_mass[k - 1]) : ~0ull;
+        int mine = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int e = 2 * tid + j;
-          if (e < static_cast<int>(n)) {
-            const u64 x0 = by_mass ? before : bn + static_cast<u64>(e), x1 = by_mass ? before + w2[j] : x0 + 1ull;
-            if (x0 < lim && x1 >= lim) {
-              s.cut = cand[e];
-              s.cut_mass = before + w2[j];
-            }
+          if (e < static_cast<int>(k))
+            mine += (e == 0 || list_mass[e - 1] < lim) && from_order(static_cast<uint32_t>(cand[e] >> 32)) >= bound ? 1 : 0;
+        }
+        mine = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)));
+        if (lane == 0) s.scan_n[warp] = static_cast<uint32_t>(mine);
+        __syncthreads();
+        int kept_n = 0;
+        for (int q = 0; q < kW; ++q) kept_n += static_cast<int>(s.scan_n[q]);
+        const u64 z = list_mass[kept_n - 1];
+        const float inv_z = static_cast<float>(exp2(static_cast<double>(frac)) / static_cast<double>(z));
+        __syncthreads();
+        // probabilities, and the kept entries in index order: sorted by (complement of the index, place)
+        int size = 32;
+        while (size < kept_n) size <<= 1;
+        u64* order = loc.mass;  // [kGather]
+        for (int e = tid; e < size; e += kT) {
+          u64 o = 0ull;
+          if (e < kept_n) {
+            const u64 key = cand[e];
+            if (a.probs)
+              a.probs[row * V + static_cast<int64_t>(~static_cast<uint32_t>(key))] =
+                  __fmul_rn(weight(from_order(static_cast<uint32_t>(key >> 32))), inv_z);
+            o = (static_cast<u64>(static_cast<uint32_t>(key)) << 32) | static_cast<uint32_t>(e);
+          }
+          order[e] = o;
+        }
+        if (!a.token && !a.prob) return;
+        __syncthreads();
+        sort_desc(order, size);
+        const u64 target = scale_floor(u, z);
+        u64 w2[2];
+        int place[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = 2 * tid + j;
+          place[j] = e < kept_n ? static_cast<int>(static_cast<uint32_t>(order[e])) : -1;
+          w2[j] = place[j] < 0 ? 0ull : list_mass[place[j]] - (place[j] > 0 ? list_mass[place[j] - 1] : 0ull);
+        }
+        const u64 inc = warp_inclusive(w2[0] + w2[1], lane);
+        if (lane == 31) s.scan[warp] = inc;
+        __syncthreads();
+        u64 before = inc - w2[0] - w2[1];
+        for (int q = 0; q < warp; ++q) before += s.scan[q];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (before <= target && target - before < w2[j]) {
+            const u64 key = cand[place[j]];
+            if (a.token) a.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(key));
+            if (a.prob) a.prob[row] = __fmul_rn(weight(from_order(static_cast<uint32_t>(key >> 32))), inv_z);
           }
           before += w2[j];
         }
+        return;
+      }
+    }
+    // ---- the general case. The cut for a limit: the key of the entry at which the count (the mass)
+    // reaches it; returns the mass up to and with that entry (use_p). `base` selects the elements that
+    // the bins in `all` (numbered by `bin0`) were made of.
+    auto resolve = [&](bool by_mass, u64 lim, bool binned, u64& cut_out) -> u64 {
+      u64 prefix = 0ull;  // bits of the key fixed so far (from the top)
+      int bits = 0, b1 = -1;
+      uint32_t bn = 0u, n = ~0u;
+      u64 bm = 0ull;
+      if (binned) {
+        find(by_mass, lim, 0u, 0ull);
+        if (s.hit < 0) return ~0ull;
+        b1 = s.hit;
+        bn = s.before_n;
+        n = s.hit_n;
+        bm = s.before_m;
+      }
+      auto in_now = [&](float l, int64_t i) {
+        return (b1 < 0 ? counted(l) : live(l) && bin1(l) == b1) && (bits == 0 || (key64(l, i) >> (64 - bits)) == prefix);
+      };
+      while (n > kGather && bits < 64) {
+        const int step = bits + 11 <= 64 ? 11 : 64 - bits;
+        const int sh = 64 - bits - step;
+        __syncthreads();
+        // a larger key comes first: bins by the complement of the digit
+        histogram(use_p, in_now, [&](float l, int64_t i) {
+          return static_cast<int>((1u << step) - 1u - (static_cast<uint32_t>(key64(l, i) >> sh) & ((1u << step) - 1u)));
+        });
+        // (find counts masses only by mass: the mass before a bin found by count is summed here)
+        find(by_mass, lim, bn, bm);
+        if (s.hit < 0) return ~0ull;  // fewer entries than the limit
+        if (use_p && !by_mass) {
+          u64 t = 0ull;
+          for (int b = tid; b < s.hit; b += kT) t += all.mass[b];
+          t = warp_sum(t);
+          __syncthreads();
+          if (lane == 0) s.scan[warp] = t;
+          __syncthreads();
+          for (int q = 0; q < kW; ++q) bm += s.scan[q];
+        } else {
+          bm = s.before_m;
+        }
+        prefix = (prefix << step) | ((1u << step) - 1u - static_cast<uint32_t>(s.hit));
+        bits += step;
+        bn = s.before_n;
+        n = s.hit_n;
+      }
+      __syncthreads();
+      gather(in_now);
+      if (rank == 0) {
+        sort_list(static_cast<int>(n), use_p, bm);
+        for (int e = tid; e < static_cast<int>(n); e += kT) {
+          const u64 before = e > 0 ? list_mass[e - 1] : bm;
+          const u64 x0 = by_mass ? before : bn + static_cast<u64>(e), x1 = by_mass ? list_mass[e] : x0 + 1ull;
+          if (x0 < lim && x1 >= lim) {
+            s.cut = cand[e];
+            s.cut_mass = list_mass[e];
+          }
+        }
         if (tid == 0) s.gathered = 0u;
         __syncthreads();
-        if (nc > 1 && tid < nc) {
-          const u64 cv = s.cut, cm = s.cut_mass;
-          if (tid > 0) {
-            st_peer(peer(&s.cut, tid), cv);
-            st_peer(peer(&s.cut_mass, tid), cm);
-          }
+        if (tid > 0 && tid < nc) {
+          st_peer(peer(&s.cut, tid), s.cut);
+          st_peer(peer(&s.cut_mass, tid), s.cut_mass);
         }
       }
       sync();
       cut_out = s.cut;
       return s.cut_mass;
     };
-
-    histogram([](float, int64_t) { return true; }, [&](float l, int64_t) { return bin1(l); });
-    u64 total = 0ull;  // mass of the tokens that top_k keeps
-    bool have_total = false;
+    const auto is_live = [&](float l, int64_t) { return live(l); };
+    const auto by_bin1 = [&](float l, int64_t) { return bin1(l); };
+    u64 total = ~0ull;  // mass of the tokens that top_k keeps (~0: all of them)
     if (use_k) {
-      total = resolve(false, static_cast<u64>(k), cut);
-      have_total = total != ~0ull;
+      if (use_p) {
+        __syncthreads();
+        histogram(true, is_live, by_bin1);
+        // the masses before the bin that the count finds
+        find(false, static_cast<u64>(k), 0u, 0ull);
+        if (s.hit >= 0) {
+          const int h = s.hit;
+          u64 t = 0ull;
+          for (int b = tid; b < h; b += kT) t += all.mass[b];
+          t = warp_sum(t);
+          __syncthreads();
+          if (lane == 0) s.scan[warp] = t;
+          __syncthreads();
+          u64 bm = 0ull;
+          for (int q = 0; q < kW; ++q) bm += s.scan[q];
+          total = bm;
+        }
+        const u64 mass_before = total;
+        const u64 got = resolve(false, static_cast<u64>(k), true, cut);
+        // (resolve's list starts at the bin: what precedes it is added here)
+        total = got == ~0ull ? ~0ull : got + mass_before;
+      } else {
+        (void)resolve(false, static_cast<u64>(k), true, cut);
+      }
+      // the k-th entry lies among those without mass: by the key's bits over the whole row (it changes
+      // which of them are kept, and no mass)
+      if (cut == 0ull) (void)resolve(false, static_cast<u64>(k), false, cut);
     }
     if (use_p) {
-      if (!have_total) {
-        u64 t = 0ull;
+      if (use_k) {
         __syncthreads();
+        histogram(true, is_live, by_bin1);
+      }
+      if (total == ~0ull) {
+        u64 t = 0ull;
         for (int b = tid; b < kBins; b += kT) t += all.mass[b];
         t = warp_sum(t);
+        __syncthreads();
         if (lane == 0) s.scan[warp] = t;
         __syncthreads();
         total = 0ull;
         for (int q = 0; q < kW; ++q) total += s.scan[q];
-        __syncthreads();
       }
       // kept: preceding mass < top_p * total, so the cut is where the running mass reaches it
       u64 lim = scale_ceil(top_p, total);
       if (lim == 0ull) lim = 1ull;  // the first token is always kept
       u64 cut_p = 0ull;
-      if (use_k && have_total) {
-        // the histogram of round 1 may have been overwritten by the refinement
-        histogram([](float, int64_t) { return true; }, [&](float l, int64_t) { return bin1(l); });
-      }
-      (void)resolve(true, lim, cut_p);
+      (void)resolve(true, lim, true, cut_p);
       cut = cut_p > cut ? cut_p : cut;
     }
   }
-  // min_p as a bound on the logit: the smallest float not below m + T ln(min_p)
-  float bound = -INFINITY;
-  if (min_p > 0.0f) {
-    const double t = static_cast<double>(m) + (min_p < 1.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0);
-    bound = static_cast<float>(t);
-    if (static_cast<double>(bound) < t) bound = nextafterf(bound, INFINITY);
-  }
-  auto kept = [&](float l, int64_t i) { return l >= bound && counted(l) && key64(l, i) >= cut; };
+  auto kept = [&](float l, int64_t i) { return l >= bound && counted(l) && (cut == 0ull || key64(l, i) >= cut); };
 
   // ---- masses of the kept tokens per warp segment, CTA and row
   u64 sum = 0ull;
-  for (int64_t j = i0 + warp * seg + lane; j < i0 + (warp + 1) * seg; j += 32)
-    if (j < i1) {
-      const float l = value(j);
-      if (kept(l, j)) sum += to_fixed(weight(l), frac);
+  {
+    const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
+    for (int64_t i = w0 + lane; i < w1; i += 32 * kBatch) {
+      float v[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) v[j] = i + 32 * j < w1 ? value(i + 32 * j) : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i + 32 * j < w1 && kept(v[j], i + 32 * j)) sum += to_fixed(weight(v[j]), frac);
     }
+  }
   sum = warp_sum(sum);
   if (lane == 0) s.wsum[warp] = sum;
   __syncthreads();
@@ -610,10 +767,9 @@ __global__ void __launch_bounds__(kT, 1) sample_kernel(const SampleArgs a, int n
              if (a.prob) a.prob[row] = __fmul_rn(weight(value(i)), inv_z);
            });
   if (a.probs)
-    for (int64_t i = i0 + tid; i < i1; i += kT) {
-      const float l = value(i);
-      a.probs[row * V + i] = kept(l, i) ? __fmul_rn(weight(l), inv_z) : 0.0f;
-    }
+    each(value, [&](float l, int64_t i) {
+      if (i < i1) __stcs(a.probs + row * V + i, kept(l, i) ? __fmul_rn(weight(l), inv_z) : 0.0f);
+    });
 }
 
 // ------------------------------------------------------------------------------- acceptance
@@ -680,17 +836,28 @@ __global__ void __launch_bounds__(kT, 1) verify_kernel(const VerifyArgs a, int n
   const float* q = !all && a.draft_probs ? a.draft_probs + (b * D + acc) * V : nullptr;
   auto prob01 = [](float v) { return v > 0.0f ? (v < 1.0f ? v : 1.0f) : 0.0f; };
   bool plain = false;  // the residual is empty: the target's own row
-  auto residual = [&](int64_t i) -> float {
-    const float pv = prob01(p[i]);
+  auto left_of = [&](float pv, float qv, int64_t i) -> float {
+    pv = prob01(pv);
     if (plain || all) return pv;
-    const float qv = q ? q[i] : (i == rejected_token ? 1.0f : 0.0f);
+    if (!q) qv = i == rejected_token ? 1.0f : 0.0f;
     return prob01(__fsub_rn(pv, prob01(qv)));
   };
+  auto residual = [&](int64_t i) -> float { return left_of(p[i], q ? q[i] : 0.0f, i); };
   u64 z = 0ull;
   for (int pass = 0; pass < 2; ++pass) {
     u64 sum = 0ull;
-    for (int64_t j = i0 + warp * seg + lane; j < i0 + (warp + 1) * seg; j += 32)
-      if (j < i1) sum += to_fixed(residual(j), frac);
+    constexpr int kBatch = 8;
+    const int64_t w1 = i0 + (warp + 1) * seg < i1 ? i0 + (warp + 1) * seg : i1;
+    for (int64_t i = i0 + warp * seg + lane; i < w1; i += 32 * kBatch) {
+      float pv[kBatch], qv[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        pv[j] = i + 32 * j < w1 ? __ldg(p + i + 32 * j) : 0.0f;
+        qv[j] = q && i + 32 * j < w1 ? __ldg(q + i + 32 * j) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) sum += to_fixed(left_of(pv[j], qv[j], i + 32 * j), frac);
+    }
     sum = warp_sum(sum);
     if (lane == 0) s.wsum[warp] = sum;
     __syncthreads();
@@ -781,10 +948,12 @@ int mass_bits(int64_t V) {
   return 62 - lg;
 }
 
-// CTAs per row: as many as keep every SM busy (up to kMaxC), and no more than give each warp a step.
+// CTAs per row: as many (a power of two, up to kMaxC) as about fill the SMs, and no more than give each
+// warp a step.
 int cluster_size(int64_t rows, int64_t V, int sm_count) {
   int nc = 1;
-  while (nc < kMaxC && rows * nc * 2 <= sm_count && V > static_cast<int64_t>(nc) * 2 * kSliceUnit) nc *= 2;
+  while (nc < kMaxC && rows * nc * 20 <= static_cast<int64_t>(sm_count) * 11 && V > static_cast<int64_t>(nc) * 2 * kSliceUnit)
+    nc *= 2;
   return nc;
 }
 
@@ -796,10 +965,11 @@ cudaError_t launch_sample(const SampleArgs& in, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   SampleArgs a = in;
   int nc = cluster_size(a.R, a.V, di.sm_count);
-  const size_t room = static_cast<size_t>(di.smem_optin) - kFixedSmem;
-  while (nc < kMaxC && static_cast<size_t>(slice_of(a.V, nc)) * 4 > room) nc *= 2;
   int64_t slice = slice_of(a.V, nc);
-  const bool res = static_cast<size_t>(slice) * 4 <= room;
+  // A slice is kept in shared memory where that leaves room for as many CTAs per SM as there are to run.
+  const size_t all_of_it = static_cast<size_t>(di.smem_optin);
+  const size_t limit = static_cast<int64_t>(a.R) * nc <= di.sm_count ? all_of_it : (all_of_it - 2048) / 2;
+  const bool res = kFixedSmem + static_cast<size_t>(slice) * 4 <= limit;
   int frac = mass_bits(a.V);
   const void* kern = a.bf16 ? (res ? reinterpret_cast<const void*>(sample_kernel<true, true>)
                                    : reinterpret_cast<const void*>(sample_kernel<true, false>))
