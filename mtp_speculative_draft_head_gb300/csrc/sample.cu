@@ -8,13 +8,16 @@
 // exceeds u times the whole.
 //
 // No sort of the row: a prefix is { i : key_i >= cut } for one 64-bit key (the logit's order bits,
-// then the complement of the index), and the cut is found by histograms. Round 1 bins the row by
-// its distance from the maximum, linearly over the distances at which a weight is more than nothing
-// (2048 bins; entries further down, masked ones among them, are left out of it). With a top_k whose
-// bin ends within kGather entries -- the usual case -- these are gathered and sorted by one CTA, which
-// finishes the row on the sorted list: no weight is formed for any other entry. Otherwise the bins
-// carry masses too; the bin that holds the cut is gathered and sorted when it has at most kGather
-// entries, and split by the key's bits, 11 at a time, until it has.
+// then the complement of the index). Two ways to the cut:
+//  * top_k up to half the cluster's threads (the usual case): the k-th largest of the threads' own maxima
+//    is a bound that the k-th largest logit cannot be below, and little more than k entries reach it.
+//    These are gathered and sorted by one CTA, which finishes the row on the sorted list: no weight is
+//    formed for any other entry, and shared-memory atomics (~50 cycles for a warp's worth, the cost
+//    of a histogram of the whole row) are spent on one entry per thread.
+//  * otherwise by a histogram of the row's masses (or entries) over the distance from the maximum, in 2048
+//    bins over the distances at which a weight is more than nothing (entries further down, masked ones
+//    among them, are left out of it). The bin that holds the cut is gathered and sorted when it has at
+//    most kGather entries, and split by the key's bits, 11 at a time, until it has.
 //
 // Masses are 64-bit fixed-point numbers (2^62 / 2^ceil(log2 V) for a weight of one), so sums do not
 // depend on the order of the atomics or of the threads: the same inputs give the same token
@@ -162,12 +165,13 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 struct Weigh {
   float m, ch, cl;
   __device__ __forceinline__ float operator()(float l) const {
-    if (l == m) return 1.0f;
     float dh, dl;
     two_sum(m, -l, dh, dl);
-    const float th = __fmul_rn(dh, ch);
-    if (!(th < 120.0f)) return 0.0f;  // below 2^-120 of the maximum's weight (NaN: an infinite distance)
-    const float tl = __fmaf_rn(dh, ch, -th) + __fmaf_rn(dh, cl, __fmul_rn(dl, ch));
+    float th = __fmul_rn(dh, ch);
+    float tl = __fmaf_rn(dh, ch, -th) + __fmaf_rn(dh, cl, __fmul_rn(dl, ch));
+    const bool tiny = !(th < 120.0f);  // below 2^-120 of the maximum's weight (NaN: an infinite distance)
+    th = tiny ? 0.0f : th;
+    tl = tiny ? 0.0f : tl;
     const float n = rintf(th);
     const float f = -((th - n) + tl);
     const float y = f * 0.69314718055994530942f;
@@ -179,7 +183,8 @@ struct Weigh {
     p = __fmaf_rn(p, y, 0.5f);
     p = __fmaf_rn(p, y, 1.0f);
     p = __fmaf_rn(p, y, 1.0f);
-    return __uint_as_float(__float_as_uint(p) - (static_cast<uint32_t>(static_cast<int>(n)) << 23));
+    const float w = __uint_as_float(__float_as_uint(p) - (static_cast<uint32_t>(static_cast<int>(n)) << 23));
+    return l == m ? 1.0f : (tiny ? 0.0f : w);
   }
 };
 
@@ -196,8 +201,13 @@ struct Shared {
   int hit;
   uint32_t before_n, hit_n;
   u64 before_m;
-  uint32_t gathered;       // leader: candidates received
-  u64 cut, cut_mass;       // published by the leader
+  uint32_t gathered;       // first CTA: candidates received
+  uint32_t found;          // this CTA's candidates
+  uint32_t counts[kMaxC];  // every CTA's candidates (pushed by its peers)
+  u64 cut, cut_mass;       // published by the first CTA
+  double log2e_t;          // log2(e) / T
+  double t_ln_min_p;       // T ln(min_p)
+  float inv_z;
 };
 // Dynamic shared memory: Shared, the local histogram (u64 mass, u32 count), the cluster's, the
 // gather buffer, then the slice.
@@ -212,7 +222,8 @@ struct Hist {
 // ------------------------------------------------------------------------------- inverse of the cdf
 // The lowest index of the row whose cumulative mass exceeds floor(u z). Every warp owns `seg`
 // consecutive elements (a multiple of 32) of the slice that starts at i0; s.wsum holds this CTA's
-// per-warp masses, s.cta every CTA's. The one warp that finds it calls found(index).
+// per-warp masses, s.cta every CTA's. The one warp that finds it calls found(index). It passes over
+// its elements 128 at a time, and looks closer at the 128 that hold the target.
 template <class MassFn, class Found>
 __device__ void locate(const Shared& s, uint32_t rank, u64 target, int64_t i0, int64_t seg, int64_t n, MassFn mass,
                        Found found) {
@@ -221,21 +232,32 @@ __device__ void locate(const Shared& s, uint32_t rank, u64 target, int64_t i0, i
   for (uint32_t r = 0; r < rank; ++r) before += s.cta[r];
   for (int w = 0; w < warp; ++w) before += s.wsum[w];
   if (target < before || target - before >= s.wsum[warp]) return;
-  for (int64_t j = i0 + warp * seg; j < i0 + (warp + 1) * seg; j += 32) {
-    const int64_t i = j + lane;
-    const u64 m = i < n ? mass(i) : 0ull;
-    const u64 c = warp_inclusive(m, lane);
-    const uint32_t hit = __ballot_sync(0xffffffffu, before + c > target);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) found(i);
-      return;
+  const int64_t end = i0 + (warp + 1) * seg < n ? i0 + (warp + 1) * seg : n;
+  for (int64_t j = i0 + warp * seg; j < end; j += 128) {
+    u64 m[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m[q] = j + 32 * q + lane < end ? mass(j + 32 * q + lane) : 0ull;
+    const u64 all = warp_sum(m[0] + m[1] + m[2] + m[3]);
+    if (before + all <= target) {
+      before += all;
+      continue;
     }
-    before += __shfl_sync(0xffffffffu, c, 31);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const u64 c = warp_inclusive(m[q], lane);
+      const uint32_t hit = __ballot_sync(0xffffffffu, before + c > target);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) found(j + 32 * q + lane);
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, c, 31);
+    }
   }
 }
 
 // ------------------------------------------------------------------------------- sampler
-// Bitonic sort, descending, of `size` (a power of two) 64-bit keys by the whole block.
+// Bitonic sort, descending, of `size` (a power of two, at least 32) 64-bit keys by the whole block. A
+// step of distance up to 32 stays within the 64 keys of one warp's lanes.
 __device__ void sort_desc(u64* key, int size) {
   for (int w = 2; w <= size; w <<= 1)
     for (int d = w >> 1; d > 0; d >>= 1) {
@@ -247,8 +269,11 @@ __device__ void sort_desc(u64* key, int size) {
           key[y] = ka;
         }
       }
-      __syncthreads();
+      // the next step is (w, d / 2), or (2 w, w)
+      if ((d > 1 ? d >> 1 : w) > 32) __syncthreads();
+      else __syncwarp();
     }
+  __syncthreads();
 }
 
 template <bool BF16, bool RES>
@@ -279,7 +304,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     loc.mass[b] = 0ull;
     loc.n[b] = 0u;
   }
-  if (tid == 0) s.gathered = 0u;
+  if (tid == 0) s.gathered = s.found = 0u;
   pdl_wait_prior_grid();
 
   // ---- the row's parameters
@@ -320,6 +345,22 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     }
   };
 
+  // this CTA's slice of probs, zeros: 16 bytes at a time between ragged ends
+  auto zero_row = [&] {
+    float* dst = a.probs + row * V;
+    int64_t b = i0, e = i1;
+    if (b >= e) return;
+    while (b < e && (reinterpret_cast<uintptr_t>(dst + b) & 15u) != 0) ++b;
+    const int64_t q = (e - b) / 4;
+    for (int64_t i = i0 + tid; i < b; i += kT) dst[i] = 0.0f;
+    for (int64_t i = tid; i < q; i += kT) __stcs(reinterpret_cast<float4*>(dst + b) + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    for (int64_t i = b + 4 * q + tid; i < e; i += kT) dst[i] = 0.0f;
+  };
+  // 2^frac / z, for one thread
+  auto inverse = [frac](u64 z) {
+    return static_cast<float>(__longlong_as_double(static_cast<long long>(1023 + frac) << 52) / static_cast<double>(z));
+  };
+
   // ---- pass 1: the slice into shared memory, its largest and smallest finite-or-+inf logit
   uint32_t hi = 0u, lo = 0xFFFFFFFFu;  // order bits; 0 is below -inf
   const uint32_t kNegInf = order_bits(-INFINITY);
@@ -331,6 +372,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       lo = o < lo ? o : lo;
     }
   });
+  const uint32_t own = hi;  // this thread's largest
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
   if (lane == 0) {
@@ -351,6 +393,11 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         s.cmin[0] = lo;
       }
     }
+  } else if (lane == 0) {
+    // fp64 is slow here: one thread each, under the exchange of the maxima (by all threads, the division
+    // and the logarithm cost 4,000 and 15,000 cycles)
+    if (warp == 1) s.log2e_t = 1.4426950408889634074 / static_cast<double>(T);
+    if (warp == 2) s.t_ln_min_p = min_p > 0.0f && min_p < 1.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0;
   }
   sync();
   uint32_t mx = 0u, mn = 0xFFFFFFFFu;
@@ -366,15 +413,14 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       if (a.token) a.token[row] = -1;
       if (a.prob) a.prob[row] = 0.0f;
     }
-    if (a.probs)
-      for (int64_t i = i0 + tid; i < i1; i += kT) __stcs(a.probs + row * V + i, 0.0f);
+    if (a.probs) zero_row();
     return;
   }
   const float m = from_order(mx);
   const bool inf = isinf(m);  // then only the infinite logits have weight
   Weigh weigh;
   {
-    const double c = 1.4426950408889634074 / static_cast<double>(T);
+    const double c = s.log2e_t;
     weigh.m = m;
     weigh.ch = static_cast<float>(c);
     weigh.cl = isinf(weigh.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(weigh.ch));
@@ -387,7 +433,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   // min_p as a bound on the logit: the smallest float not below m + T ln(min_p)
   float bound = -INFINITY;
   if (min_p > 0.0f) {
-    const double t = static_cast<double>(m) + (min_p < 1.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0);
+    const double t = static_cast<double>(m) + s.t_ln_min_p;
     bound = static_cast<float>(t);
     if (static_cast<double>(bound) < t) bound = nextafterf(bound, INFINITY);
   }
@@ -409,22 +455,10 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       const int b = static_cast<int>(__fmul_rn(__fsub_rn(m, l), inv));
       return b < kBins - 1 ? b : kBins - 1;
     };
-    // One histogram round over the elements that `in` selects: bins of entries (and, with_mass, of
-    // masses), summed over the cluster into `all`. loc is left zero.
-    auto histogram = [&](bool with_mass, auto in, auto bin) {
-      each(value, [&](float l, int64_t i) {
-        const bool on = in(l, i);
-        const int b = on ? bin(l, i) : -1;
-        // a whole warp in one bin (equal or far-away logits) adds once
-        if (__all_sync(0xffffffffu, b == __shfl_sync(0xffffffffu, b, 0))) {
-          if (on && lane == 0) atomicAdd(&loc.n[b], 32u);
-        } else if (on) {
-          atomicAdd(&loc.n[b], 1u);
-        }
-        if (with_mass && on) add64(reinterpret_cast<uint32_t*>(&loc.mass[b]), to_fixed(weigh(l), frac));
-      });
+    // The bins of loc summed over the cluster into `all` on every CTA (each sums one section and hands it
+    // on); loc is left zero.
+    auto share_bins = [&](bool with_mass) {
       sync();
-      // every CTA sums one section of the bins over the cluster and hands it to all
       const int per = kBins / nc;
       for (int b = rank * per + tid; b < static_cast<int>(rank + 1) * per; b += kT) {
         u64 w = 0ull;
@@ -449,6 +483,22 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         loc.n[b] = 0u;
       }
     };
+    // One histogram round over the elements that `in` selects, of entries and / or of masses.
+    auto histogram = [&](bool with_n, bool with_mass, auto in, auto bin) {
+      each(value, [&](float l, int64_t i) {
+        const bool on = in(l, i);
+        const int b = on ? bin(l, i) : -1;
+        if (with_n) {  // a whole warp in one bin (equal or far-away logits) adds once
+          if (__all_sync(0xffffffffu, b == __shfl_sync(0xffffffffu, b, 0))) {
+            if (on && lane == 0) atomicAdd(&loc.n[b], 32u);
+          } else if (on) {
+            atomicAdd(&loc.n[b], 1u);
+          }
+        }
+        if (with_mass && on) add64(reinterpret_cast<uint32_t*>(&loc.mass[b]), to_fixed(weigh(l), frac));
+      });
+      share_bins(with_mass);
+    };
     // The first bin at whose end the running count (by_mass: the running mass) reaches lim, given what
     // precedes bin 0. Sets s.hit (-1: none), s.before_n, s.before_m, s.hit_n.
     auto find = [&](bool by_mass, u64 lim, uint32_t base_n, u64 base_m) {
@@ -457,7 +507,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       uint32_t n[kPer], nt = 0u;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        w[j] = by_mass ? all.mass[tid * kPer + j] : 0ull;
+        w[j] = all.mass[tid * kPer + j];
         n[j] = all.n[tid * kPer + j];
         wt += w[j];
         nt += n[j];
@@ -491,19 +541,32 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       }
       __syncthreads();
     };
-    // The entries that `in` selects (n of them, at most kGather) to the first CTA's list.
-    auto gather = [&](auto in) {
+    // The entries that `in` selects to the first CTA's list (the first kGather that come); returns how many
+    // there are, on every CTA.
+    auto gather = [&](auto in) -> int {
+      uint32_t mine = 0u;
       each(value, [&](float l, int64_t i) {
         if (in(l, i)) {
-          if (nc > 1) {
-            const uint32_t at = add_peer32(peer(&s.gathered, 0), 1u);
-            st_peer(peer(&cand[at], 0), key64(l, i));
-          } else {
-            cand[atomicAdd(&s.gathered, 1u)] = key64(l, i);
+          ++mine;
+          const uint32_t at = nc > 1 ? add_peer32(peer(&s.gathered, 0), 1u) : atomicAdd(&s.gathered, 1u);
+          if (at < kGather) {
+            if (nc > 1) st_peer(peer(&cand[at], 0), key64(l, i));
+            else cand[at] = key64(l, i);
           }
         }
       });
+      mine = __reduce_add_sync(0xffffffffu, mine);
+      if (lane == 0 && mine) atomicAdd(&s.found, mine);
+      __syncthreads();
+      if (tid < nc) {
+        if (nc > 1) st_peer32(peer(&s.counts[rank], tid), s.found);
+        else s.counts[0] = s.found;
+      }
       sync();
+      uint32_t n = 0u;
+      for (int r = 0; r < nc; ++r) n += s.counts[r];
+      if (tid == 0) s.gathered = s.found = 0u;  // (before the next barrier, ahead of the next list)
+      return static_cast<int>(n < 0x7FFFFFFFu ? n : 0x7FFFFFFFu);
     };
     // (first CTA) the list sorted, descending, and its entries' running masses in `list_mass`, from `base`
     u64* list_mass = all.mass;  // [kGather]; the histogram is not needed any more when this is used
@@ -530,19 +593,20 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       __syncthreads();
     };
 
-    const bool mass1 = !use_k;  // masses wait until the count shows that they are needed
-    histogram(mass1, [&](float l, int64_t) { return live(l); }, [&](float l, int64_t) { return bin1(l); });
-    if (use_k) {
+    if (use_k && 2 * k <= static_cast<int64_t>(nc) * kT) {
+      // ---- the whole row on one sorted list: the bins of the threads' maxima first
+      {
+        const float l = own == 0u ? -INFINITY : from_order(own);
+        if (live(l)) atomicAdd(&loc.n[bin1(l)], 1u);
+      }
+      share_bins(false);
       find(false, static_cast<u64>(k), 0u, 0ull);
       const int b1 = s.hit;
-      const uint32_t n = s.before_n + s.hit_n;
-      if (b1 >= 0 && n <= kGather) {
-        // ---- the whole row on one sorted list
-        if (a.probs)
-          for (int64_t i = i0 + tid; i < i1; i += kT) __stcs(a.probs + row * V + i, 0.0f);
-        gather([&](float l, int64_t) { return live(l) && bin1(l) <= b1; });
+      if (a.probs) zero_row();  // (the first CTA's own stores come after the gather's barrier)
+      const int n = b1 < 0 ? kGather + 1 : gather([&](float l, int64_t) { return live(l) && bin1(l) <= b1; });
+      if (n <= kGather) {
         if (rank != 0) return;
-        sort_list(static_cast<int>(n), true, 0ull);
+        sort_list(n, true, 0ull);
         // kept: the first k; of those, preceding mass < top_p * theirs; of those, logit >= bound
         const u64 lim = use_p ? scale_ceil(top_p, list_mass[k - 1]) : ~0ull;
         int mine = 0;
@@ -558,8 +622,9 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         int kept_n = 0;
         for (int q = 0; q < kW; ++q) kept_n += static_cast<int>(s.scan_n[q]);
         const u64 z = list_mass[kept_n - 1];
-        const float inv_z = static_cast<float>(exp2(static_cast<double>(frac)) / static_cast<double>(z));
+        if (tid == 0) s.inv_z = inverse(z);
         __syncthreads();
+        const float inv_z = s.inv_z;
         // probabilities, and the kept entries in index order: sorted by (complement of the index, place)
         int size = 32;
         while (size < kept_n) size <<= 1;
@@ -605,56 +670,44 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       }
     }
     // ---- the general case. The cut for a limit: the key of the entry at which the count (the mass)
-    // reaches it; returns the mass up to and with that entry (use_p). `base` selects the elements that
-    // the bins in `all` (numbered by `bin0`) were made of.
+    // reaches it; returns the mass up to and with that entry (when masses are kept: use_p). binned: `all`
+    // holds the live entries by bin1; otherwise all entries count, from the key's first bits on.
     auto resolve = [&](bool by_mass, u64 lim, bool binned, u64& cut_out) -> u64 {
       u64 prefix = 0ull;  // bits of the key fixed so far (from the top)
       int bits = 0, b1 = -1;
-      uint32_t bn = 0u, n = ~0u;
+      uint32_t bn = 0u;
       u64 bm = 0ull;
+      auto in_now = [&](float l, int64_t i) {
+        return (b1 < 0 ? counted(l) : live(l) && bin1(l) == b1) && (bits == 0 || (key64(l, i) >> (64 - bits)) == prefix);
+      };
+      int n = kGather + 1;
       if (binned) {
         find(by_mass, lim, 0u, 0ull);
         if (s.hit < 0) return ~0ull;
         b1 = s.hit;
         bn = s.before_n;
-        n = s.hit_n;
         bm = s.before_m;
+        n = gather(in_now);
       }
-      auto in_now = [&](float l, int64_t i) {
-        return (b1 < 0 ? counted(l) : live(l) && bin1(l) == b1) && (bits == 0 || (key64(l, i) >> (64 - bits)) == prefix);
-      };
-      while (n > kGather && bits < 64) {
+      while (n > kGather) {
         const int step = bits + 11 <= 64 ? 11 : 64 - bits;
         const int sh = 64 - bits - step;
         __syncthreads();
         // a larger key comes first: bins by the complement of the digit
-        histogram(use_p, in_now, [&](float l, int64_t i) {
+        histogram(true, use_p, in_now, [&](float l, int64_t i) {
           return static_cast<int>((1u << step) - 1u - (static_cast<uint32_t>(key64(l, i) >> sh) & ((1u << step) - 1u)));
         });
-        // (find counts masses only by mass: the mass before a bin found by count is summed here)
         find(by_mass, lim, bn, bm);
         if (s.hit < 0) return ~0ull;  // fewer entries than the limit
-        if (use_p && !by_mass) {
-          u64 t = 0ull;
-          for (int b = tid; b < s.hit; b += kT) t += all.mass[b];
-          t = warp_sum(t);
-          __syncthreads();
-          if (lane == 0) s.scan[warp] = t;
-          __syncthreads();
-          for (int q = 0; q < kW; ++q) bm += s.scan[q];
-        } else {
-          bm = s.before_m;
-        }
         prefix = (prefix << step) | ((1u << step) - 1u - static_cast<uint32_t>(s.hit));
         bits += step;
         bn = s.before_n;
-        n = s.hit_n;
+        bm = s.before_m;
+        n = gather(in_now);
       }
-      __syncthreads();
-      gather(in_now);
       if (rank == 0) {
-        sort_list(static_cast<int>(n), use_p, bm);
-        for (int e = tid; e < static_cast<int>(n); e += kT) {
+        sort_list(n, use_p, bm);
+        for (int e = tid; e < n; e += kT) {
           const u64 before = e > 0 ? list_mass[e - 1] : bm;
           const u64 x0 = by_mass ? before : bn + static_cast<u64>(e), x1 = by_mass ? list_mass[e] : x0 + 1ull;
           if (x0 < lim && x1 >= lim) {
@@ -662,7 +715,6 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
             s.cut_mass = list_mass[e];
           }
         }
-        if (tid == 0) s.gathered = 0u;
         __syncthreads();
         if (tid > 0 && tid < nc) {
           st_peer(peer(&s.cut, tid), s.cut);
@@ -677,44 +729,20 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     const auto by_bin1 = [&](float l, int64_t) { return bin1(l); };
     u64 total = ~0ull;  // mass of the tokens that top_k keeps (~0: all of them)
     if (use_k) {
-      if (use_p) {
-        __syncthreads();
-        histogram(true, is_live, by_bin1);
-        // the masses before the bin that the count finds
-        find(false, static_cast<u64>(k), 0u, 0ull);
-        if (s.hit >= 0) {
-          const int h = s.hit;
-          u64 t = 0ull;
-          for (int b = tid; b < h; b += kT) t += all.mass[b];
-          t = warp_sum(t);
-          __syncthreads();
-          if (lane == 0) s.scan[warp] = t;
-          __syncthreads();
-          u64 bm = 0ull;
-          for (int q = 0; q < kW; ++q) bm += s.scan[q];
-          total = bm;
-        }
-        const u64 mass_before = total;
-        const u64 got = resolve(false, static_cast<u64>(k), true, cut);
-        // (resolve's list starts at the bin: what precedes it is added here)
-        total = got == ~0ull ? ~0ull : got + mass_before;
-      } else {
-        (void)resolve(false, static_cast<u64>(k), true, cut);
-      }
-      // the k-th entry lies among those without mass: by the key's bits over the whole row (it changes
+      __syncthreads();
+      histogram(true, use_p, is_live, by_bin1);
+      total = resolve(false, static_cast<u64>(k), true, cut);
+      // the k-th entry may lie among those without mass: by the key's bits over the whole row (it changes
       // which of them are kept, and no mass)
       if (cut == 0ull) (void)resolve(false, static_cast<u64>(k), false, cut);
     }
     if (use_p) {
-      if (use_k) {
-        __syncthreads();
-        histogram(true, is_live, by_bin1);
-      }
+      __syncthreads();
+      histogram(false, true, is_live, by_bin1);
       if (total == ~0ull) {
         u64 t = 0ull;
         for (int b = tid; b < kBins; b += kT) t += all.mass[b];
         t = warp_sum(t);
-        __syncthreads();
         if (lane == 0) s.scan[warp] = t;
         __syncthreads();
         total = 0ull;
@@ -740,7 +768,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       for (int j = 0; j < kBatch; ++j) v[j] = i + 32 * j < w1 ? value(i + 32 * j) : -INFINITY;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        if (i + 32 * j < w1 && kept(v[j], i + 32 * j)) sum += to_fixed(weight(v[j]), frac);
+        sum += kept(v[j], i + 32 * j) ? to_fixed(weigh(v[j]), frac) : 0ull;  // (-inf past the end: not kept)
     }
   }
   sum = warp_sum(sum);
@@ -755,7 +783,9 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   sync();  // the last exchange: after it every CTA reads its own shared memory only
   u64 z = 0ull;
   for (int r = 0; r < nc; ++r) z += s.cta[r];
-  const float inv_z = static_cast<float>(exp2(static_cast<double>(frac)) / static_cast<double>(z));
+  if (tid == 0) s.inv_z = inverse(z);
+  __syncthreads();
+  const float inv_z = s.inv_z;
   if (a.token || a.prob)
     locate(s, rank, scale_floor(u, z), i0, seg, i1,
            [&](int64_t i) {
@@ -778,7 +808,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
 // token after the a accepted ones comes from max(p_a - q_a, 0), or from p_n when all are accepted,
 // by inversion with u_D. Emitted tokens are then distributed as the target's. Bound by the read of
 // one row of p and one of q per sequence.
-__global__ void __launch_bounds__(kT, 1) verify_kernel(const VerifyArgs a, int nc, int64_t slice, int frac) {
+__global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int nc, int64_t slice, int frac) {
   __shared__ Shared s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = nc > 1 ? cluster_rank() : 0u;
@@ -893,7 +923,8 @@ __global__ void __launch_bounds__(kT, 1) verify_kernel(const VerifyArgs a, int n
            [&](int64_t i) {
              a.tokens[b * (D + 1) + acc] = static_cast<int32_t>(i);
              if (a.prob)
-               a.prob[b] = static_cast<float>(static_cast<double>(residual(i)) * exp2(static_cast<double>(frac)) /
+               a.prob[b] = static_cast<float>(static_cast<double>(residual(i)) *
+                                              __longlong_as_double(static_cast<long long>(1023 + frac) << 52) /
                                               static_cast<double>(z));
            });
 }
@@ -948,12 +979,11 @@ int mass_bits(int64_t V) {
   return 62 - lg;
 }
 
-// CTAs per row: as many (a power of two, up to kMaxC) as about fill the SMs, and no more than give each
-// warp a step.
+// CTAs per row: as many (a power of two, up to kMaxC) as two CTAs on every SM allow, and no more than
+// give each warp a step.
 int cluster_size(int64_t rows, int64_t V, int sm_count) {
   int nc = 1;
-  while (nc < kMaxC && rows * nc * 20 <= static_cast<int64_t>(sm_count) * 11 && V > static_cast<int64_t>(nc) * 2 * kSliceUnit)
-    nc *= 2;
+  while (nc < kMaxC && rows * nc <= sm_count && V > static_cast<int64_t>(nc) * 2 * kSliceUnit) nc *= 2;
   return nc;
 }
 
