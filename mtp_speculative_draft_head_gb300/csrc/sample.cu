@@ -46,7 +46,7 @@ constexpr int kW = kT / 32;
 constexpr int kMaxC = 16;         // CTAs per cluster
 constexpr int kBins = 2048;
 constexpr int kGather = 1024;     // candidates sorted at once
-constexpr int kSliceUnit = kT;    // a slice is a multiple of this: every warp owns whole 32-element steps
+constexpr int kSliceUnit = 4 * kT;  // a slice is a multiple of this: every warp owns whole steps of 128 elements
 
 typedef unsigned long long u64;
 
@@ -205,8 +205,8 @@ struct Shared {
   uint32_t found;          // this CTA's candidates
   uint32_t counts[kMaxC];  // every CTA's candidates (pushed by its peers)
   u64 cut, cut_mass;       // published by the first CTA
-  double log2e_t;          // log2(e) / T
-  double t_ln_min_p;       // T ln(min_p)
+  float ch, cl;            // log2(e) / T as a double-float
+  float bh, bl;            // T ln(min_p) as a double-float
   float inv_z;
 };
 // Dynamic shared memory: Shared, the local histogram (u64 mass, u32 count), the cluster's, the
@@ -256,12 +256,38 @@ __device__ void locate(const Shared& s, uint32_t rank, u64 target, int64_t i0, i
 }
 
 // ------------------------------------------------------------------------------- sampler
-// Bitonic sort, descending, of `size` (a power of two, at least 32) 64-bit keys by the whole block. A
-// step of distance up to 32 stays within the 64 keys of one warp's lanes.
+// Bitonic sort, descending, of `size` (a power of two, 32 to kGather) 64-bit keys by the whole block. Up to
+// kT keys sit one to a thread: a step of distance below 32 is a shuffle, the others (10 of 45 at 512)
+// go through shared memory. More sort in shared memory, where steps of distance up to 32 stay within
+// the 64 keys of one warp's lanes.
 __device__ void sort_desc(u64* key, int size) {
+  const int tid = threadIdx.x;
+  if (size <= kT) {
+    const bool warp_on = (tid & ~31) < size;
+    u64 k = warp_on ? key[tid] : 0ull;
+    for (int w = 2; w <= size; w <<= 1)
+      for (int d = w >> 1; d > 0; d >>= 1) {
+        u64 o = 0ull;
+        if (d >= 32) {
+          __syncthreads();
+          if (warp_on) key[tid] = k;
+          __syncthreads();
+          if (warp_on) o = key[tid ^ d];
+        } else if (warp_on) {
+          o = __shfl_xor_sync(0xffffffffu, k, d);
+        }
+        // the lower place of a descending run keeps the larger key
+        const bool larger = ((tid & w) == 0) == ((tid & d) == 0);
+        k = (o > k) == larger ? o : k;
+      }
+    __syncthreads();
+    if (warp_on) key[tid] = k;
+    __syncthreads();
+    return;
+  }
   for (int w = 2; w <= size; w <<= 1)
     for (int d = w >> 1; d > 0; d >>= 1) {
-      for (int t = threadIdx.x; t < size / 2; t += kT) {
+      for (int t = tid; t < size / 2; t += kT) {
         const int x = 2 * t - (t & (d - 1)), y = x + d;
         const u64 ka = key[x], kb = key[y];
         if ((ka < kb) == ((x & w) == 0)) {
@@ -321,28 +347,55 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   }
 
   const char* base = static_cast<const char*>(a.logits) + row * a.ld * (BF16 ? 2 : 4);
+  auto number = [](float v) { return v == v ? v : -INFINITY; };  // NaN never wins
   auto raw = [&](int64_t i) -> float {
-    float v;
-    if constexpr (BF16) v = bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(base) + i));
-    else v = __ldg(reinterpret_cast<const float*>(base) + i);
-    return v == v ? v : -INFINITY;  // NaN never wins
+    if constexpr (BF16) return number(bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(base) + i)));
+    else return number(__ldg(reinterpret_cast<const float*>(base) + i));
+  };
+  // four elements at i (a multiple of 4 from i0): one load where the row is aligned and has them all
+  const bool wide = (reinterpret_cast<uintptr_t>(base) & (BF16 ? 7u : 15u)) == 0;
+  auto raw4 = [&](int64_t i) -> float4 {
+    if (wide && i + 4 <= i1) {
+      if constexpr (BF16) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(base + 2 * i));
+        return make_float4(number(bf16_lo(q.x)), number(bf16_hi(q.x)), number(bf16_lo(q.y)), number(bf16_hi(q.y)));
+      } else {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(base + 4 * i));
+        return make_float4(number(q.x), number(q.y), number(q.z), number(q.w));
+      }
+    }
+    return make_float4(i < i1 ? raw(i) : -INFINITY, i + 1 < i1 ? raw(i + 1) : -INFINITY,
+                       i + 2 < i1 ? raw(i + 2) : -INFINITY, i + 3 < i1 ? raw(i + 3) : -INFINITY);
   };
   auto value = [&](int64_t i) -> float {
     if constexpr (RES) return res[i - i0];
     else return raw(i);
   };
-  // fn(logit, index) over this thread's elements, kBatch loads in flight. Whole warps call fn: past the
-  // end of the slice with -inf, which counts for nothing.
-  constexpr int kBatch = 8;
-  auto each = [&](auto get, auto fn) {
-    for (int64_t i = i0 + tid; i - lane < i1; i += kBatch * kT) {
-      float v[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) v[j] = i + j * kT < i1 ? get(i + j * kT) : -INFINITY;
+  auto value4 = [&](int64_t i) -> float4 {
+    if constexpr (RES) return *reinterpret_cast<const float4*>(res + (i - i0));
+    else return raw4(i);
+  };
+  // fn(four logits, index of the first) over this thread's elements, kBatch loads in flight. Whole warps
+  // call fn: past the end of the slice with -inf, which counts for nothing.
+  constexpr int kBatch = 4;
+  auto each4 = [&](auto get, auto fn) {
+    for (int64_t i = i0 + 4 * tid; i - 4 * lane < i1; i += 4 * kBatch * kT) {
+      float4 v[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        if (i + j * kT - lane < i1) fn(v[j], i + j * kT);
+        v[j] = i + 4 * j * kT - 4 * lane < i1 ? get(i + 4 * j * kT) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i + 4 * j * kT - 4 * lane < i1) fn(v[j], i + 4 * j * kT);
     }
+  };
+  auto each = [&](auto fn) {  // fn(logit, index)
+    each4(value4, [&](const float4& v, int64_t i) {
+      fn(v.x, i);
+      fn(v.y, i + 1);
+      fn(v.z, i + 2);
+      fn(v.w, i + 3);
+    });
   };
 
   // this CTA's slice of probs, zeros: 16 bytes at a time between ragged ends
@@ -364,12 +417,14 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   // ---- pass 1: the slice into shared memory, its largest and smallest finite-or-+inf logit
   uint32_t hi = 0u, lo = 0xFFFFFFFFu;  // order bits; 0 is below -inf
   const uint32_t kNegInf = order_bits(-INFINITY);
-  each(raw, [&](float v, int64_t i) {
-    if constexpr (RES) res[i - i0] = v;
-    const uint32_t o = order_bits(v);
-    if (o > kNegInf) {
-      hi = o > hi ? o : hi;
-      lo = o < lo ? o : lo;
+  each4(raw4, [&](const float4& v, int64_t i) {
+    if constexpr (RES) *reinterpret_cast<float4*>(res + (i - i0)) = v;
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t o = order_bits(x[j]);
+      hi = o > hi && o > kNegInf ? o : hi;
+      lo = o < lo && o > kNegInf ? o : lo;
     }
   });
   const uint32_t own = hi;  // this thread's largest
@@ -396,8 +451,13 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   } else if (lane == 0) {
     // fp64 is slow here: one thread each, under the exchange of the maxima (by all threads, the division
     // and the logarithm cost 4,000 and 15,000 cycles)
-    if (warp == 1) s.log2e_t = 1.4426950408889634074 / static_cast<double>(T);
-    if (warp == 2) s.t_ln_min_p = min_p > 0.0f && min_p < 1.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0;
+    auto split = [](double v, float& h, float& l) {
+      h = static_cast<float>(v);
+      l = isinf(h) ? 0.0f : static_cast<float>(v - static_cast<double>(h));
+    };
+    if (warp == 1) split(1.4426950408889634074 / static_cast<double>(T), s.ch, s.cl);
+    if (warp == 2)
+      split(min_p > 0.0f && min_p < 1.0f ? static_cast<double>(T) * log(static_cast<double>(min_p)) : 0.0, s.bh, s.bl);
   }
   sync();
   uint32_t mx = 0u, mn = 0xFFFFFFFFu;
@@ -419,12 +479,9 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   const float m = from_order(mx);
   const bool inf = isinf(m);  // then only the infinite logits have weight
   Weigh weigh;
-  {
-    const double c = s.log2e_t;
-    weigh.m = m;
-    weigh.ch = static_cast<float>(c);
-    weigh.cl = isinf(weigh.ch) ? 0.0f : static_cast<float>(c - static_cast<double>(weigh.ch));
-  }
+  weigh.m = m;
+  weigh.ch = s.ch;
+  weigh.cl = s.cl;
   auto counted = [&](float l) { return inf ? l == m : l > -INFINITY; };
   auto weight = [&](float l) -> float { return counted(l) ? weigh(l) : 0.0f; };
   auto key64 = [&](float l, int64_t i) -> u64 {
@@ -433,9 +490,12 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   // min_p as a bound on the logit: the smallest float not below m + T ln(min_p)
   float bound = -INFINITY;
   if (min_p > 0.0f) {
-    const double t = static_cast<double>(m) + s.t_ln_min_p;
-    bound = static_cast<float>(t);
-    if (static_cast<double>(bound) < t) bound = nextafterf(bound, INFINITY);
+    // m + bh + bl = bound + e exactly; a sum above bound takes the next float (no sum: infinities)
+    float e;
+    two_sum(m, s.bh, bound, e);
+    if (isinf(m)) bound = m;
+    else if (isinf(bound)) bound = -3.402823466e38f;
+    else if (e + s.bl > 0.0f) bound = nextafterf(bound, INFINITY);
   }
 
   // ---- the cut: tokens with key >= cut are kept
@@ -485,7 +545,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     };
     // One histogram round over the elements that `in` selects, of entries and / or of masses.
     auto histogram = [&](bool with_n, bool with_mass, auto in, auto bin) {
-      each(value, [&](float l, int64_t i) {
+      each([&](float l, int64_t i) {
         const bool on = in(l, i);
         const int b = on ? bin(l, i) : -1;
         if (with_n) {  // a whole warp in one bin (equal or far-away logits) adds once
@@ -545,7 +605,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     // there are, on every CTA.
     auto gather = [&](auto in) -> int {
       uint32_t mine = 0u;
-      each(value, [&](float l, int64_t i) {
+      each([&](float l, int64_t i) {
         if (in(l, i)) {
           ++mine;
           const uint32_t at = nc > 1 ? add_peer32(peer(&s.gathered, 0), 1u) : atomicAdd(&s.gathered, 1u);
@@ -625,32 +685,45 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         if (tid == 0) s.inv_z = inverse(z);
         __syncthreads();
         const float inv_z = s.inv_z;
-        // probabilities, and the kept entries in index order: sorted by (complement of the index, place)
+        if (a.probs)
+          for (int e = tid; e < kept_n; e += kT)
+            a.probs[row * V + static_cast<int64_t>(~static_cast<uint32_t>(cand[e]))] =
+                __fmul_rn(weight(from_order(static_cast<uint32_t>(cand[e] >> 32))), inv_z);
+        if (!a.token && !a.prob) return;
+        const u64 target = scale_floor(u, z);
+        auto take = [&](int e) {
+          const u64 key = cand[e];
+          if (a.token) a.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(key));
+          if (a.prob) a.prob[row] = __fmul_rn(weight(from_order(static_cast<uint32_t>(key >> 32))), inv_z);
+        };
+        auto mass_of = [&](int e) { return list_mass[e] - (e > 0 ? list_mass[e - 1] : 0ull); };
+        u64* order = loc.mass;  // [kGather]
+        if (kept_n <= 128) {
+          // few: each entry sums the masses of the lower indices (larger complements) itself
+          for (int e = tid; e < kept_n; e += kT) order[e] = mass_of(e);
+          __syncthreads();
+          if (tid < kept_n) {
+            const uint32_t me = static_cast<uint32_t>(cand[tid]);
+            u64 before = 0ull;
+            for (int j = 0; j < kept_n; ++j) before += static_cast<uint32_t>(cand[j]) > me ? order[j] : 0ull;
+            if (before <= target && target - before < order[tid]) take(tid);
+          }
+          return;
+        }
+        // the kept entries in index order: sorted by (complement of the index, place)
         int size = 32;
         while (size < kept_n) size <<= 1;
-        u64* order = loc.mass;  // [kGather]
-        for (int e = tid; e < size; e += kT) {
-          u64 o = 0ull;
-          if (e < kept_n) {
-            const u64 key = cand[e];
-            if (a.probs)
-              a.probs[row * V + static_cast<int64_t>(~static_cast<uint32_t>(key))] =
-                  __fmul_rn(weight(from_order(static_cast<uint32_t>(key >> 32))), inv_z);
-            o = (static_cast<u64>(static_cast<uint32_t>(key)) << 32) | static_cast<uint32_t>(e);
-          }
-          order[e] = o;
-        }
-        if (!a.token && !a.prob) return;
+        for (int e = tid; e < size; e += kT)
+          order[e] = e < kept_n ? (static_cast<u64>(static_cast<uint32_t>(cand[e])) << 32) | static_cast<uint32_t>(e) : 0ull;
         __syncthreads();
         sort_desc(order, size);
-        const u64 target = scale_floor(u, z);
         u64 w2[2];
         int place[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int e = 2 * tid + j;
           place[j] = e < kept_n ? static_cast<int>(static_cast<uint32_t>(order[e])) : -1;
-          w2[j] = place[j] < 0 ? 0ull : list_mass[place[j]] - (place[j] > 0 ? list_mass[place[j] - 1] : 0ull);
+          w2[j] = place[j] < 0 ? 0ull : mass_of(place[j]);
         }
         const u64 inc = warp_inclusive(w2[0] + w2[1], lane);
         if (lane == 31) s.scan[warp] = inc;
@@ -659,11 +732,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         for (int q = 0; q < warp; ++q) before += s.scan[q];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (before <= target && target - before < w2[j]) {
-            const u64 key = cand[place[j]];
-            if (a.token) a.token[row] = static_cast<int32_t>(~static_cast<uint32_t>(key));
-            if (a.prob) a.prob[row] = __fmul_rn(weight(from_order(static_cast<uint32_t>(key >> 32))), inv_z);
-          }
+          if (before <= target && target - before < w2[j]) take(place[j]);
           before += w2[j];
         }
         return;
@@ -762,13 +831,17 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   u64 sum = 0ull;
   {
     const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
-    for (int64_t i = w0 + lane; i < w1; i += 32 * kBatch) {
-      float v[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) v[j] = i + 32 * j < w1 ? value(i + 32 * j) : -INFINITY;
+    auto mass = [&](float l, int64_t i) { return kept(l, i) ? to_fixed(weigh(l), frac) : 0ull; };
+    for (int64_t i = w0 + 4 * lane; i < w1; i += 128 * kBatch) {
+      float4 v[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        sum += kept(v[j], i + 32 * j) ? to_fixed(weigh(v[j]), frac) : 0ull;  // (-inf past the end: not kept)
+        v[j] = i + 128 * j < w1 ? value4(i + 128 * j) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t at = i + 128 * j;
+        sum += mass(v[j].x, at) + mass(v[j].y, at + 1) + mass(v[j].z, at + 2) + mass(v[j].w, at + 3);
+      }
     }
   }
   sum = warp_sum(sum);
@@ -796,10 +869,22 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
              if (a.token) a.token[row] = static_cast<int32_t>(i);
              if (a.prob) a.prob[row] = __fmul_rn(weight(value(i)), inv_z);
            });
-  if (a.probs)
-    each(value, [&](float l, int64_t i) {
-      if (i < i1) __stcs(a.probs + row * V + i, kept(l, i) ? __fmul_rn(weight(l), inv_z) : 0.0f);
+  if (a.probs) {
+    float* dst = a.probs + row * V;
+    const bool wide_out = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
+    each4(value4, [&](const float4& v, int64_t i) {
+      auto prob = [&](float l, int64_t at) { return kept(l, at) ? __fmul_rn(weigh(l), inv_z) : 0.0f; };
+      const float4 o = make_float4(prob(v.x, i), prob(v.y, i + 1), prob(v.z, i + 2), prob(v.w, i + 3));
+      if (wide_out && i + 4 <= i1) {
+        __stcs(reinterpret_cast<float4*>(dst + i), o);
+      } else {
+        if (i < i1) dst[i] = o.x;
+        if (i + 1 < i1) dst[i + 1] = o.y;
+        if (i + 2 < i1) dst[i + 2] = o.z;
+        if (i + 3 < i1) dst[i + 3] = o.w;
+      }
     });
+  }
 }
 
 // ------------------------------------------------------------------------------- acceptance
