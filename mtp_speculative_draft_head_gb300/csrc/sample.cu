@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -80,11 +81,6 @@ __device__ __forceinline__ uint32_t ld_peer32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
-}
-__device__ __forceinline__ uint32_t add_peer32(uint32_t addr, uint32_t v) {
-  uint32_t r;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(addr), "r"(v) : "memory");
-  return r;
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
@@ -159,23 +155,32 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// m 2^s to nearest, as a 64-bit number, for m < 2^24 and s <= 39.
+__device__ __forceinline__ u64 shift_round(uint32_t m, int s) {
+  const int up = s > 0 ? s : 0;
+  const int dn = s < 0 ? (s > -31 ? -s : 31) : 0;
+  return static_cast<u64>((m + ((1u << dn) >> 1)) >> dn) << up;
+}
+
 // exp(-(m - l) / T) for l <= m: the difference exactly (TwoSum), times log2(e) / T as a double-float,
 // split into a whole power of two and 2^f, |f| <= 1/2, by the exponential series (eight terms:
-// remainder 0.3466^8 / 8! < 2^-27).
+// remainder 0.3466^8 / 8! < 2^-27). As a float, or as a fixed-point mass.
 struct Weigh {
   float m, ch, cl;
-  __device__ __forceinline__ float operator()(float l) const {
+  int frac;
+  // 2^f's float and the whole power n: the weight is p 2^-n; false: nothing (below 2^-120, or no distance)
+  __device__ __forceinline__ bool parts(float l, float& p, int& n) const {
     float dh, dl;
     two_sum(m, -l, dh, dl);
     float th = __fmul_rn(dh, ch);
     float tl = __fmaf_rn(dh, ch, -th) + __fmaf_rn(dh, cl, __fmul_rn(dl, ch));
-    const bool tiny = !(th < 120.0f);  // below 2^-120 of the maximum's weight (NaN: an infinite distance)
-    th = tiny ? 0.0f : th;
-    tl = tiny ? 0.0f : tl;
-    const float n = rintf(th);
-    const float f = -((th - n) + tl);
-    const float y = f * 0.69314718055994530942f;
-    float p = 1.0f / 5040.0f;
+    const bool some = th < 120.0f;  // (not for NaN: an infinite distance)
+    th = some ? th : 0.0f;
+    tl = some ? tl : 0.0f;
+    const float r = rintf(th);
+    n = static_cast<int>(r);
+    const float y = ((r - th) - tl) * 0.69314718055994530942f;
+    p = 1.0f / 5040.0f;
     p = __fmaf_rn(p, y, 1.0f / 720.0f);
     p = __fmaf_rn(p, y, 1.0f / 120.0f);
     p = __fmaf_rn(p, y, 1.0f / 24.0f);
@@ -183,8 +188,22 @@ struct Weigh {
     p = __fmaf_rn(p, y, 0.5f);
     p = __fmaf_rn(p, y, 1.0f);
     p = __fmaf_rn(p, y, 1.0f);
-    const float w = __uint_as_float(__float_as_uint(p) - (static_cast<uint32_t>(static_cast<int>(n)) << 23));
-    return l == m ? 1.0f : (tiny ? 0.0f : w);
+    return some;
+  }
+  __device__ __forceinline__ float operator()(float l) const {
+    float p;
+    int n;
+    const bool some = parts(l, p, n);
+    const float w = __uint_as_float(__float_as_uint(p) - (static_cast<uint32_t>(n) << 23));
+    return l == m ? 1.0f : (some ? w : 0.0f);
+  }
+  __device__ __forceinline__ u64 mass(float l) const {
+    float p;
+    int n;
+    const bool some = parts(l, p, n) || l == m;  // (l = m = inf: distance NaN, p = 1, n = 0)
+    const uint32_t b = __float_as_uint(p);       // 0.70 < p < 1.42
+    const u64 w = shift_round((b & 0x7FFFFFu) | 0x800000u, static_cast<int>(b >> 23) - 150 + frac - n);
+    return some ? w : 0ull;
   }
 };
 
@@ -201,7 +220,6 @@ struct Shared {
   int hit;
   uint32_t before_n, hit_n;
   u64 before_m;
-  uint32_t gathered;       // first CTA: candidates received
   uint32_t found;          // this CTA's candidates
   uint32_t counts[kMaxC];  // every CTA's candidates (pushed by its peers)
   u64 cut, cut_mass;       // published by the first CTA
@@ -330,7 +348,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     loc.mass[b] = 0ull;
     loc.n[b] = 0u;
   }
-  if (tid == 0) s.gathered = s.found = 0u;
+  if (tid == 0) s.found = 0u;
   pdl_wait_prior_grid();
 
   // ---- the row's parameters
@@ -352,45 +370,62 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     if constexpr (BF16) return number(bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(base) + i)));
     else return number(__ldg(reinterpret_cast<const float*>(base) + i));
   };
-  // four elements at i (a multiple of 4 from i0): one load where the row is aligned and has them all
+  // Four elements as they lie in memory: one load where the row is aligned and has all four (`end`: where it,
+  // or the slice, ends), -inf past the end.
+  using Quad = typename std::conditional<BF16, uint2, float4>::type;
   const bool wide = (reinterpret_cast<uintptr_t>(base) & (BF16 ? 7u : 15u)) == 0;
-  auto raw4 = [&](int64_t i) -> float4 {
-    if (wide && i + 4 <= i1) {
-      if constexpr (BF16) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(base + 2 * i));
-        return make_float4(number(bf16_lo(q.x)), number(bf16_hi(q.x)), number(bf16_lo(q.y)), number(bf16_hi(q.y)));
-      } else {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(base + 4 * i));
-        return make_float4(number(q.x), number(q.y), number(q.z), number(q.w));
-      }
+  auto load4 = [&](int64_t i, int64_t end) -> Quad {
+    if (wide && i + 4 <= end) {
+      if constexpr (BF16) return __ldg(reinterpret_cast<const uint2*>(base + 2 * i));
+      else return __ldg(reinterpret_cast<const float4*>(base + 4 * i));
     }
-    return make_float4(i < i1 ? raw(i) : -INFINITY, i + 1 < i1 ? raw(i + 1) : -INFINITY,
-                       i + 2 < i1 ? raw(i + 2) : -INFINITY, i + 3 < i1 ? raw(i + 3) : -INFINITY);
+    if constexpr (BF16) {
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = i + j < end ? __ldg(reinterpret_cast<const uint16_t*>(base) + i + j) : 0xFF80u;
+      return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    } else {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = i + j < end ? __ldg(reinterpret_cast<const float*>(base) + i + j) : -INFINITY;
+      return make_float4(x[0], x[1], x[2], x[3]);
+    }
+  };
+  auto unpack = [&](const Quad& q) {
+    if constexpr (BF16) return make_float4(number(bf16_lo(q.x)), number(bf16_hi(q.x)), number(bf16_lo(q.y)), number(bf16_hi(q.y)));
+    else return make_float4(number(q.x), number(q.y), number(q.z), number(q.w));
+  };
+  // fn(four elements, index of the first) for i, i + stride, ... below `end` (`first`: the same for a whole
+  // warp), four loads ahead: the body is long, so the loop is rolled and the loads queue in registers.
+  // The lanes of a warp are called together: past the end with -inf, which counts for nothing.
+  auto from_row = [&](int64_t first, int64_t i, int stride, int64_t end, auto fn) {
+    const int64_t off = i - first;
+    Quad q0 = load4(i, end), q1 = load4(i + stride, end), q2 = load4(i + 2 * stride, end), q3 = load4(i + 3 * stride, end);
+#pragma unroll 1
+    for (; first < end; first += stride) {
+      const Quad now = q0;
+      q0 = q1;
+      q1 = q2;
+      q2 = q3;
+      q3 = load4(first + off + 4 * stride, end);
+      fn(unpack(now), first + off);
+    }
+  };
+  auto walk = [&](int64_t first, int64_t i, int stride, int64_t end, auto fn) {
+    if constexpr (RES) {  // (shared memory holds -inf from the end of the slice to the next multiple of 128)
+      const int64_t off = i - first;
+#pragma unroll 2
+      for (; first < end; first += stride) fn(*reinterpret_cast<const float4*>(res + (first + off - i0)), first + off);
+    } else {
+      from_row(first, i, stride, end, fn);
+    }
   };
   auto value = [&](int64_t i) -> float {
     if constexpr (RES) return res[i - i0];
     else return raw(i);
   };
-  auto value4 = [&](int64_t i) -> float4 {
-    if constexpr (RES) return *reinterpret_cast<const float4*>(res + (i - i0));
-    else return raw4(i);
-  };
-  // fn(four logits, index of the first) over this thread's elements, kBatch loads in flight. Whole warps
-  // call fn: past the end of the slice with -inf, which counts for nothing.
-  constexpr int kBatch = 4;
-  auto each4 = [&](auto get, auto fn) {
-    for (int64_t i = i0 + 4 * tid; i - 4 * lane < i1; i += 4 * kBatch * kT) {
-      float4 v[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        v[j] = i + 4 * j * kT - 4 * lane < i1 ? get(i + 4 * j * kT) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (i + 4 * j * kT - 4 * lane < i1) fn(v[j], i + 4 * j * kT);
-    }
-  };
-  auto each = [&](auto fn) {  // fn(logit, index)
-    each4(value4, [&](const float4& v, int64_t i) {
+  auto each = [&](auto fn) {  // fn(logit, index) over this thread's elements
+    walk(i0 + 128 * warp, i0 + 4 * tid, 4 * kT, i1, [&](const float4& v, int64_t i) {
       fn(v.x, i);
       fn(v.y, i + 1);
       fn(v.z, i + 2);
@@ -415,19 +450,19 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   };
 
   // ---- pass 1: the slice into shared memory, its largest and smallest finite-or-+inf logit
-  uint32_t hi = 0u, lo = 0xFFFFFFFFu;  // order bits; 0 is below -inf
-  const uint32_t kNegInf = order_bits(-INFINITY);
-  each4(raw4, [&](const float4& v, int64_t i) {
+  float most = -INFINITY, least = INFINITY;
+  from_row(i0 + 128 * warp, i0 + 4 * tid, 4 * kT, i1, [&](const float4& v, int64_t i) {
     if constexpr (RES) *reinterpret_cast<float4*>(res + (i - i0)) = v;
     const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t o = order_bits(x[j]);
-      hi = o > hi && o > kNegInf ? o : hi;
-      lo = o < lo && o > kNegInf ? o : lo;
+      most = fmaxf(most, x[j]);
+      least = fminf(least, x[j] > -INFINITY ? x[j] : INFINITY);
     }
   });
-  const uint32_t own = hi;  // this thread's largest
+  // as order bits; 0 and all ones: none
+  uint32_t hi = most > -INFINITY ? order_bits(most) : 0u;
+  uint32_t lo = most > -INFINITY ? order_bits(least) : 0xFFFFFFFFu;
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
   if (lane == 0) {
@@ -482,6 +517,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   weigh.m = m;
   weigh.ch = s.ch;
   weigh.cl = s.cl;
+  weigh.frac = frac;
   auto counted = [&](float l) { return inf ? l == m : l > -INFINITY; };
   auto weight = [&](float l) -> float { return counted(l) ? weigh(l) : 0.0f; };
   auto key64 = [&](float l, int64_t i) -> u64 {
@@ -509,7 +545,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     reach = range < reach ? range : reach;
     float inv = __fdiv_rn(static_cast<float>(kBins), reach);
     if (!(inv <= 3.0e38f) || !(reach <= 3.0e38f)) inv = 0.0f;  // nothing to divide, or not in fp32: one bin
-    auto live = [&](float l) { return counted(l) && (l == m || __fsub_rn(m, l) <= reach); };
+    auto live = [&](float l) { return l == m || (l > -INFINITY && __fsub_rn(m, l) <= reach); };
     auto bin1 = [&](float l) -> int {
       if (l == m) return 0;
       const int b = static_cast<int>(__fmul_rn(__fsub_rn(m, l), inv));
@@ -555,7 +591,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
             atomicAdd(&loc.n[b], 1u);
           }
         }
-        if (with_mass && on) add64(reinterpret_cast<uint32_t*>(&loc.mass[b]), to_fixed(weigh(l), frac));
+        if (with_mass && on) add64(reinterpret_cast<uint32_t*>(&loc.mass[b]), weigh.mass(l));
       });
       share_bins(with_mass);
     };
@@ -601,32 +637,36 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       }
       __syncthreads();
     };
-    // The entries that `in` selects to the first CTA's list (the first kGather that come); returns how many
-    // there are, on every CTA.
+    // The entries that `in` selects to the first CTA's list, if they are at most kGather; returns how many
+    // there are, on every CTA. Each CTA lists its own first (an atomic on another CTA's shared memory takes
+    // some 2,000 cycles), in the upper half of `all`, which no list overwrites.
     auto gather = [&](auto in) -> int {
-      uint32_t mine = 0u;
+      u64* mine = nc > 1 ? all.mass + kGather : cand;
       each([&](float l, int64_t i) {
         if (in(l, i)) {
-          ++mine;
-          const uint32_t at = nc > 1 ? add_peer32(peer(&s.gathered, 0), 1u) : atomicAdd(&s.gathered, 1u);
-          if (at < kGather) {
-            if (nc > 1) st_peer(peer(&cand[at], 0), key64(l, i));
-            else cand[at] = key64(l, i);
-          }
+          const uint32_t at = atomicAdd(&s.found, 1u);
+          if (at < kGather) mine[at] = key64(l, i);
         }
       });
-      mine = __reduce_add_sync(0xffffffffu, mine);
-      if (lane == 0 && mine) atomicAdd(&s.found, mine);
       __syncthreads();
-      if (tid < nc) {
-        if (nc > 1) st_peer32(peer(&s.counts[rank], tid), s.found);
-        else s.counts[0] = s.found;
+      const uint32_t own = s.found;
+      if (nc > 1) {
+        if (tid < nc) st_peer32(peer(&s.counts[rank], tid), own);
+        cluster_sync_all();
+        uint32_t n = 0u, at = 0u;
+        for (int r = 0; r < nc; ++r) {
+          if (r == static_cast<int>(rank)) at = n;
+          n += s.counts[r];
+        }
+        if (n <= kGather)
+          for (uint32_t j = tid; j < own; j += kT) st_peer(peer(&cand[at + j], 0), mine[j]);
+        if (tid == 0) s.found = 0u;
+        cluster_sync_all();
+        return static_cast<int>(n < 0x7FFFFFFFu ? n : 0x7FFFFFFFu);
       }
-      sync();
-      uint32_t n = 0u;
-      for (int r = 0; r < nc; ++r) n += s.counts[r];
-      if (tid == 0) s.gathered = s.found = 0u;  // (before the next barrier, ahead of the next list)
-      return static_cast<int>(n < 0x7FFFFFFFu ? n : 0x7FFFFFFFu);
+      __syncthreads();
+      if (tid == 0) s.found = 0u;
+      return static_cast<int>(own);
     };
     // (first CTA) the list sorted, descending, and its entries' running masses in `list_mass`, from `base`
     u64* list_mass = all.mass;  // [kGather]; the histogram is not needed any more when this is used
@@ -639,7 +679,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       u64 w2[2] = {0ull, 0ull};  // two entries a thread
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        if (with_mass && 2 * tid + j < n) w2[j] = to_fixed(weight(from_order(static_cast<uint32_t>(cand[2 * tid + j] >> 32))), frac);
+        if (with_mass && 2 * tid + j < n) w2[j] = weigh.mass(from_order(static_cast<uint32_t>(cand[2 * tid + j] >> 32)));
       const u64 inc = warp_inclusive(w2[0] + w2[1], lane);
       if (lane == 31) s.scan[warp] = inc;
       __syncthreads();
@@ -655,15 +695,15 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
 
     if (use_k && 2 * k <= static_cast<int64_t>(nc) * kT) {
       // ---- the whole row on one sorted list: the bins of the threads' maxima first
-      {
-        const float l = own == 0u ? -INFINITY : from_order(own);
-        if (live(l)) atomicAdd(&loc.n[bin1(l)], 1u);
-      }
+      if (live(most)) atomicAdd(&loc.n[bin1(most)], 1u);
       share_bins(false);
       find(false, static_cast<u64>(k), 0u, 0ull);
       const int b1 = s.hit;
-      if (a.probs) zero_row();  // (the first CTA's own stores come after the gather's barrier)
-      const int n = b1 < 0 ? kGather + 1 : gather([&](float l, int64_t) { return live(l) && bin1(l) <= b1; });
+      if (a.probs) zero_row();  // (the first CTA's own stores come after the gather's barriers)
+      const float upto = b1 == kBins - 1 ? INFINITY : static_cast<float>(b1 + 1);  // bin1(l) <= b1
+      const int n = b1 < 0 ? kGather + 1 : gather([&](float l, int64_t) {
+        return live(l) && (l == m || __fmul_rn(__fsub_rn(m, l), inv) < upto);
+      });
       if (n <= kGather) {
         if (rank != 0) return;
         sort_list(n, true, 0ull);
@@ -825,24 +865,34 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       cut = cut_p > cut ? cut_p : cut;
     }
   }
-  auto kept = [&](float l, int64_t i) { return l >= bound && counted(l) && (cut == 0ull || key64(l, i) >= cut); };
+  // kept: above the cut's (or min_p's) logit, or at it and not behind the cut's index; without either,
+  // anything but -inf, and with an infinite maximum only that
+  float edge = -INFINITY;
+  uint32_t edge_index = 0xFFFFFFFFu;  // complement of the last index kept at the edge (all ones: none)
+  if (cut != 0ull) {
+    edge = from_order(static_cast<uint32_t>(cut >> 32));
+    edge_index = static_cast<uint32_t>(cut);
+  }
+  if (bound > edge) {
+    edge = bound;
+    edge_index = 0u;
+  }
+  if (inf && !(edge == m)) {
+    edge = m;
+    edge_index = 0u;
+  }
+  auto kept = [&](float l, int64_t i) {
+    return l > edge || (l == edge && static_cast<uint32_t>(~static_cast<uint32_t>(i)) >= edge_index);
+  };
 
   // ---- masses of the kept tokens per warp segment, CTA and row
   u64 sum = 0ull;
   {
     const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
-    auto mass = [&](float l, int64_t i) { return kept(l, i) ? to_fixed(weigh(l), frac) : 0ull; };
-    for (int64_t i = w0 + 4 * lane; i < w1; i += 128 * kBatch) {
-      float4 v[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        v[j] = i + 128 * j < w1 ? value4(i + 128 * j) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int64_t at = i + 128 * j;
-        sum += mass(v[j].x, at) + mass(v[j].y, at + 1) + mass(v[j].z, at + 2) + mass(v[j].w, at + 3);
-      }
-    }
+    auto mass = [&](float l, int64_t i) { return kept(l, i) ? weigh.mass(l) : 0ull; };
+    walk(w0, w0 + 4 * lane, 128, w1, [&](const float4& v, int64_t i) {
+      sum += mass(v.x, i) + mass(v.y, i + 1) + mass(v.z, i + 2) + mass(v.w, i + 3);
+    });
   }
   sum = warp_sum(sum);
   if (lane == 0) s.wsum[warp] = sum;
@@ -863,7 +913,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     locate(s, rank, scale_floor(u, z), i0, seg, i1,
            [&](int64_t i) {
              const float l = value(i);
-             return kept(l, i) ? to_fixed(weight(l), frac) : 0ull;
+             return kept(l, i) ? weigh.mass(l) : 0ull;
            },
            [&](int64_t i) {
              if (a.token) a.token[row] = static_cast<int32_t>(i);
@@ -872,7 +922,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   if (a.probs) {
     float* dst = a.probs + row * V;
     const bool wide_out = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
-    each4(value4, [&](const float4& v, int64_t i) {
+    walk(i0 + 128 * warp, i0 + 4 * tid, 4 * kT, i1, [&](const float4& v, int64_t i) {
       auto prob = [&](float l, int64_t at) { return kept(l, at) ? __fmul_rn(weigh(l), inv_z) : 0.0f; };
       const float4 o = make_float4(prob(v.x, i), prob(v.y, i + 1), prob(v.z, i + 2), prob(v.w, i + 3));
       if (wide_out && i + 4 <= i1) {
