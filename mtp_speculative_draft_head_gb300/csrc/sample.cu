@@ -274,12 +274,33 @@ __device__ void locate(const Shared& s, uint32_t rank, u64 target, int64_t i0, i
 }
 
 // ------------------------------------------------------------------------------- sampler
-// Bitonic sort, descending, of `size` (a power of two, 32 to kGather) 64-bit keys by the whole block. Up to
-// kT keys sit one to a thread: a step of distance below 32 is a shuffle, the others (10 of 45 at 512)
+// Sort, descending, of `size` (a power of two, 32 to kGather) 64-bit keys by the whole block; the keys other
+// than 0 are distinct. Up to kT / 2 by counting; more by a bitonic sort, in which up to kT keys sit one to a
+// thread: a step of distance below 32 is a shuffle, the others (10 of 45 at 512)
 // go through shared memory. More sort in shared memory, where steps of distance up to 32 stay within
 // the 64 keys of one warp's lanes.
 __device__ void sort_desc(u64* key, int size) {
   const int tid = threadIdx.x;
+  if (2 * size <= kT) {
+    // few distinct keys (and zeros): each one's place is the number of larger ones, counted by two threads
+    const u64 k = key[tid >> 1 & (size - 1)];
+    uint32_t place = 0u;
+    if (tid < 2 * size) {
+      const ulonglong2* half = reinterpret_cast<const ulonglong2*>(key) + (tid & 1) * (size / 4);
+#pragma unroll 4
+      for (int j = 0; j < size / 4; ++j) {
+        const ulonglong2 o = half[j];
+        place += (o.x > k ? 1u : 0u) + (o.y > k ? 1u : 0u);
+      }
+      place += __shfl_xor_sync(0xffffffffu, place, 1);
+    }
+    __syncthreads();
+    if (tid < size) key[tid] = 0ull;
+    __syncthreads();
+    if (tid < 2 * size && (tid & 1) == 0 && k != 0ull) key[place] = k;
+    __syncthreads();
+    return;
+  }
   if (size <= kT) {
     const bool warp_on = (tid & ~31) < size;
     u64 k = warp_on ? key[tid] : 0ull;
@@ -424,15 +445,6 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     if constexpr (RES) return res[i - i0];
     else return raw(i);
   };
-  auto each = [&](auto fn) {  // fn(logit, index) over this thread's elements
-    walk(i0 + 128 * warp, i0 + 4 * tid, 4 * kT, i1, [&](const float4& v, int64_t i) {
-      fn(v.x, i);
-      fn(v.y, i + 1);
-      fn(v.z, i + 2);
-      fn(v.w, i + 3);
-    });
-  };
-
   // this CTA's slice of probs, zeros: 16 bytes at a time between ragged ends
   auto zero_row = [&] {
     float* dst = a.probs + row * V;
@@ -545,11 +557,11 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     reach = range < reach ? range : reach;
     float inv = __fdiv_rn(static_cast<float>(kBins), reach);
     if (!(inv <= 3.0e38f) || !(reach <= 3.0e38f)) inv = 0.0f;  // nothing to divide, or not in fp32: one bin
-    auto live = [&](float l) { return l == m || (l > -INFINITY && __fsub_rn(m, l) <= reach); };
+    // (bitwise: the predicates of every element, kept free of branches)
+    auto live = [&](float l) { return (l == m) | ((l > -INFINITY) & (__fsub_rn(m, l) <= reach)); };
     auto bin1 = [&](float l) -> int {
-      if (l == m) return 0;
-      const int b = static_cast<int>(__fmul_rn(__fsub_rn(m, l), inv));
-      return b < kBins - 1 ? b : kBins - 1;
+      const int b = min(static_cast<int>(__fmul_rn(__fsub_rn(m, l), inv)), kBins - 1);
+      return l == m ? 0 : b;
     };
     // The bins of loc summed over the cluster into `all` on every CTA (each sums one section and hands it
     // on); loc is left zero.
@@ -579,19 +591,39 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         loc.n[b] = 0u;
       }
     };
-    // One histogram round over the elements that `in` selects, of entries and / or of masses.
+    // One histogram round over the elements that `in` selects, of entries and / or of masses. (Masses are
+    // formed outside the branches, so that an element's chain runs beside its neighbours'.)
     auto histogram = [&](bool with_n, bool with_mass, auto in, auto bin) {
-      each([&](float l, int64_t i) {
-        const bool on = in(l, i);
-        const int b = on ? bin(l, i) : -1;
-        if (with_n) {  // a whole warp in one bin (equal or far-away logits) adds once
-          if (__all_sync(0xffffffffu, b == __shfl_sync(0xffffffffu, b, 0))) {
-            if (on && lane == 0) atomicAdd(&loc.n[b], 32u);
-          } else if (on) {
-            atomicAdd(&loc.n[b], 1u);
+      walk(i0 + 128 * warp, i0 + 4 * tid, 4 * kT, i1, [&](const float4& v, int64_t i) {
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        bool on[4];
+        int b[4];
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          on[j] = in(x[j], i + j);
+          b[j] = on[j] ? bin(x[j], i + j) : -1;
+          any = any || on[j];
+        }
+        if (!__any_sync(0xffffffffu, any)) return;
+        if (with_n) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // a whole warp in one bin (equal or far-away logits) adds once
+            if (__all_sync(0xffffffffu, b[j] == __shfl_sync(0xffffffffu, b[j], 0))) {
+              if (on[j] && lane == 0) atomicAdd(&loc.n[b[j]], 32u);
+            } else if (on[j]) {
+              atomicAdd(&loc.n[b[j]], 1u);
+            }
           }
         }
-        if (with_mass && on) add64(reinterpret_cast<uint32_t*>(&loc.mass[b]), weigh.mass(l));
+        if (with_mass) {
+          u64 w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = weigh.mass(x[j]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (on[j]) add64(reinterpret_cast<uint32_t*>(&loc.mass[b[j]]), w[j]);
+        }
       });
       share_bins(with_mass);
     };
@@ -640,14 +672,19 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     // The entries that `in` selects to the first CTA's list, if they are at most kGather; returns how many
     // there are, on every CTA. Each CTA lists its own first (an atomic on another CTA's shared memory takes
     // some 2,000 cycles), in the upper half of `all`, which no list overwrites.
-    auto gather = [&](auto in) -> int {
+    auto gather = [&](auto in, auto then) -> int {
       u64* mine = nc > 1 ? all.mass + kGather : cand;
-      each([&](float l, int64_t i) {
-        if (in(l, i)) {
+      walk(i0 + 128 * warp, i0 + 4 * tid, 4 * kT, i1, [&](const float4& v, int64_t i) {
+        uint32_t on = (in(v.x, i) ? 1u : 0u) | (in(v.y, i + 1) ? 2u : 0u) | (in(v.z, i + 2) ? 4u : 0u) | (in(v.w, i + 3) ? 8u : 0u);
+        while (on != 0u) {
+          const int j = __ffs(on) - 1;
+          on &= on - 1u;
+          const float l = j < 2 ? (j == 0 ? v.x : v.y) : (j == 2 ? v.z : v.w);
           const uint32_t at = atomicAdd(&s.found, 1u);
-          if (at < kGather) mine[at] = key64(l, i);
+          if (at < kGather) mine[at] = key64(l, i + j);
         }
       });
+      then();  // (what the first CTA's own stores, after the barriers, must find done)
       __syncthreads();
       const uint32_t own = s.found;
       if (nc > 1) {
@@ -699,10 +736,12 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       share_bins(false);
       find(false, static_cast<u64>(k), 0u, 0ull);
       const int b1 = s.hit;
-      if (a.probs) zero_row();  // (the first CTA's own stores come after the gather's barriers)
       const float upto = b1 == kBins - 1 ? INFINITY : static_cast<float>(b1 + 1);  // bin1(l) <= b1
       const int n = b1 < 0 ? kGather + 1 : gather([&](float l, int64_t) {
-        return live(l) && (l == m || __fmul_rn(__fsub_rn(m, l), inv) < upto);
+        return live(l) & ((l == m) | (__fmul_rn(__fsub_rn(m, l), inv) < upto));
+      }, [&] {
+        // after the row's last read: written earlier, the zeros of many rows push the logits out of L2
+        if (a.probs) zero_row();
       });
       if (n <= kGather) {
         if (rank != 0) return;
@@ -787,7 +826,8 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       uint32_t bn = 0u;
       u64 bm = 0ull;
       auto in_now = [&](float l, int64_t i) {
-        return (b1 < 0 ? counted(l) : live(l) && bin1(l) == b1) && (bits == 0 || (key64(l, i) >> (64 - bits)) == prefix);
+        const bool in = b1 < 0 ? counted(l) : live(l) & (bin1(l) == b1);
+        return bits == 0 ? in : in & ((key64(l, i) >> (64 - bits)) == prefix);
       };
       int n = kGather + 1;
       if (binned) {
@@ -796,7 +836,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         b1 = s.hit;
         bn = s.before_n;
         bm = s.before_m;
-        n = gather(in_now);
+        n = gather(in_now, [] {});
       }
       while (n > kGather) {
         const int step = bits + 11 <= 64 ? 11 : 64 - bits;
@@ -812,7 +852,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
         bits += step;
         bn = s.before_n;
         bm = s.before_m;
-        n = gather(in_now);
+        n = gather(in_now, [] {});
       }
       if (rank == 0) {
         sort_list(n, use_p, bm);
@@ -882,16 +922,24 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     edge_index = 0u;
   }
   auto kept = [&](float l, int64_t i) {
-    return l > edge || (l == edge && static_cast<uint32_t>(~static_cast<uint32_t>(i)) >= edge_index);
+    return (l > edge) | ((l == edge) & (static_cast<uint32_t>(~static_cast<uint32_t>(i)) >= edge_index));
   };
 
   // ---- masses of the kept tokens per warp segment, CTA and row
   u64 sum = 0ull;
   {
     const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
-    auto mass = [&](float l, int64_t i) { return kept(l, i) ? weigh.mass(l) : 0ull; };
     walk(w0, w0 + 4 * lane, 128, w1, [&](const float4& v, int64_t i) {
-      sum += mass(v.x, i) + mass(v.y, i + 1) + mass(v.z, i + 2) + mass(v.w, i + 3);
+      const float x[4] = {v.x, v.y, v.z, v.w};
+      bool on[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) on[j] = kept(x[j], i + j);
+      if (!__any_sync(0xffffffffu, on[0] || on[1] || on[2] || on[3])) return;
+      u64 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = weigh.mass(x[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += on[j] ? w[j] : 0ull;
     });
   }
   sum = warp_sum(sum);
@@ -923,8 +971,18 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     float* dst = a.probs + row * V;
     const bool wide_out = (reinterpret_cast<uintptr_t>(dst) & 15u) == 0;
     walk(i0 + 128 * warp, i0 + 4 * tid, 4 * kT, i1, [&](const float4& v, int64_t i) {
-      auto prob = [&](float l, int64_t at) { return kept(l, at) ? __fmul_rn(weigh(l), inv_z) : 0.0f; };
-      const float4 o = make_float4(prob(v.x, i), prob(v.y, i + 1), prob(v.z, i + 2), prob(v.w, i + 3));
+      const float x[4] = {v.x, v.y, v.z, v.w};
+      float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      bool on[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) on[j] = kept(x[j], i + j);
+      if (__any_sync(0xffffffffu, on[0] || on[1] || on[2] || on[3])) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = weigh(x[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = on[j] ? __fmul_rn(w[j], inv_z) : 0.0f;
+      }
+      const float4 o = make_float4(w[0], w[1], w[2], w[3]);
       if (wide_out && i + 4 <= i1) {
         __stcs(reinterpret_cast<float4*>(dst + i), o);
       } else {
