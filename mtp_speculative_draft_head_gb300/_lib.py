@@ -349,12 +349,16 @@ def mtp_head_quantize_fp8(w, q, row_scale, status, stream=None) -> None:
 
 
 # ------------------------------------------------------------------ FP4 copies, sampling, acceptance
-def _t(t, name, dtype, shape, optional=False, like=None):
-    """The address of a contiguous CUDA tensor of this type and shape, on the device of ``like``."""
+# These check every tensor (type, shape, layout, device) and launch on the tensors' own device.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _t(t, name, dtype, shape, dev, optional=False):
+    """The address of a contiguous tensor of this type and shape on CUDA device ``dev``."""
     if t is None and optional:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and (t.is_cuda if like is None else t.device == like.device)):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
@@ -364,37 +368,38 @@ def _t(t, name, dtype, shape, optional=False, like=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _status(t, like):
-    return _t(t, "status", torch.int32, (1,), True, like)
+def _first(t, name, n):
+    """The shape and CUDA device number of the tensor that decides both for a call."""
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a tensor of {n} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.shape, t.get_device()
 
 
-def _ws(t, like):
+def _ws(t, dev):
     if t is None:
         return None, 0
-    if not t.is_cuda or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _rank(t, name, n):
-    if t is None or t.dim() != n:
-        raise ValueError(f"{name} must be a tensor of {n} dimensions")
-    return tuple(t.shape)
-
-
-def _call(like, stream, name, *args):
-    """The entry point on the device of ``like``, on the given stream or that device's current one."""
+def _call(dev, stream, name, *args):
+    """The entry point on device ``dev``, on the given stream or that device's current one."""
     fn = getattr(_lib or load(), name)
-    dev = like.device.index
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _check(fn(*args, _stream(stream)), name)
-    return _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)), name)
+            code = fn(*args, _stream(stream))
+    else:
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if code != OK:
+        raise MTPError(code, name)
 
 
 def mtp_head_fp4_padded(H: int) -> int:
@@ -413,25 +418,24 @@ def fp4_empty(V: int, H: int, device=None) -> tuple[torch.Tensor, torch.Tensor, 
             torch.empty(V, dtype=torch.float32, device=dev))
 
 
-def _fp4(q, block_scale, row_scale, V, H, like):
-    hp = mtp_head_fp4_padded(H)
-    return (_t(q, "q", torch.uint8, (V, hp // 2), like=like),
-            _t(block_scale, "block_scale", torch.uint8, (V, hp // 16), like=like),
-            _t(row_scale, "row_scale", torch.float32, (V,), like=like))
+def _fp4(q, block_scale, row_scale, V, H, dev):
+    hp = (H + 255) // 256 * 256  # mtp_head_fp4_padded (the library checks the range)
+    return (_t(q, "q", _U8, (V, hp // 2), dev), _t(block_scale, "block_scale", _U8, (V, hp // 16), dev),
+            _t(row_scale, "row_scale", _F32, (V,), dev))
 
 
 def mtp_head_quantize_fp4(w, q, block_scale, row_scale, status, stream=None) -> None:
     """The FP4 copy (q, block_scale, row_scale) of w [V, H] BF16."""
-    V, H = _rank(w, "w", 2)
-    _call(w, stream, "mtp_head_quantize_fp4", _t(w, "w", torch.bfloat16, (V, H)),
-          *_fp4(q, block_scale, row_scale, V, H, w), _t(status, "status", torch.int32, (1,), like=w), V, H)
+    (V, H), dev = _first(w, "w", 2)
+    _call(dev, stream, "mtp_head_quantize_fp4", _t(w, "w", _BF16, (V, H), dev),
+          *_fp4(q, block_scale, row_scale, V, H, dev), _t(status, "status", _I32, (1,), dev), V, H)
 
 
 def mtp_head_dequantize_fp4(q, block_scale, row_scale, w, stream=None) -> None:
     """w [V, H] BF16: the matrix that an FP4 copy stands for."""
-    V, H = _rank(w, "w", 2)
-    _call(w, stream, "mtp_head_dequantize_fp4", *_fp4(q, block_scale, row_scale, V, H, w),
-          _t(w, "w", torch.bfloat16, (V, H)), V, H)
+    (V, H), dev = _first(w, "w", 2)
+    _call(dev, stream, "mtp_head_dequantize_fp4", *_fp4(q, block_scale, row_scale, V, H, dev),
+          _t(w, "w", _BF16, (V, H), dev), V, H)
 
 
 def mtp_head_fp4_workspace_bytes(B: int, H: int, V: int) -> int:
@@ -449,12 +453,12 @@ def fp4_workspace(B: int, H: int, V: int, device=None) -> torch.Tensor:
 def mtp_head_logits_argmax_fp4(x, final_norm_w, q, block_scale, row_scale, logits, draft, ws, status=None,
                                eps: float = 1e-6, stream=None) -> None:
     """Output stage over the FP4 copy of lm_head; logits [B, V] optional, draft [B]."""
-    B, H = _rank(x, "x", 2)
-    V = _rank(row_scale, "row_scale", 1)[0]
-    _call(x, stream, "mtp_head_logits_argmax_fp4", _t(x, "x", torch.bfloat16, (B, H)),
-          _t(final_norm_w, "final_norm_w", torch.bfloat16, (H,), like=x), *_fp4(q, block_scale, row_scale, V, H, x),
-          _t(logits, "logits", torch.float32, (B, V), True, x), _t(draft, "draft", torch.int32, (B,), like=x),
-          _status(status, x), *_ws(ws, x), B, H, V, eps)
+    (B, H), dev = _first(x, "x", 2)
+    (V,), _ = _first(row_scale, "row_scale", 1)
+    _call(dev, stream, "mtp_head_logits_argmax_fp4", _t(x, "x", _BF16, (B, H), dev),
+          _t(final_norm_w, "final_norm_w", _BF16, (H,), dev), *_fp4(q, block_scale, row_scale, V, H, dev),
+          _t(logits, "logits", _F32, (B, V), dev, True), _t(draft, "draft", _I32, (B,), dev),
+          _t(status, "status", _I32, (1,), dev, True), *_ws(ws, dev), B, H, V, eps)
 
 
 def mtp_head_linear_fp4_workspace_bytes(R: int, N: int, K: int) -> int:
@@ -471,11 +475,11 @@ def linear_fp4_workspace(R: int, N: int, K: int, device=None) -> torch.Tensor:
 
 def mtp_head_linear_fp4(x, q, block_scale, row_scale, y, ws, status=None, stream=None) -> None:
     """y [R, N] = rows of x [R, K], quantised to FP4, times the FP4 copy of a [N, K] matrix."""
-    R, K = _rank(x, "x", 2)
-    N = _rank(row_scale, "row_scale", 1)[0]
-    _call(x, stream, "mtp_head_linear_fp4", _t(x, "x", torch.bfloat16, (R, K)),
-          *_fp4(q, block_scale, row_scale, N, K, x), _t(y, "y", torch.bfloat16, (R, N), like=x), _status(status, x),
-          *_ws(ws, x), R, N, K)
+    (R, K), dev = _first(x, "x", 2)
+    (N,), _ = _first(row_scale, "row_scale", 1)
+    _call(dev, stream, "mtp_head_linear_fp4", _t(x, "x", _BF16, (R, K), dev),
+          *_fp4(q, block_scale, row_scale, N, K, dev), _t(y, "y", _BF16, (R, N), dev),
+          _t(status, "status", _I32, (1,), dev, True), *_ws(ws, dev), R, N, K)
 
 
 def mtp_head_context_fp4_workspace_bytes(R: int, H: int) -> int:
@@ -493,49 +497,41 @@ def context_fp4_workspace(R: int, H: int, device=None) -> torch.Tensor:
 def mtp_head_context_rows_fp4(embed, enorm_w, hnorm_w, eh_q, eh_block_scale, eh_row_scale, tokens, target_hidden,
                               x_out, ws, status=None, eps: float = 1e-6, stream=None) -> None:
     """The input stage of R rows with an FP4 copy of eh_proj."""
-    V, H = _rank(embed, "embed", 2)
-    R = _rank(tokens, "tokens", 1)[0]
-    _call(embed, stream, "mtp_head_context_rows_fp4", _t(embed, "embed", torch.bfloat16, (V, H)),
-          _t(enorm_w, "enorm_w", torch.bfloat16, (H,), like=embed),
-          _t(hnorm_w, "hnorm_w", torch.bfloat16, (H,), like=embed),
-          *_fp4(eh_q, eh_block_scale, eh_row_scale, H, 2 * H, embed),
-          _t(tokens, "tokens", torch.int32, (R,), like=embed),
-          _t(target_hidden, "target_hidden", torch.bfloat16, (R, H), like=embed),
-          _t(x_out, "x_out", torch.bfloat16, (R, H), like=embed), _status(status, embed), *_ws(ws, embed), R, H, V, eps)
+    (V, H), dev = _first(embed, "embed", 2)
+    (R,), _ = _first(tokens, "tokens", 1)
+    _call(dev, stream, "mtp_head_context_rows_fp4", _t(embed, "embed", _BF16, (V, H), dev),
+          _t(enorm_w, "enorm_w", _BF16, (H,), dev), _t(hnorm_w, "hnorm_w", _BF16, (H,), dev),
+          *_fp4(eh_q, eh_block_scale, eh_row_scale, H, 2 * H, dev), _t(tokens, "tokens", _I32, (R,), dev),
+          _t(target_hidden, "target_hidden", _BF16, (R, H), dev), _t(x_out, "x_out", _BF16, (R, H), dev),
+          _t(status, "status", _I32, (1,), dev, True), *_ws(ws, dev), R, H, V, eps)
 
 
 def mtp_head_sample(logits, u=None, token=None, prob=None, probs=None, temperature=None, top_k=None, top_p=None,
                     min_p=None, status=None, stream=None) -> None:
     """One token per row of logits [R, V] (fp32 or BF16; the rows may be strided) from u [R]. The
     parameters are [R] tensors or None; token, prob [R] and probs [R, V] are outputs, each optional."""
-    R, V = _rank(logits, "logits", 2)
-    if not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    (R, V), dev = _first(logits, "logits", 2)
+    if logits.dtype not in (_F32, _BF16):
         raise ValueError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
-    ld = logits.stride(0) if R > 1 else max(V, logits.stride(0))
+    ld = logits.stride(0) if R > 1 else V
     if (V > 1 and logits.stride(1) != 1) or ld < V:
         raise ValueError("logits: each row must be contiguous, and the rows must not overlap")
-    f32, i32 = torch.float32, torch.int32
-    _call(logits, stream, "mtp_head_sample", logits.data_ptr(),
-          LOGITS_BF16 if logits.dtype == torch.bfloat16 else LOGITS_FP32, ld,
-          _t(temperature, "temperature", f32, (R,), True, logits), _t(top_k, "top_k", i32, (R,), True, logits),
-          _t(top_p, "top_p", f32, (R,), True, logits), _t(min_p, "min_p", f32, (R,), True, logits),
-          _t(u, "u", f32, (R,), True, logits), _t(token, "token", i32, (R,), True, logits),
-          _t(prob, "prob", f32, (R,), True, logits), _t(probs, "probs", f32, (R, V), True, logits),
-          _status(status, logits), R, V)
+    r = (R,)
+    _call(dev, stream, "mtp_head_sample", logits.data_ptr(), LOGITS_BF16 if logits.dtype is _BF16 else LOGITS_FP32, ld,
+          _t(temperature, "temperature", _F32, r, dev, True), _t(top_k, "top_k", _I32, r, dev, True),
+          _t(top_p, "top_p", _F32, r, dev, True), _t(min_p, "min_p", _F32, r, dev, True), _t(u, "u", _F32, r, dev, True),
+          _t(token, "token", _I32, r, dev, True), _t(prob, "prob", _F32, r, dev, True),
+          _t(probs, "probs", _F32, (R, V), dev, True), _t(status, "status", _I32, (1,), dev, True), R, V)
 
 
 def mtp_head_verify(target_probs, draft_probs, draft_tokens, u, tokens, accepted, prob=None, draft_len=None,
                     status=None, stream=None) -> None:
     """Drafts [B, D] accepted against target_probs [B, D + 1, V]; draft_probs [B, D, V], or None for
     greedy drafts. tokens [B, D + 1], accepted [B] and prob [B] (optional) are outputs."""
-    B, D1, V = _rank(target_probs, "target_probs", 3)
+    (B, D1, V), dev = _first(target_probs, "target_probs", 3)
     D = D1 - 1
-    f32, i32 = torch.float32, torch.int32
-    _call(target_probs, stream, "mtp_head_verify", _t(target_probs, "target_probs", f32, (B, D1, V)),
-          _t(draft_probs, "draft_probs", f32, (B, D, V), True, target_probs),
-          _t(draft_tokens, "draft_tokens", i32, (B, D), like=target_probs),
-          _t(draft_len, "draft_len", i32, (B,), True, target_probs), _t(u, "u", f32, (B, D1), like=target_probs),
-          _t(tokens, "tokens", i32, (B, D1), like=target_probs), _t(accepted, "accepted", i32, (B,), like=target_probs),
-          _t(prob, "prob", f32, (B,), True, target_probs), _status(status, target_probs), B, D, V)
+    _call(dev, stream, "mtp_head_verify", _t(target_probs, "target_probs", _F32, (B, D1, V), dev),
+          _t(draft_probs, "draft_probs", _F32, (B, D, V), dev, True), _t(draft_tokens, "draft_tokens", _I32, (B, D), dev),
+          _t(draft_len, "draft_len", _I32, (B,), dev, True), _t(u, "u", _F32, (B, D1), dev),
+          _t(tokens, "tokens", _I32, (B, D1), dev), _t(accepted, "accepted", _I32, (B,), dev),
+          _t(prob, "prob", _F32, (B,), dev, True), _t(status, "status", _I32, (1,), dev, True), B, D, V)
