@@ -4,8 +4,8 @@
 //
 // The codes without a division per element, as in the FP8 quantiser (quantize.cu): with
 // r = 1 / (s_j rs), formed in fp32, the products |w| r (1 + 2^-21) and |w| r (1 - 2^-21) bracket
-// the real quotient strictly (s_j rs, its reciprocal, the factor and the product round by at most
-// 2^-24 each, together less than 2^-21). The conversion is monotonic, so equal codes of both
+// the real quotient strictly (s_j rs, the factor and the product round by at most 2^-24 each, the
+// approximate reciprocal errs by at most 2^-23: together less than 2^-21). The conversion is monotonic, so equal codes of both
 // bracket ends are the code of the quotient. Otherwise one rounding boundary b lies inside the
 // bracket and the sign of |w| - (b s_j) rs decides: b s_j has 7 significant bits and is exact, so
 // one fused multiply-add gives that sign exactly (zero: a tie, to the even code). It comes up for
@@ -55,48 +55,70 @@ __device__ __forceinline__ float to_odd(double q) {
   return f;
 }
 
-// E4M3 code of amax / (6 rs), rs > 0.
-__device__ __forceinline__ uint32_t block_scale_code(float amax, float rs, float r6_up, float r6_dn) {
-  if (rs >= kSmallRs) {
-    const uint32_t two = e4m3x2(__fmul_rn(amax, r6_dn), __fmul_rn(amax, r6_up));
-    const uint32_t c = two & 0xFFu;  // the lower end; the upper is c or c + 1
-    if (c == two >> 8) return c;
-    const float b6 = 3.0f * (e4m3_value(c) + e4m3_value(c + 1));  // 6 * the midpoint, exact
-    const float d = __fmaf_rn(-b6, rs, amax);
-    return c + ((d > 0.0f || (d == 0.0f && (c & 1u))) ? 1u : 0u);
-  }
-  return e4m3x2(to_odd(static_cast<double>(amax) / (6.0 * static_cast<double>(rs))), 0.0f) & 0xFFu;
+// 1 / x within 2^-23 of it, x and the result normal numbers.
+__device__ __forceinline__ float recip(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// Eight codes of the BF16 pairs u[0..3] for the block scale value s (> 0) and row scale rs.
-__device__ __forceinline__ uint32_t codes8(const uint32_t (&u)[4], float s, float rs, float r_up, float r_dn) {
-  float a[8];
-  if (rs >= kSmallRs) {
-#pragma unroll
-    for (int t = 0; t < 8; ++t) a[t] = __fmul_rn((t & 1) ? bf16_hi(u[t >> 1]) : bf16_lo(u[t >> 1]), r_up);
-    const uint32_t up = e2m1x8(a);
-#pragma unroll
-    for (int t = 0; t < 8; ++t) a[t] = __fmul_rn((t & 1) ? bf16_hi(u[t >> 1]) : bf16_lo(u[t >> 1]), r_dn);
-    uint32_t dn = e2m1x8(a);
-    uint32_t diff = up ^ dn;
-    while (diff != 0u) {  // the codes on either side of a boundary differ in their low three bits
-      const int t = (__ffs(diff) - 1) >> 2;
-      diff &= ~(0xFu << (4 * t));
-      const uint32_t c = (dn >> (4 * t)) & 7u;
-      // midpoint above code c: 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, as quarters in nibbles
-      const float mid = 0.25f * static_cast<float>((0x14EA7531ull >> (4 * c)) & (c == 6u ? 0x1Fu : 0xFu));
-      const uint32_t pair = t < 4 ? (t < 2 ? u[0] : u[1]) : (t < 6 ? u[2] : u[3]);
-      const float f = fabsf((t & 1) ? bf16_hi(pair) : bf16_lo(pair));
-      const float d = __fmaf_rn(-(mid * s), rs, f);
-      if (d > 0.0f || (d == 0.0f && (c & 1u))) dn += 1u << (4 * t);
-    }
-    return dn;
-  }
+// The quotients in fp64, for rows with a scale below kSmallRs. (Out of line, in block_codes_fp64: inlined,
+// their conversions were executed for every block, on an fp64 pipe that was busy a third of the time.)
+__device__ __forceinline__ uint32_t block_scale_code_fp64(float amax, float rs) {
+  return e4m3x2(to_odd(static_cast<double>(amax) / (6.0 * static_cast<double>(rs))), 0.0f) & 0xFFu;
+}
+__device__ __forceinline__ uint32_t codes8_fp64(uint4 u, float s, float rs) {
   const double d = static_cast<double>(s) * static_cast<double>(rs);  // exact: 4 + 24 bits
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float a[8];
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
-    a[t] = to_odd(static_cast<double>((t & 1) ? bf16_hi(u[t >> 1]) : bf16_lo(u[t >> 1])) / d);
+  for (int t = 0; t < 8; ++t) a[t] = to_odd(static_cast<double>((t & 1) ? bf16_hi(w[t >> 1]) : bf16_lo(w[t >> 1])) / d);
   return e2m1x8(a);
+}
+
+// E4M3 code of amax / (6 rs), rs >= kSmallRs.
+__device__ __forceinline__ uint32_t block_scale_code(float amax, float rs, float r6_up, float r6_dn) {
+  const uint32_t two = e4m3x2(__fmul_rn(amax, r6_dn), __fmul_rn(amax, r6_up));
+  const uint32_t c = two & 0xFFu;  // the lower end; the upper is c or c + 1
+  if (c == two >> 8) return c;
+  const float b6 = 3.0f * (e4m3_value(c) + e4m3_value(c + 1));  // 6 * the midpoint, exact
+  const float d = __fmaf_rn(-b6, rs, amax);
+  return c + ((d > 0.0f || (d == 0.0f && (c & 1u))) ? 1u : 0u);
+}
+
+// Eight codes of the BF16 pairs u[0..3] for the block scale value s (> 0) and row scale rs >= kSmallRs.
+__device__ __forceinline__ uint32_t codes8(const uint32_t (&u)[4], float s, float rs, float r_up, float r_dn) {
+  const uint64_t up2 = f2_pack(r_up, r_up), dn2 = f2_pack(r_dn, r_dn);
+  float a[8];
+  uint64_t f2[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    f2[t] = bf16x2_to_f2(u[t]);
+    const uint64_t y = f2_mul(f2[t], up2);
+    a[2 * t] = f2_lo(y);
+    a[2 * t + 1] = f2_hi(y);
+  }
+  const uint32_t up = e2m1x8(a);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint64_t y = f2_mul(f2[t], dn2);
+    a[2 * t] = f2_lo(y);
+    a[2 * t + 1] = f2_hi(y);
+  }
+  uint32_t dn = e2m1x8(a);
+  uint32_t diff = up ^ dn;
+  while (diff != 0u) {  // the codes on either side of a boundary differ in their low three bits
+    const int t = (__ffs(diff) - 1) >> 2;
+    diff &= ~(0xFu << (4 * t));
+    const uint32_t c = (dn >> (4 * t)) & 7u;
+    // midpoint above code c: 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, as quarters in nibbles
+    const float mid = 0.25f * static_cast<float>((0x14EA7531ull >> (4 * c)) & (c == 6u ? 0x1Fu : 0xFu));
+    const uint32_t pair = t < 4 ? (t < 2 ? u[0] : u[1]) : (t < 6 ? u[2] : u[3]);
+    const float f = fabsf((t & 1) ? bf16_hi(pair) : bf16_lo(pair));
+    const float d = __fmaf_rn(-(mid * s), rs, f);
+    if (d > 0.0f || (d == 0.0f && (c & 1u))) dn += 1u << (4 * t);
+  }
+  return dn;
 }
 
 // max of the two 16-bit halves, lane by lane
@@ -131,6 +153,45 @@ __device__ __forceinline__ void load16(const uint16_t* row, int k0, int k, uint4
     b = make_uint4(u[4], u[5], u[6], u[7]);
   }
 }
+
+// The scale and codes of one block of 16 columns.
+struct BlockCodes {
+  uint32_t c0, c1, sc;
+};
+__device__ __noinline__ uint4 block_codes_fp64(uint4 u0, uint4 u1, float amax, float rs) {
+  const uint32_t sc = block_scale_code_fp64(amax, rs);
+  if (sc == 0u) return make_uint4(0u, 0u, 0u, 0u);
+  const float s = e4m3_value(sc);
+  return make_uint4(codes8_fp64(u0, s, rs), codes8_fp64(u1, s, rs), sc, 0u);
+}
+__device__ __forceinline__ BlockCodes block_codes(const uint4& u0, const uint4& u1, float rs, float r6_up, float r6_dn) {
+  BlockCodes o{0u, 0u, 0u};
+  const uint32_t bm = mag_max(mag_max(0u, u0), u1);
+  const float amax = bf16_bits_to_f32(max(bm & 0xFFFFu, bm >> 16));
+  if (rs < kSmallRs) {
+    const uint4 v = block_codes_fp64(u0, u1, amax, rs);
+    return BlockCodes{v.x, v.y, v.z};
+  }
+  o.sc = block_scale_code(amax, rs, r6_up, r6_dn);
+  if (o.sc != 0u) {
+    const float s = e4m3_value(o.sc);
+    const float r = recip(__fmul_rn(s, rs));
+    const float r_up = __fmul_rn(r, kUp), r_dn = __fmul_rn(r, kDn);
+    o.c0 = codes8({u0.x, u0.y, u0.z, u0.w}, s, rs, r_up, r_dn);
+    o.c1 = codes8({u1.x, u1.y, u1.z, u1.w}, s, rs, r_up, r_dn);
+  }
+  return o;
+}
+
+// First scale byte of a row, and the distance of scale byte b from it (fp4.h).
+__device__ __forceinline__ uint8_t* scale_row(uint8_t* bs, int64_t row, int kp, int tile) {
+  if (tile == 0) return bs + row * (kp / kFp4Block);
+  const int64_t tl = row / tile;
+  const int lr = static_cast<int>(row - tl * tile);
+  const int64_t chunk = tl * ((tile + 127) / 128) + lr / 128;
+  return bs + chunk * (kp / 64) * 512 + (lr & 31) * 16 + ((lr & 127) >> 5) * 4;
+}
+__device__ __forceinline__ int scale_at(int b, int tile) { return tile > 0 ? (b >> 2) * 512 + (b & 3) : b; }
 
 // TPR threads of a block (a warp, or the whole block) per row, two passes over it: the magnitude
 // maximum, then 16 columns (one block scale) a thread at a time.
@@ -174,87 +235,193 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t*
       rs = 0.0f;
     }
     if (t == 0) rs_out[row] = rs;
-    const float r6 = rs >= kSmallRs ? __frcp_rn(__fmul_rn(6.0f, rs)) : 0.0f;
+    const float r6 = rs >= kSmallRs ? recip(__fmul_rn(6.0f, rs)) : 0.0f;
     const float r6_up = __fmul_rn(r6, kUp), r6_dn = __fmul_rn(r6, kDn);
     uint8_t* qr = q + row * (kp / 2);
-    uint8_t* br = bs + row * nblk;
-    if (tile > 0) { // the first scale byte of this row in the linear's order (fp4.h)
-      const int64_t tl = row / tile;
-      const int lr = static_cast<int>(row - tl * tile);
-      const int64_t chunk = tl * ((tile + 127) / 128) + lr / 128;
-      br = bs + chunk * (kp / 64) * 512 + (lr & 31) * 16 + ((lr & 127) >> 5) * 4;
-    }
+    uint8_t* br = scale_row(bs, row, kp, tile);
     for (int b = t; b < nblk; b += TPR) {
-      uint32_t c0 = 0u, c1 = 0u, sc = 0u;
+      BlockCodes o{0u, 0u, 0u};
       if (rs > 0.0f && b * kFp4Block < k) {
         uint4 u0, u1;
         load16<VEC>(wr, b * kFp4Block, k, u0, u1);
-        const uint32_t bm = mag_max(mag_max(0u, u0), u1);
-        sc = block_scale_code(bf16_bits_to_f32(max(bm & 0xFFFFu, bm >> 16)), rs, r6_up, r6_dn);
-        if (sc != 0u) {
-          const float s = e4m3_value(sc);
-          const float r = rs >= kSmallRs ? __frcp_rn(__fmul_rn(s, rs)) : 0.0f;
-          const float r_up = __fmul_rn(r, kUp), r_dn = __fmul_rn(r, kDn);
-          c0 = codes8({u0.x, u0.y, u0.z, u0.w}, s, rs, r_up, r_dn);
-          c1 = codes8({u1.x, u1.y, u1.z, u1.w}, s, rs, r_up, r_dn);
-        }
+        o = block_codes(u0, u1, rs, r6_up, r6_dn);
       }
-      reinterpret_cast<uint2*>(qr)[b] = make_uint2(c0, c1);
-      br[tile > 0 ? (b >> 2) * 512 + (b & 3) : b] = static_cast<uint8_t>(sc);
+      reinterpret_cast<uint2*>(qr)[b] = make_uint2(o.c0, o.c1);
+      br[scale_at(b, tile)] = static_cast<uint8_t>(o.sc);
     }
   }
 }
 
-// bf16( fp32( code * s_j * rs ) ), 16 columns (one block scale) a thread. Idx: 32 bits when they
-// number the blocks of the whole matrix (a 64-bit division a thread cost a third of the time).
-template <bool VEC, class Idx>
+// Rows that TPR threads hold in registers, kHeld blocks of 16 columns a thread: one read of the matrix.
+// TPR = 32: a warp per row, eight rows a CTA; otherwise a CTA per row. Threads per SM over registers per
+// thread: at H = 6144, V = 154880 768 threads (80 registers) took 516 us, 1,024 (64) 473, 1,280 (48, a few
+// spilled) 458: 5.3 TB/s of bytes read and written; the two-pass kernel below 539.
+constexpr int kHeld = 3;
+template <int TPR>
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, (TPR == 128 || TPR == 256 ? 1280 : 1024) / (TPR == 32 ? 256 : TPR))
+    fp4_quantize_held_kernel(const uint16_t* __restrict__ w, uint8_t* __restrict__ q, uint8_t* __restrict__ bs,
+                             float* __restrict__ rs_out, int32_t* __restrict__ status, const int32_t* __restrict__ valid,
+                             int rows, int k, int tile) {
+  constexpr int kThreads = TPR == 32 ? 256 : TPR;
+  __shared__ uint32_t red[2][kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = threadIdx.x % TPR;
+  const int kp = fp4_padded(k), nblk = kp / kFp4Block;
+  pdl_wait_prior_grid();
+  // The next kernel may launch at once (what it reads before its own wait, a linear's weights, was
+  // written before this grid's wait ended).
+  pdl_launch_dependents();
+  int turn = 0;
+  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / TPR; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * kThreads / TPR) {
+    const uint4* wr = reinterpret_cast<const uint4*>(w + row * k);  // k % 8 == 0
+    const bool ok = valid == nullptr || valid[row] != 0;
+    uint4 u[kHeld][2];
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int p = 2 * (t + i * TPR);  // 8-column piece
+      u[i][0] = ok && 8 * p < k ? __ldcs(wr + p) : z;
+      u[i][1] = ok && 8 * p + 8 < k ? __ldcs(wr + p + 1) : z;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) m = mag_max(mag_max(m, u[i][0]), u[i][1]);
+    uint32_t mx = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    if constexpr (TPR > 32) {
+      if (lane == 0) red[turn][warp] = mx;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) mx = max(mx, red[turn][i]);
+      turn ^= 1;  // the next row's maxima go elsewhere: one barrier a row is enough
+    }
+    float rs = __fdiv_rn(bf16_bits_to_f32(mx), 2688.0f);
+    if (mx >= 0x7F80u) {  // a NaN or Inf in the row
+      if (t == 0) store_status(status, MTP_ERR_NONFINITE);
+      rs = 0.0f;
+    }
+    if (t == 0) rs_out[row] = rs;
+    const float r6 = rs >= kSmallRs ? recip(__fmul_rn(6.0f, rs)) : 0.0f;
+    const float r6_up = __fmul_rn(r6, kUp), r6_dn = __fmul_rn(r6, kDn);
+    uint2* qr = reinterpret_cast<uint2*>(q + row * (kp / 2));
+    uint8_t* br = scale_row(bs, row, kp, tile);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int b = t + i * TPR;
+      if (b < nblk) {
+        BlockCodes o{0u, 0u, 0u};
+        if (rs > 0.0f) o = block_codes(u[i][0], u[i][1], rs, r6_up, r6_dn);
+        qr[b] = make_uint2(o.c0, o.c1);
+        br[scale_at(b, tile)] = static_cast<uint8_t>(o.sc);
+      }
+    }
+  }
+}
+
+// bf16( fp32( code * s_j * rs ) ): eight columns (a 4-byte load, a 16-byte store) a thread, kUnits at a
+// time, neighbouring lanes neighbouring columns. per_row: eights of a row; magic = floor(2^64 / per_row) + 1
+// (its product with a 32-bit number has the quotient in the upper half).
+constexpr int kUnits = 4;
+__global__ void __launch_bounds__(kQThreads) fp4_dequantize_vec_kernel(const Fp4Matrix m, uint16_t* __restrict__ w,
+                                                                       uint32_t total, uint32_t per_row,
+                                                                       unsigned long long magic, int kp) {
+  pdl_wait_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const uint64_t step = static_cast<uint64_t>(gridDim.x) * kQThreads * kUnits;
+  for (uint64_t i0 = (static_cast<uint64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5)) * 32 * kUnits + lane; i0 < total;
+       i0 += step) {
+    uint32_t c[kUnits], s[kUnits];
+    float rs[kUnits];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+      const uint64_t i = i0 + 32 * j;
+      if (i < total) {
+        const uint32_t row = static_cast<uint32_t>(__umul64hi(i, magic)), b = static_cast<uint32_t>(i) - row * per_row;
+        c[j] = __ldcs(reinterpret_cast<const uint32_t*>(m.q + static_cast<size_t>(row) * (kp / 2)) + b);
+        s[j] = m.bs[static_cast<size_t>(row) * (kp / kFp4Block) + (b >> 1)];
+        rs[j] = m.rs[row];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+      const uint64_t i = i0 + 32 * j;
+      if (i < total) {
+        const uint32_t s2 = e4m3x2_to_f16x2(s[j] * 0x0101u);
+        uint32_t v[4], o[4];
+        e2m1x8_to_f16x2x4(c[j], v);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t p = f16x2_mul(v[t], s2);  // exact
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+              : "=r"(o[t])
+              : "f"(__fmul_rn(f16_hi(p), rs[j])), "f"(__fmul_rn(f16_lo(p), rs[j])));
+        }
+        __stcs(reinterpret_cast<uint4*>(w) + i, make_uint4(o[0], o[1], o[2], o[3]));
+      }
+    }
+  }
+  // (no early launch: a sweep that follows may read w, as its lm_head, before its own wait)
+}
+
+// The same for rows that are not made of eights: 16 columns (one block scale) a thread.
 __global__ void __launch_bounds__(kQThreads) fp4_dequantize_kernel(const Fp4Matrix m, uint16_t* __restrict__ w, int rows,
                                                                    int k) {
   const int kp = fp4_padded(k), nblk = (k + kFp4Block - 1) / kFp4Block;
-  const Idx total = static_cast<Idx>(rows) * static_cast<Idx>(nblk), step = static_cast<Idx>(gridDim.x) * kQThreads;
+  const int64_t total = static_cast<int64_t>(rows) * nblk;
   pdl_wait_prior_grid();
-  for (Idx i = static_cast<Idx>(blockIdx.x) * kQThreads + threadIdx.x; i < total; i += step) {
-    const Idx r = i / static_cast<Idx>(nblk);
-    const int64_t row = static_cast<int64_t>(r);
-    const int b = static_cast<int>(i - r * static_cast<Idx>(nblk));
-    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(m.q + row * (kp / 2)) + b);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kQThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kQThreads) {
+    const int64_t row = i / nblk;
+    const int b = static_cast<int>(i - row * nblk);
+    const uint2 c = reinterpret_cast<const uint2*>(m.q + row * (kp / 2))[b];
     const uint32_t s2 = e4m3x2_to_f16x2(m.bs[row * (kp / kFp4Block) + b] * 0x0101u);
     const float rs = m.rs[row];
-    uint32_t o[8];
+    uint16_t* dst = w + row * k + b * kFp4Block;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t v[4];
       e2m1x8_to_f16x2x4(h == 0 ? c.x : c.y, v);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t p = f16x2_mul(v[t], s2);  // exact
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-            : "=r"(o[4 * h + t])
-            : "f"(__fmul_rn(f16_hi(p), rs)), "f"(__fmul_rn(f16_lo(p), rs)));
+      for (int t = 0; t < 8; ++t) {
+        const uint32_t p = f16x2_mul(v[t >> 1], s2);  // exact
+        if (b * kFp4Block + 8 * h + t < k)
+          dst[8 * h + t] = static_cast<uint16_t>(bf16_bits_rn(__fmul_rn((t & 1) ? f16_hi(p) : f16_lo(p), rs)));
       }
     }
-    uint16_t* dst = w + row * k + b * kFp4Block;
-    if constexpr (VEC) {
-      __stcs(reinterpret_cast<uint4*>(dst), make_uint4(o[0], o[1], o[2], o[3]));
-      if (b * kFp4Block + 8 < k) __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(o[4], o[5], o[6], o[7]));
-    } else {
-#pragma unroll
-      for (int t = 0; t < 16; ++t)
-        if (b * kFp4Block + t < k) dst[t] = static_cast<uint16_t>(o[t >> 1] >> (16 * (t & 1)));
-    }
-    if (total - i <= step) break;  // the next index would pass the end (and may not fit Idx)
   }
-  // (no early launch: a sweep that follows may read w, as its lm_head, before its own wait)
 }
 
 }  // namespace
 
+namespace {
+
+template <int TPR>
+cudaError_t launch_held(const DeviceInfo& di, int rows, cudaStream_t stream, void** args) {
+  constexpr int kThreads = TPR == 32 ? 256 : TPR;
+  const int64_t blocks = (static_cast<int64_t>(rows) * TPR + kThreads - 1) / kThreads;
+  const int64_t cap = static_cast<int64_t>(di.sm_count) * (2048 / kThreads);
+  return launch_pdl(reinterpret_cast<const void*>(fp4_quantize_held_kernel<TPR>),
+                    dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(kThreads), 0, stream, args);
+}
+
+}  // namespace
+
+// Rows of up to 512 * kHeld blocks of 16 columns (24,576 columns) are held in the registers of as few
+// threads as hold them; longer ones, and rows that are not made of 16-byte pieces, take two passes.
 cudaError_t launch_fp4_quantize(const uint16_t* w, uint8_t* q, uint8_t* bs, float* rs, int32_t* status,
                                 const int32_t* valid, int rows, int k, cudaStream_t stream, int tile) {
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   const bool vec = k % 8 == 0;
+  const int nblk = fp4_padded(k) / kFp4Block;
+  void* args[] = {&w, &q, &bs, &rs, &status, &valid, &rows, &k, &tile};
+  if (vec) {
+    if (nblk <= 32 * kHeld) return launch_held<32>(di, rows, stream, args);
+    if (nblk <= 128 * kHeld) return launch_held<128>(di, rows, stream, args);
+    if (nblk <= 256 * kHeld) return launch_held<256>(di, rows, stream, args);
+    if (nblk <= 512 * kHeld) return launch_held<512>(di, rows, stream, args);
+  }
   const bool wide = rows < di.sm_count * 8;  // fewer rows than warps in flight: a block per row
   const void* kern = wide ? (vec ? reinterpret_cast<const void*>(fp4_quantize_kernel<kQThreads, true>)
                                  : reinterpret_cast<const void*>(fp4_quantize_kernel<kQThreads, false>))
@@ -263,7 +430,6 @@ cudaError_t launch_fp4_quantize(const uint16_t* w, uint8_t* q, uint8_t* bs, floa
   const int per_block = wide ? 1 : kQThreads / 32;
   int64_t blocks = (static_cast<int64_t>(rows) + per_block - 1) / per_block;
   if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
-  void* args[] = {&w, &q, &bs, &rs, &status, &valid, &rows, &k, &tile};
   return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0, stream, args);
 }
 
@@ -271,18 +437,27 @@ cudaError_t launch_fp4_dequantize(const Fp4Matrix& m, uint16_t* w, int rows, int
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
-  const bool vec = k % 8 == 0;
+  Fp4Matrix mm = m;
+  const int64_t eights = static_cast<int64_t>(rows) * (k / 8);
+  if (k % 8 == 0 && eights < (static_cast<int64_t>(1) << 32)) {
+    uint32_t total = static_cast<uint32_t>(eights), per_row = static_cast<uint32_t>(k / 8);
+    // (one eight a row: the quotient is the number itself, 2^64 does not fit)
+    unsigned long long magic = per_row == 1 ? 0ull : ~0ull / per_row + 1;
+    int kp = fp4_padded(k);
+    if (per_row > 1) {
+      int64_t blocks = (eights + kQThreads * kUnits - 1) / (kQThreads * kUnits);
+      if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
+      void* args[] = {&mm, &w, &total, &per_row, &magic, &kp};
+      return launch_pdl(reinterpret_cast<const void*>(fp4_dequantize_vec_kernel), dim3(static_cast<unsigned>(blocks)),
+                        dim3(kQThreads), 0, stream, args);
+    }
+  }
   const int64_t total = static_cast<int64_t>(rows) * ((k + kFp4Block - 1) / kFp4Block);
   int64_t blocks = (total + kQThreads - 1) / kQThreads;
   if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
-  Fp4Matrix mm = m;
-  const bool small = total < (static_cast<int64_t>(1) << 32);
   void* args[] = {&mm, &w, &rows, &k};
-  const void* kern = vec ? (small ? reinterpret_cast<const void*>(fp4_dequantize_kernel<true, uint32_t>)
-                                  : reinterpret_cast<const void*>(fp4_dequantize_kernel<true, uint64_t>))
-                         : (small ? reinterpret_cast<const void*>(fp4_dequantize_kernel<false, uint32_t>)
-                                  : reinterpret_cast<const void*>(fp4_dequantize_kernel<false, uint64_t>));
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0, stream, args);
+  return launch_pdl(reinterpret_cast<const void*>(fp4_dequantize_kernel), dim3(static_cast<unsigned>(blocks)),
+                    dim3(kQThreads), 0, stream, args);
 }
 
 }  // namespace mtp
