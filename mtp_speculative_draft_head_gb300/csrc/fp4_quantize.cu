@@ -252,6 +252,16 @@ __global__ void __launch_bounds__(kQThreads) fp4_quantize_kernel(const uint16_t*
   }
 }
 
+// A read-once load that stays in front of what follows.
+__device__ __forceinline__ uint4 ld_now(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // Rows that TPR threads hold in registers, kHeld blocks of 16 columns a thread: one read of the matrix.
 // TPR = 32: a warp per row, eight rows a CTA; otherwise a CTA per row. Threads per SM over registers per
 // thread: at H = 6144, V = 154880 768 threads (80 registers) took 516 us, 1,024 (64) 473, 1,280 (48, a few
@@ -268,10 +278,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, (TPR == 128 || TPR == 2
   const int t = threadIdx.x % TPR;
   const int kp = fp4_padded(k), nblk = kp / kFp4Block;
   pdl_wait_prior_grid();
-  // The next kernel may launch at once (what it reads before its own wait, a linear's weights, was
-  // written before this grid's wait ended).
-  pdl_launch_dependents();
   int turn = 0;
+  bool first = true;
   for (int64_t row = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / TPR; row < rows;
        row += static_cast<int64_t>(gridDim.x) * kThreads / TPR) {
     const uint4* wr = reinterpret_cast<const uint4*>(w + row * k);  // k % 8 == 0
@@ -281,9 +289,14 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, (TPR == 128 || TPR == 2
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int p = 2 * (t + i * TPR);  // 8-column piece
-      u[i][0] = ok && 8 * p < k ? __ldcs(wr + p) : z;
-      u[i][1] = ok && 8 * p + 8 < k ? __ldcs(wr + p + 1) : z;
+      u[i][0] = u[i][1] = z;
+      if (ok && 8 * p < k) u[i][0] = ld_now(wr + p);
+      if (ok && 8 * p + 8 < k) u[i][1] = ld_now(wr + p + 1);
     }
+    // The next kernel may launch once the first rows are asked for (so that a linear's weight stream does not
+    // get in front of them); what it reads before its own wait was written before this grid's wait ended.
+    if (first) pdl_launch_dependents();
+    first = false;
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) m = mag_max(mag_max(m, u[i][0]), u[i][1]);

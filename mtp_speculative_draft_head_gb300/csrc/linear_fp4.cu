@@ -54,7 +54,8 @@ struct LTile {
   static constexpr int kStageBytes = kABytes + kBBytes + kSfChunk * (1 + kChunks);
   static constexpr int kFit = (206 * 1024) / kStageBytes;
   static constexpr int kStages = kFit < 9 ? kFit : 9;
-  static constexpr uint32_t kSfaCol = 2 * NT;                  // after the two accumulators
+  // after the two accumulators; an MMA takes the scales from an address that is a multiple of four columns
+  static constexpr uint32_t kSfaCol = 2 * NT;
   static constexpr uint32_t kSfbCol = kSfaCol + 16;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 4) * 8 + 16 + 4 * NT * 4;
   static_assert(NT % 16 == 0 && NT <= 256, "N of an M = 128 MMA");
@@ -73,7 +74,7 @@ struct LinearSched {
 struct LinearParams {
   const uint8_t* w_bs;   // [N, kp / 16]
   const float* w_rs;     // [N]
-  const uint8_t* x_sf;   // workspace: [tiles of nt][chunks][kp / 64][512]
+  const uint8_t* x_sf;   // workspace: scales in operand order (fp4.h)
   const float* x_rs;     // workspace: [R]
   uint16_t* y;           // [R, N]
   int32_t* status;
@@ -469,8 +470,16 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const bool epi = warp >= 4;
     float* slots = reinterpret_cast<float*>(smem);
     bool done = true;
+    // the scales of the first CTA's epilogue, under the last MMAs
+    const int row = tile_row(t0) + 32 * q + lane, r0 = (t0 / c.mt) * NT;
+    float rw = 0.0f;
+    float* rx = rx_all + q * NT;
     if (epi) {
       pdl_wait_prior_grid();
+      if (rank == 0) {
+        if (row < p.N) rw = __ldg(p.w_rs + row);
+        load_rx(rx, r0);
+      }
       done = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_full[0]), 0));
       tmem_fence_after_sync();
       if (!done && lane == 0) give_up();
@@ -493,10 +502,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
     }
     cluster_barrier();
     if (epi && rank == 0 && !aborted()) {
-      const int row = tile_row(t0) + 32 * q + lane, r0 = (t0 / c.mt) * NT;
-      const float rw = row < p.N ? __ldg(p.w_rs + row) : 0.0f;
-      float* rx = rx_all + q * NT;
-      load_rx(rx, r0);
 #pragma unroll
       for (int c0 = 0; c0 < NT; c0 += 16) {
         if (r0 + c0 < p.R) {
