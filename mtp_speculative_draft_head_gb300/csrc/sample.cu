@@ -98,18 +98,6 @@ __device__ __forceinline__ u64 warp_inclusive(u64 v, int lane) {
 }
 
 // ------------------------------------------------------------------------------- numbers
-// v >= 0 as a fixed-point number with `frac` fraction bits (<= 62), to nearest; v < 2.
-__device__ __forceinline__ u64 to_fixed(float v, int frac) {
-  const uint32_t u = __float_as_uint(v);
-  const int e = static_cast<int>(u >> 23);  // sign bit is 0
-  if (e == 0) return 0ull;                  // below 2^-126
-  const u64 m = (u & 0x7FFFFFu) | 0x800000u;
-  const int sh = e - 150 + frac;  // v = m 2^(e - 150)
-  if (sh >= 0) return m << sh;
-  if (sh < -24) return 0ull;
-  return (m + (1ull << (-sh - 1))) >> -sh;
-}
-
 // floor(u * z) for u in [0, 1).
 __device__ __forceinline__ u64 scale_floor(float u, u64 z) {
   const uint32_t b = __float_as_uint(u);
@@ -238,38 +226,39 @@ struct Hist {
 };
 
 // ------------------------------------------------------------------------------- inverse of the cdf
-// The lowest index of the row whose cumulative mass exceeds floor(u z). Every warp owns `seg`
-// consecutive elements (a multiple of 32) of the slice that starts at i0; s.wsum holds this CTA's
-// per-warp masses, s.cta every CTA's. The one warp that finds it calls found(index). It passes over
-// its elements 128 at a time, and looks closer at the 128 that hold the target.
+// The lowest index of the row whose cumulative mass exceeds floor(u z). Every warp owns `seg` consecutive
+// elements of the slice that starts at i0 and ends by `end`; s.wsum holds this CTA's per-warp masses, s.cta
+// every CTA's. The CTA that has it goes once more over the one warp's elements, a few consecutive ones a
+// thread; the thread that finds it calls found(index). (By that warp alone, 128 elements at a time, this took
+// longer than the pass over the whole slice.)
 template <class MassFn, class Found>
-__device__ void locate(const Shared& s, uint32_t rank, u64 target, int64_t i0, int64_t seg, int64_t n, MassFn mass,
-                       Found found) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ void locate(Shared& s, uint32_t rank, u64 target, int64_t i0, int64_t seg, int64_t end, MassFn mass, Found found) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   u64 before = 0;
   for (uint32_t r = 0; r < rank; ++r) before += s.cta[r];
-  for (int w = 0; w < warp; ++w) before += s.wsum[w];
-  if (target < before || target - before >= s.wsum[warp]) return;
-  const int64_t end = i0 + (warp + 1) * seg < n ? i0 + (warp + 1) * seg : n;
-  for (int64_t j = i0 + warp * seg; j < end; j += 128) {
-    u64 m[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) m[q] = j + 32 * q + lane < end ? mass(j + 32 * q + lane) : 0ull;
-    const u64 all = warp_sum(m[0] + m[1] + m[2] + m[3]);
-    if (before + all <= target) {
-      before += all;
-      continue;
+  int w = 0;
+  if (target < before) return;  // an earlier CTA's
+  while (w < kW && target - before >= s.wsum[w]) before += s.wsum[w++];
+  if (w == kW) return;  // a later one's
+  const int64_t b0 = i0 + w * seg, b1 = b0 + seg < end ? b0 + seg : end;
+  const int64_t per = (seg + kT - 1) / kT;
+  const int64_t t0 = b0 + tid * per, t1 = t0 + per < b1 ? t0 + per : b1;
+  u64 sum = 0;
+#pragma unroll 8
+  for (int64_t i = t0; i < t1; ++i) sum += mass(i);
+  const u64 inc = warp_inclusive(sum, lane);
+  if (lane == 31) s.scan[warp] = inc;
+  __syncthreads();
+  before += inc - sum;
+  for (int q = 0; q < warp; ++q) before += s.scan[q];
+  if (target < before || target - before >= sum) return;
+  for (int64_t i = t0; i < t1; ++i) {
+    const u64 m = mass(i);
+    if (target - before < m) {
+      found(i);
+      return;
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const u64 c = warp_inclusive(m[q], lane);
-      const uint32_t hit = __ballot_sync(0xffffffffu, before + c > target);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) found(j + 32 * q + lane);
-        return;
-      }
-      before += __shfl_sync(0xffffffffu, c, 31);
-    }
+    before += m;
   }
 }
 
@@ -1037,10 +1026,14 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
     if (i < n) {
       x = a.draft_tokens[b * D + i];
       if (x >= 0 && x < V) {
-        const double u = a.u[b * (D + 1) + i];
-        const double p = a.target_probs[(b * (D + 1) + i) * V + x];
-        const double q = a.draft_probs ? a.draft_probs[(b * D + i) * V + x] : 1.0f;
-        ok = u * q < p;  // the product is exact in fp64
+        const float u = a.u[b * (D + 1) + i];
+        const float p = a.target_probs[(b * (D + 1) + i) * V + x];
+        const float q = a.draft_probs ? a.draft_probs[(b * D + i) * V + x] : 1.0f;
+        // u q < p exactly: the rounded product, and its error where it ties (in fp64, which is slow here, only
+        // where the error may leave the fp32 range)
+        const float h = __fmul_rn(u, q);
+        ok = h < p || (h == p && __fmaf_rn(u, q, -h) < 0.0f);
+        if (h < 1e-30f && p < 1e-30f) ok = static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p);
       }
     }
     const uint32_t no = __ballot_sync(0xffffffffu, !ok);
@@ -1057,29 +1050,57 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
   const bool all = acc == n;
   const float* p = a.target_probs + (b * (D + 1) + acc) * V;
   const float* q = !all && a.draft_probs ? a.draft_probs + (b * D + acc) * V : nullptr;
-  auto prob01 = [](float v) { return v > 0.0f ? (v < 1.0f ? v : 1.0f) : 0.0f; };
   bool plain = false;  // the residual is empty: the target's own row
   auto left_of = [&](float pv, float qv, int64_t i) -> float {
-    pv = prob01(pv);
-    if (plain || all) return pv;
     if (!q) qv = i == rejected_token ? 1.0f : 0.0f;
-    return prob01(__fsub_rn(pv, prob01(qv)));
+    qv = plain || all ? 0.0f : __saturatef(qv);  // (NaN saturates to 0)
+    return __saturatef(__fsub_rn(__saturatef(pv), qv));
   };
-  auto residual = [&](int64_t i) -> float { return left_of(p[i], q ? q[i] : 0.0f, i); };
+  auto mass_of = [&](float pv, float qv, int64_t i) -> u64 {
+    const uint32_t r = __float_as_uint(left_of(pv, qv, i));
+    // (a subnormal's mantissa gets a bit too much here, and rounds to nothing all the same)
+    return shift_round((r & 0x7FFFFFu) | 0x800000u, static_cast<int>(r >> 23) - 150 + frac);
+  };
+  auto residual = [&](int64_t i) -> float { return left_of(__ldg(p + i), q ? __ldg(q + i) : 0.0f, i); };
+  const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
   u64 z = 0ull;
   for (int pass = 0; pass < 2; ++pass) {
     u64 sum = 0ull;
-    constexpr int kBatch = 8;
-    const int64_t w1 = i0 + (warp + 1) * seg < i1 ? i0 + (warp + 1) * seg : i1;
-    for (int64_t i = i0 + warp * seg + lane; i < w1; i += 32 * kBatch) {
-      float pv[kBatch], qv[kBatch];
+    const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
+    // steps of 128 elements, two steps' loads under the work on the two before
+    auto load4 = [&](const float* row, int64_t i) {
+      if (wide && i + 4 <= w1) return __ldg(reinterpret_cast<const float4*>(row + i));
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = i + e < w1 ? __ldg(row + i + e) : 0.0f;
+      return make_float4(x[0], x[1], x[2], x[3]);
+    };
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int kBatch = 2;
+    float4 pn[kBatch], qn[kBatch];
+    auto fetch = [&](int64_t i) {
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        pv[j] = i + 32 * j < w1 ? __ldg(p + i + 32 * j) : 0.0f;
-        qv[j] = q && i + 32 * j < w1 ? __ldg(q + i + 32 * j) : 0.0f;
+        pn[j] = load4(p, i + 128 * j);
+        qn[j] = q ? load4(q, i + 128 * j) : none;
       }
+    };
+    fetch(w0 + 4 * lane);
+#pragma unroll 1
+    for (int64_t i = w0 + 4 * lane; i - 4 * lane < w1; i += 128 * kBatch) {
+      float4 pv[kBatch], qv[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) sum += to_fixed(left_of(pv[j], qv[j], i + 32 * j), frac);
+      for (int j = 0; j < kBatch; ++j) {
+        pv[j] = pn[j];
+        qv[j] = qn[j];
+      }
+      fetch(i + 128 * kBatch);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t at = i + 128 * j;  // (past the end the loads gave zeros)
+        sum += mass_of(pv[j].x, qv[j].x, at) + mass_of(pv[j].y, qv[j].y, at + 1) + mass_of(pv[j].z, qv[j].z, at + 2) +
+               mass_of(pv[j].w, qv[j].w, at + 3);
+      }
     }
     sum = warp_sum(sum);
     if (lane == 0) s.wsum[warp] = sum;
@@ -1112,7 +1133,7 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
   }
   if (z != 0ull)
     locate(s, rank, scale_floor(ud, z), i0, seg, i1,
-           [&](int64_t i) { return to_fixed(residual(i), frac); },
+           [&](int64_t i) { return mass_of(__ldg(p + i), q ? __ldg(q + i) : 0.0f, i); },
            [&](int64_t i) {
              a.tokens[b * (D + 1) + acc] = static_cast<int32_t>(i);
              if (a.prob)
@@ -1163,6 +1184,9 @@ cudaError_t launch_cluster(const void* kernel, unsigned grid, int nc, size_t sme
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
+// Largest slice that a CTA keeps in shared memory (227 KB of it).
+constexpr int64_t kHeldSlice = static_cast<int64_t>((227 * 1024 - kFixedSmem) / 4 / kSliceUnit * kSliceUnit);
+
 int64_t slice_of(int64_t V, int nc) { return ((V + nc - 1) / nc + kSliceUnit - 1) / kSliceUnit * kSliceUnit; }
 
 // Fraction bits of a mass: V weights of at most one stay below 2^62 (plus their roundings).
@@ -1172,11 +1196,33 @@ int mass_bits(int64_t V) {
   return 62 - lg;
 }
 
-// CTAs per row: as many (a power of two, up to kMaxC) as two CTAs on every SM allow, and no more than
-// give each warp a step.
-int cluster_size(int64_t rows, int64_t V, int sm_count) {
+// Whether a cluster of nc can be of use: each warp has more than a step of its own.
+bool worth(int64_t V, int nc) { return V > static_cast<int64_t>(nc) * kSliceUnit; }
+
+// CTAs per row of the sampler (a power of two up to kMaxC). Clusters of 16 as long as they all run at once:
+// with two CTAs on an SM 14 of them fit the GPU's SM groups. Without top_k each CTA's time is in the histogram's
+// shared-memory atomics, so the spread over more SMs still pays for a short second wave. Beyond that clusters of
+// four, all resident up to 36 rows, and for more rows the smallest that keep a slice in shared memory. At V =
+// 154880: 16 rows with top_k and top_p take 25.5 us with 16 CTAs, 26.8 with 8 and 20.6 with 4; with top_p alone
+// 53.5, 56.4 and 61.0; 24 rows 31.4, 28.0 and 20.9, and 71.6, 75.7 and 59.9; 80 rows 81, 74 and 54, and 199, 195
+// and 149. 160 rows of V = 32000 take 33.1 with one CTA and 39.3 with 4.
+int sample_cluster(int64_t rows, int64_t V, bool top_k) {
+  int nc = 4;
+  if (rows <= (top_k ? 14 : 18)) {
+    nc = kMaxC;
+  } else if (rows > 36) {
+    nc = 1;
+    while (nc < 4 && V > nc * kHeldSlice) nc *= 2;
+  }
+  while (nc > 1 && !worth(V, nc)) nc /= 2;
+  return nc;
+}
+
+// CTAs per sequence of the acceptance: one on each SM. 16 sequences at V = 154880 take 17.7 us with 16 CTAs each
+// (two waves), 14.8 with 8, 14.4 with 4; 80 at V = 32000 take 12.0 with one CTA and 14.5 with two.
+int verify_cluster(int64_t rows, int64_t V, int sm_count) {
   int nc = 1;
-  while (nc < kMaxC && rows * nc <= sm_count && V > static_cast<int64_t>(nc) * 2 * kSliceUnit) nc *= 2;
+  while (nc < kMaxC && rows * nc * 2 <= sm_count && worth(V, nc * 2)) nc *= 2;
   return nc;
 }
 
@@ -1187,12 +1233,9 @@ cudaError_t launch_sample(const SampleArgs& in, cudaStream_t stream) {
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   SampleArgs a = in;
-  int nc = cluster_size(a.R, a.V, di.sm_count);
+  int nc = sample_cluster(a.R, a.V, a.top_k != nullptr);
   int64_t slice = slice_of(a.V, nc);
-  // A slice is kept in shared memory where that leaves room for as many CTAs per SM as there are to run.
-  const size_t all_of_it = static_cast<size_t>(di.smem_optin);
-  const size_t limit = static_cast<int64_t>(a.R) * nc <= di.sm_count ? all_of_it : (all_of_it - 2048) / 2;
-  const bool res = kFixedSmem + static_cast<size_t>(slice) * 4 <= limit;
+  const bool res = slice <= kHeldSlice;
   int frac = mass_bits(a.V);
   const void* kern = a.bf16 ? (res ? reinterpret_cast<const void*>(sample_kernel<true, true>)
                                    : reinterpret_cast<const void*>(sample_kernel<true, false>))
@@ -1208,7 +1251,7 @@ cudaError_t launch_verify(const VerifyArgs& in, cudaStream_t stream) {
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   VerifyArgs a = in;
-  int nc = cluster_size(a.B, a.V, di.sm_count);
+  int nc = verify_cluster(a.B, a.V, di.sm_count);
   int64_t slice = slice_of(a.V, nc);
   int frac = mass_bits(a.V);
   void* args[] = {&a, &nc, &slice, &frac};
