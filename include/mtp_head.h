@@ -38,8 +38,9 @@
  *   - Shapes: 1 <= B <= 16, 1 <= H <= 65536, 1 <= V < 2^31, eps finite and >= 0.
  *   - Programmatic dependent launch: the input stage and the output stage are launched so that
  *     they may start streaming their weight matrix (eh_proj / lm_head) before the previous
- *     kernel on the stream has finished. They read tokens, target_hidden, x, the norm weights
- *     and the workspace only after it has finished. Do not write those two weight matrices in
+ *     kernel on the stream has finished; the FP4 output stage and the FP4 linear do so with their
+ *     copies. They read tokens, target_hidden, x, the norm weights
+ *     and the workspace only after it has finished. Do not write those weight matrices in
  *     a kernel that itself triggers early launch of its dependents.
  */
 #ifndef MTP_HEAD_H
@@ -451,7 +452,8 @@ size_t mtp_head_context_fp4_workspace_bytes(int R, int H); /* 0 for invalid shap
  * of all of those; of those, the ones with l_i >= m + temperature * ln(min_p). At least one is
  * kept. The token is the lowest index whose cumulative kept mass, in index order, exceeds u times
  * the whole. Masses are summed in 64-bit fixed point: results do not vary from run to run.
- * 1 <= R <= 65536, 1 <= V < 2^31. No workspace.
+ * 1 <= R <= 65536, 1 <= V < 2^31. No workspace. logits and probs need their elements' alignment only;
+ * probs must not overlap logits (MTP_ERR_ARG).
  * ---------------------------------------------------------------------------------------- */
 enum { MTP_LOGITS_FP32 = 0, MTP_LOGITS_BF16 = 1 };
 
@@ -485,7 +487,8 @@ int mtp_head_sample(const void* logits, int logits_dtype, int64_t ld, const floa
  * and prob 0. A draft outside [0, V) that is reached is rejected (MTP_ERR_TOKEN_RANGE); a sequence
  * with draft_len outside 0..D, or u outside [0, 1) at any i < n or at D, gives accepted 0, tokens -1
  * and prob 0 (MTP_ERR_ARG).
- * 1 <= B <= 65536, 1 <= D <= 1024, 1 <= V < 2^31. No workspace. `tokens` must not overlap the inputs.
+ * 1 <= B <= 65536, 1 <= D <= 1024, 1 <= V < 2^31. No workspace. `tokens` must not overlap
+ * draft_tokens (MTP_ERR_ARG).
  * ---------------------------------------------------------------------------------------- */
 int mtp_head_verify(const float* target_probs, const float* draft_probs,
                     const int32_t* draft_tokens, const int32_t* draft_len, const float* u,
@@ -501,7 +504,7 @@ int mtp_head_verify(const float* target_probs, const float* draft_probs,
  * the workspace is left ready for the next call. Default 2 s (2000000000 ns), far above any
  * real wait. The limit applies to the output-stage kernels (every batch size) and to the
  * single-sequence input stage, launched after this call (a CUDA graph keeps the limit it was
- * recorded with); the batched input stage and the context-row kernels always use 2 s, and so
+ * recorded with); the batched input stage, the context-row kernels and the FP4 linear always use 2 s, and so
  * does every wait for a kernel's own copies before it exits. Process-wide; returns the previous
  * limit. A short limit (a few ns: the device clock it is compared with advances about once a
  * microsecond) makes the waits that find their data missing run out; ns = 0 makes every stage

@@ -28,6 +28,9 @@ int mtp_head_sample(const void* logits, int logits_dtype, int64_t ld, const floa
   if (!aligned(logits, logits_dtype == MTP_LOGITS_FP32 ? 4 : 2) || bad4(temperature) || bad4(top_k) || bad4(top_p) ||
       bad4(min_p) || bad4(u) || bad4(token) || bad4(prob) || bad4(probs) || bad4(status))
     return MTP_ERR_ALIGN;
+  // (the rows are read more than once)
+  const size_t item = logits_dtype == MTP_LOGITS_FP32 ? 4 : 2;
+  if (overlap(logits, (static_cast<size_t>(R - 1) * ld + V) * item, probs, static_cast<size_t>(R) * V * 4)) return MTP_ERR_ARG;
   return guarded([&] {
     SampleArgs a{logits, temperature, top_k, top_p, min_p, u, token, prob, probs, status, ld, R, V,
                  logits_dtype == MTP_LOGITS_BF16};
@@ -43,6 +46,8 @@ int mtp_head_verify(const float* target_probs, const float* draft_probs, const i
   if (!aligned(target_probs, 4) || bad4(draft_probs) || !aligned(draft_tokens, 4) || bad4(draft_len) ||
       !aligned(u, 4) || !aligned(tokens, 4) || !aligned(accepted, 4) || bad4(prob) || bad4(status))
     return MTP_ERR_ALIGN;
+  const size_t b = static_cast<size_t>(B);
+  if (overlap(tokens, b * (D + 1) * 4, draft_tokens, b * D * 4)) return MTP_ERR_ARG;
   return guarded([&] {
     VerifyArgs a{target_probs, draft_probs, draft_tokens, draft_len, u, tokens, accepted, prob, status, B, D, V};
     return map_cuda(launch_verify(a, static_cast<cudaStream_t>(stream)));

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/mtp_head.h"
@@ -10,6 +11,12 @@
 namespace mtp {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Whether two ranges of bytes share one (either may be absent).
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
 
 inline int check_eps(float eps) { return (eps >= 0.0f && !isinf(eps)) ? MTP_OK : MTP_ERR_ARG; }
 

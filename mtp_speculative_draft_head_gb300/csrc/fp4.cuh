@@ -47,6 +47,13 @@ __device__ __forceinline__ float f16_hi(uint32_t h) {
   return r;
 }
 
+// One lane of a converged warp (as a predicate: what issues a warp's copies and MMAs).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Value of an E4M3 code 0..0x7E (non-negative), exactly.
 __device__ __forceinline__ float e4m3_value(uint32_t code) { return f16_lo(e4m3x2_to_f16x2(code)); }
 

@@ -116,6 +116,18 @@ def test_verify_validation(lib, kw, code):
                                a["status"], a["B"], a["D"], a["V"], None) == code
 
 
+def test_outputs_on_their_inputs_are_refused(lib):
+    """probs on any byte of the (strided) logits, tokens on any byte of the drafts: refused before a launch."""
+    R, V, ld = 3, 100, 128
+    span = ((R - 1) * ld + V) * 4
+    for probs in (A, A + span - 4, A - R * V * 4 + 4):
+        assert lib.mtp_head_sample(A, m.LOGITS_FP32, ld, None, None, None, None, A, A, A, probs, None, R, V,
+                                   None) == m.ERR_ARG
+    B, D = 2, 3
+    for tokens in (A, A + B * D * 4 - 4, A - B * (D + 1) * 4 + 4):
+        assert lib.mtp_head_verify(A, A, A, None, A, tokens, A, None, None, B, D, V, None) == m.ERR_ARG
+
+
 def test_binding_refuses_host_tensors_and_wrong_ranks():
     bf, i32 = torch.bfloat16, torch.int32
     w4 = m.fp4_empty(4, 64, "cpu")

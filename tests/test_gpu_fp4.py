@@ -335,6 +335,64 @@ def test_linear_graph_replay_on_new_rows():
         check_linear(x, w4, y)
 
 
+def test_linear_calls_in_flight_together():
+    """Calls of every schedule (k split, whole tiles, pairs) on streams of their own at once, with workspaces of
+    their own, and graphs of them replayed beside: the bits of the plain calls."""
+    shapes = [(4, 300, 1024), (40, 10240, 100), (700, 6144, 256), (1, 6144, 2048)]
+    ins, want = [], []
+    for R, N, K in shapes:
+        x = bf16(np.random.default_rng(R).standard_normal((R, K)))
+        w4, _ = make_copy(bf16(rng_matrix(N, K, R + 1)))
+        ins.append((x, w4))
+        y = torch.zeros(R, N, dtype=torch.bfloat16, device=DEV)
+        m.mtp_head_linear_fp4(x, *w4, y, m.linear_fp4_workspace(R, N, K, DEV))
+        want.append(y)
+    new = lambda: [(torch.zeros_like(y), m.linear_fp4_workspace(*s, DEV)) for y, s in zip(want, shapes)]  # noqa: E731
+    eager, rec = new(), new()
+    graphs = [m.MtpDraftHead.capture(lambda s, i=i: m.mtp_head_linear_fp4(ins[i][0], *ins[i][1], *rec[i], stream=s))
+              for i in range(len(shapes))]
+    streams = [torch.cuda.Stream() for _ in range(2 * len(shapes))]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, (x, w4) in enumerate(ins):
+            m.mtp_head_linear_fp4(x, *w4, *eager[i], stream=streams[i])
+            with torch.cuda.stream(streams[len(shapes) + i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for y, (e, _), (r, _) in zip(want, eager, rec):
+        assert torch.equal(y, e) and torch.equal(y, r)
+
+
+def test_linear_output_as_the_next_stages_weights():
+    """Each kernel of a chain launches early only past its own wait: a matrix made by the linear, copied to FP4
+    and multiplied again in the same breath gives what the calls give one by one."""
+    a = bf16(np.random.default_rng(1).standard_normal((512, 768)))
+    w4, _ = make_copy(bf16(rng_matrix(256, 768, 2)))
+    x = bf16(np.random.default_rng(3).standard_normal((9, 256)))
+    y, out = torch.zeros(512, 256, dtype=torch.bfloat16, device=DEV), torch.zeros(9, 512, dtype=torch.bfloat16, device=DEV)
+    y4 = m.fp4_empty(512, 256, DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws, ws2 = m.linear_fp4_workspace(512, 256, 768, DEV), m.linear_fp4_workspace(9, 512, 256, DEV)
+
+    def chain(wait):
+        m.mtp_head_linear_fp4(a, *w4, y, ws)
+        wait()
+        m.mtp_head_quantize_fp4(y, *y4, st)
+        wait()
+        m.mtp_head_linear_fp4(x, *y4, out, ws2)
+        wait()
+    chain(torch.cuda.synchronize)
+    want = out.clone()
+    for _ in range(20):
+        out.zero_()
+        y.zero_()
+        for t in y4:
+            t.zero_()
+        chain(lambda: None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 # ---------------------------------------------------------------------------- input stage
 @pytest.mark.parametrize("R,H", [(1, 64), (3, 264), (16, 512), (40, 256), (300, 1024)])
 def test_context_rows(R, H):

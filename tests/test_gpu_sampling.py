@@ -285,6 +285,73 @@ def test_graph_replay_with_new_numbers():
         check(l, (token, prob, None), u.tolist(), par)
 
 
+def test_longest_row():
+    """2^31 - 1 tokens: equal logits share evenly (every weight is one, so the token is floor(u V) exactly); a
+    few planted ones, the last index among them, are found."""
+    V = 2 ** 31 - 1
+    l = torch.full((1, V), -2.0, dtype=torch.bfloat16, device=DEV)
+    for u in (0.0, 0.3, 0.75, 1.0 - 2.0 ** -24):
+        t, pr, _ = sample(l, [u], probs=False)
+        assert int(t) == int(np.float32(u).astype(np.float64) * V)
+        assert abs(float(pr) * V - 1) <= PROB
+    at = [5, 2 ** 30 + 7, V - 1]
+    l[0, at] = torch.tensor([3.0, 4.0, 3.5], dtype=torch.bfloat16, device=DEV)
+    for par in (dict(k=[3]), dict(p=[1e-7]), dict(mp=[0.3])):
+        want = np.exp(np.array([3.0, 4.0, 3.5]) - 4.0)
+        if "p" in par:  # the mass of all: 2^31 weights of e^-6, so only the largest is before the limit
+            want = np.array([0.0, 1.0, 0.0])
+        want /= want.sum()
+        for u in (0.0, 0.5, 0.999):
+            t, pr, _ = sample(l, [u], par, probs=False)
+            j = int((np.cumsum(want) <= u).sum())
+            assert int(t) == at[j] and abs(float(pr) - want[j]) <= PROB * want[j]
+
+
+def test_rows_past_32_bits():
+    """Row offsets beyond 2^32 elements of logits, and beyond 2^31 of the distribution."""
+    V, ld = 1000, 2 ** 31 - 1
+    buf = torch.empty(2 * ld + V, dtype=torch.bfloat16, device=DEV)
+    l = buf.as_strided((3, V), (ld, 1))
+    l.copy_(logits(3, V, 50, True))
+    u, par = [0.2, 0.6, 0.9], params(3, 51)
+    check(l, sample(l, u, par), u, par)
+    del buf, l
+    R, V = 16384, 151936
+    l = torch.randn(R, V, dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(3))
+    u = np.random.default_rng(9).random(R).astype(np.float32).tolist()
+    par = dict(p=[0.9] * R, k=[50] * R)
+    t, pr, dist = sample(l, u, par)
+    rows = [0, 8191, 14133, 14134, 14135, R - 1]
+    check(l[rows], (t[rows], pr[rows], dist[rows]), [u[r] for r in rows], {k: [v[r] for r in rows] for k, v in par.items()})
+    assert int((t < 0).sum()) == 0
+
+
+def test_calls_in_flight_together():
+    """Calls on several streams at once, and two captured graphs replayed side by side: each gives the bits of
+    its own plain call (the operators share nothing)."""
+    ls = [logits(r, v, s) for r, v, s in ((1, 154880, 1), (20, 40000, 2), (90, 5000, 3))]
+    us = [np.random.default_rng(s).random(l.shape[0]).astype(np.float32).tolist() for s, l in enumerate(ls)]
+    pars = [params(l.shape[0], 7 + s) for s, l in enumerate(ls)]
+    want = [sample(l, u, p) for l, u, p in zip(ls, us, pars)]
+    uts = [torch.tensor(u, dtype=torch.float32, device=DEV) for u in us]
+    tps = [tensors(p) for p in pars]
+    out = [[torch.zeros_like(t) for t in w] for w in want]
+    graphs = [m.MtpDraftHead.capture(lambda s, i=i: m.mtp_head_sample(ls[i], uts[i], *out[i], stream=s, **tps[i]))
+              for i in range(3)]
+    got = [[torch.zeros_like(t) for t in w] for w in want]
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(3):
+            m.mtp_head_sample(ls[i], uts[i], *got[i], stream=streams[i], **tps[i])
+            with torch.cuda.stream(streams[3 + i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for w, g, o in zip(want, got, out):
+        for x, y, z in zip(w, g, o):
+            assert torch.equal(x, y) and torch.equal(x, z)
+
+
 # ---------------------------------------------------------------------------- acceptance
 def accept_reference(p, q, x, u, n):
     """(accepted, distribution of the next token or None) of one sequence, fp64."""
