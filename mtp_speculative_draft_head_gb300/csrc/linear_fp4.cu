@@ -23,10 +23,10 @@
 // is split over a cluster of 2 to 8 CTAs, whose fp32 partial sums meet in the first CTA's shared
 // memory and are added in k order.
 //
-// Measured, 12288 -> 6144, with the rows' quantisation: 16 rows 18.0 us (42.5 MB of weights, 6.4 us at the copy
-// rate: latencies of a short kernel, the quantiser before it and the cluster's join are the rest); 4096 rows 148 us,
-// 30 of them the quantiser's, 5.2 PFLOP/s in the product. There the operands' way into the SMs bounds it: a stage of
-// 51 KB takes 757 cycles (68 bytes a cycle and SM), its MMAs 318.
+// Measured, 12288 -> 6144, with the rows' quantisation: 16 rows 18.0 us with the weights in L2, 20.9 out of HBM (42.5
+// MB, 6.4 us at the copy rate: latencies of a short kernel, the quantiser before it and the cluster's join are the rest); 4096 rows 147 us,
+// 30 of them the quantiser's, 5.3 PFLOP/s in the product. There the operands' way into shared memory and out of it
+// bounds it: a stage writes 51 KB and its MMAs read 45 KB, 757 cycles at 128 bytes a cycle, against 318 cycles of MMAs.
 //
 // Warp roles: 0 weight codes, 1 tensor-memory allocation and MMA issue, 2 weight scales, 3
 // activation codes and scales, 4..7 epilogue (warp w reads
@@ -58,12 +58,14 @@ struct LTile {
   static constexpr int kChunks = (NT + 127) / 128;             // 128-row scale blocks of the activations
   static constexpr int kBBytes = NT * kLK / 2;
   static constexpr int kStageBytes = kABytes + kBBytes + kSfChunk * (1 + kChunks);
-  static constexpr int kFit = (206 * 1024) / kStageBytes;
+  static constexpr int kSfBytes = 4 * kLM * 16, kSfBufs = 2;   // a fetch of the weights' scales: four stages of them
+  static constexpr int kFit = (227 * 1024 - 1024 - 512 - 16 * NT - kSfBufs * kSfBytes) / kStageBytes;
   static constexpr int kStages = kFit < 9 ? kFit : 9;
   // after the two accumulators; an MMA takes the scales from an address that is a multiple of four columns
   static constexpr uint32_t kSfaCol = 2 * NT;
   static constexpr uint32_t kSfbCol = kSfaCol + 16;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 4) * 8 + 16 + 4 * NT * 4;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + (2 * kStages + 4) * 8 + 16 +
+                                  4 * NT * 4 + kSfBufs * kSfBytes;
   static_assert(NT % 16 == 0 && NT <= 256, "N of an M = 128 MMA");
   static_assert(kSfbCol + 16 * kChunks <= kTmemCols, "tensor memory");
 };
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
   uint64_t* acc_empty = acc_full + 2;     // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   float* rx_all = reinterpret_cast<float*>(tmem_slot + 4);  // [4][NT]
+  uint8_t* sf_raw = reinterpret_cast<uint8_t*>(rx_all + 4 * NT);  // 16-byte aligned: all before it comes in such pieces
   __shared__ int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -373,61 +376,75 @@ __global__ void __launch_bounds__(kLThreads, 1)
     if (!ok && lane == 0) give_up();
   } else if (warp == 2) {
     // ------------------------------------------------------------------ weight scales
-    // Lane r holds the 16 scale bytes of rows r, r + 32, r + 64, r + 96 of the tile for one stage:
-    // word k of a row belongs to MMA k. Four stages (64 bytes a row, two whole sectors) are loaded at a
-    // time, one group ahead of the stores; a group ends with its tile.
-    constexpr int kGroup = 4;
-    uint4 v[2][kGroup][4];
-    int ft = t0, fkb = kb0;  // the next stage to fetch
-    auto fetch = [&](uint4 (&d)[kGroup][4]) {
+    // Four stages (64 bytes a row) are fetched at a time into shared memory, four lanes a row so that each row is
+    // one request, one group ahead of the stores; a group ends with its tile. For a stage lane r then takes the
+    // 16 scale bytes of rows r, r + 32, r + 64, r + 96: word k of a row belongs to MMA k. (Loaded to registers,
+    // 16 bytes of a row a lane, each row took two requests: 16 rows of 12288 -> 6144,
+    // weights out of HBM, 23.1 us instead of 20.9.)
+    // Buffer: row r's 16-byte piece g at 64 r + 16 (g ^ ((r >> 1) & 3)), so that neither side has bank conflicts.
+    constexpr int kGroup = 4, kBufs = TL::kSfBufs;
+    int ft = t0, fkb = kb0, fb = 0;  // the next stage to fetch, and its buffer
+    auto fetch = [&] {
+      const int g = lane & 3;
+      const bool on = ft < c.tiles && fkb + g < kb0 + nkb;
+      const int row0 = on ? tile_row(ft) + (lane >> 2) : 0;
+      const uint8_t* src = p.w_bs + (on ? static_cast<size_t>(fkb + g) * 16 : 0);
+      const uint32_t dst = smem_addr(sf_raw) + fb * TL::kSfBytes;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = tile_row(ft) + 32 * j + lane;
-        const uint4* src = reinterpret_cast<const uint4*>(p.w_bs + static_cast<size_t>(row) * (p.kp / 16)) + fkb;
-#pragma unroll
-        for (int g = 0; g < kGroup; ++g)
-          d[g][j] = ft < c.tiles && row < p.N && fkb + g < kb0 + nkb ? __ldg(src + g) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 16; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        const bool in = on && row0 + 8 * i < p.N;
+        // (in: the row exists; otherwise nothing is read and the piece becomes zeros)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 64 + ((g ^ ((r >> 1) & 3)) << 4)),
+                     "l"(src + (in ? static_cast<size_t>(row0 + 8 * i) * (p.kp / 16) : 0)), "r"(in ? 16 : 0)
+                     : "memory");
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (++fb == kBufs) fb = 0;
       fkb += kGroup;
       if (fkb >= kb0 + nkb) {
         fkb = kb0;
         ft += step;
       }
     };
-    fetch(v[0]);
+#pragma unroll
+    for (int i = 0; i < kBufs - 1; ++i) fetch();
     Ring<kStages> r;
     bool ok = true;
-    auto put = [&](const uint4 (&d)[4]) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
-      if (ok) {
-        uint4* dst = reinterpret_cast<uint4*>(smem + r.s * TL::kStageBytes + kABytes + TL::kBBytes) + lane;
-        dst[0] = make_uint4(d[0].x, d[1].x, d[2].x, d[3].x);
-        dst[32] = make_uint4(d[0].y, d[1].y, d[2].y, d[3].y);
-        dst[64] = make_uint4(d[0].z, d[1].z, d[2].z, d[3].z);
-        dst[96] = make_uint4(d[0].w, d[1].w, d[2].w, d[3].w);
-        fence_proxy_async_smem();
+    int ub = 0;
+    for (int t = t0; t < c.tiles && ok; t += step)
+      for (int kb = 0; kb < nkb && ok; kb += kGroup) {
+        __syncwarp();  // the buffer that the next fetch fills has been read by every lane
+        fetch();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kBufs - 1) : "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&full[r.s]));
-        r.next();
-      }
-    };
-    int t = t0, kb = 0;
-    while (t < c.tiles && ok) {
+        const uint32_t src = smem_addr(sf_raw) + ub * TL::kSfBytes + lane * 64;
+        if (++ub == kBufs) ub = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (t < c.tiles && ok) {
-          fetch(v[h ^ 1]);
+        for (int g = 0; g < kGroup; ++g)
+          if (kb + g < nkb && ok) {
+            uint4 d[4];
 #pragma unroll
-          for (int g = 0; g < kGroup; ++g)
-            if (kb + g < nkb && ok) put(v[h][g]);
-          kb += kGroup;
-          if (kb >= nkb) {
-            kb = 0;
-            t += step;
+            for (int j = 0; j < 4; ++j)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(d[j].x), "=r"(d[j].y), "=r"(d[j].z), "=r"(d[j].w)
+                           : "r"(src + j * 2048 + ((g ^ ((lane >> 1) & 3)) << 4))
+                           : "memory");
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
+            if (ok) {
+              uint4* dst = reinterpret_cast<uint4*>(smem + r.s * TL::kStageBytes + kABytes + TL::kBBytes) + lane;
+              dst[0] = make_uint4(d[0].x, d[1].x, d[2].x, d[3].x);
+              dst[32] = make_uint4(d[0].y, d[1].y, d[2].y, d[3].y);
+              dst[64] = make_uint4(d[0].z, d[1].z, d[2].z, d[3].z);
+              dst[96] = make_uint4(d[0].w, d[1].w, d[2].w, d[3].w);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&full[r.s]));
+              r.next();
+            }
           }
-        }
       }
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && lane == 0) give_up();
   } else if (warp >= 4 && !SPLIT) {
     // ------------------------------------------------------------------ epilogue
