@@ -1184,8 +1184,9 @@ cudaError_t launch_cluster(const void* kernel, unsigned grid, int nc, size_t sme
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-// Largest slice that a CTA keeps in shared memory (227 KB of it).
+// Longest slice that a CTA keeps in shared memory: of 227 KB, or of half of an SM's (two CTAs).
 constexpr int64_t kHeldSlice = static_cast<int64_t>((227 * 1024 - kFixedSmem) / 4 / kSliceUnit * kSliceUnit);
+constexpr int64_t kHeldSliceOfTwo = static_cast<int64_t>((113 * 1024 - kFixedSmem) / 4 / kSliceUnit * kSliceUnit);
 
 int64_t slice_of(int64_t V, int nc) { return ((V + nc - 1) / nc + kSliceUnit - 1) / kSliceUnit * kSliceUnit; }
 
@@ -1202,18 +1203,13 @@ bool worth(int64_t V, int nc) { return V > static_cast<int64_t>(nc) * kSliceUnit
 // CTAs per row of the sampler (a power of two up to kMaxC). Clusters of 16 as long as they all run at once:
 // with two CTAs on an SM 14 of them fit the GPU's SM groups. Without top_k each CTA's time is in the histogram's
 // shared-memory atomics, so the spread over more SMs still pays for a short second wave. Beyond that clusters of
-// four, all resident up to 36 rows, and for more rows the smallest that keep a slice in shared memory. At V =
-// 154880: 16 rows with top_k and top_p take 25.5 us with 16 CTAs, 26.8 with 8 and 20.6 with 4; with top_p alone
-// 53.5, 56.4 and 61.0; 24 rows 31.4, 28.0 and 20.9, and 71.6, 75.7 and 59.9; 80 rows 81, 74 and 54, and 199, 195
-// and 149. 160 rows of V = 32000 take 33.1 with one CTA and 39.3 with 4.
-int sample_cluster(int64_t rows, int64_t V, bool top_k) {
+// four, and single CTAs for short rows that fill the GPU anyway. At V = 154880, rows in L2: 16 rows with top_k and
+// top_p take 25.5 us with 16 CTAs, 26.8 with 8 and 20.6 with 4; with top_p alone 53.5, 56.4 and 61.0; 24 rows 31.4,
+// 28.0 and 20.9, and 71.6, 75.7 and 59.9. 160 rows of V = 32000 with top_k take 33.1 with one CTA and 39.3 with 4.
+int sample_cluster(int64_t rows, int64_t V, bool top_k, int sm_count) {
   int nc = 4;
-  if (rows <= (top_k ? 14 : 18)) {
-    nc = kMaxC;
-  } else if (rows > 36) {
-    nc = 1;
-    while (nc < 4 && V > nc * kHeldSlice) nc *= 2;
-  }
+  if (rows <= (top_k ? 14 : 18)) nc = kMaxC;
+  else if (rows >= sm_count && V <= kHeldSlice) nc = 1;
   while (nc > 1 && !worth(V, nc)) nc /= 2;
   return nc;
 }
@@ -1233,9 +1229,12 @@ cudaError_t launch_sample(const SampleArgs& in, cudaStream_t stream) {
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   SampleArgs a = in;
-  int nc = sample_cluster(a.R, a.V, a.top_k != nullptr);
+  int nc = sample_cluster(a.R, a.V, a.top_k != nullptr, di.sm_count);
   int64_t slice = slice_of(a.V, nc);
-  const bool res = slice <= kHeldSlice;
+  // A slice is kept in shared memory where that leaves room for as many CTAs per SM as there are to run (two hide
+  // each other's loads: 80 rows with top_k and top_p, out of HBM, 66 us, and 74 with one and its slice held).
+  const bool one_each = static_cast<int64_t>(a.R) * nc <= di.sm_count || nc == 1;
+  const bool res = slice <= (one_each ? kHeldSlice : kHeldSliceOfTwo);
   int frac = mass_bits(a.V);
   const void* kern = a.bf16 ? (res ? reinterpret_cast<const void*>(sample_kernel<true, true>)
                                    : reinterpret_cast<const void*>(sample_kernel<true, false>))
