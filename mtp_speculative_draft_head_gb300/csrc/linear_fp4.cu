@@ -23,10 +23,11 @@
 // is split over a cluster of 2 to 8 CTAs, whose fp32 partial sums meet in the first CTA's shared
 // memory and are added in k order.
 //
-// Measured, 12288 -> 6144, with the rows' quantisation: 16 rows 18.0 us with the weights in L2, 20.9 out of HBM (42.5
-// MB, 6.4 us at the copy rate: latencies of a short kernel, the quantiser before it and the cluster's join are the rest); 4096 rows 147 us,
-// 30 of them the quantiser's, 5.3 PFLOP/s in the product. There the operands' way into shared memory and out of it
-// bounds it: a stage writes 51 KB and its MMAs read 45 KB, 757 cycles at 128 bytes a cycle, against 318 cycles of MMAs.
+// Measured, 12288 -> 6144, with the rows' quantisation: 16 rows 18.0 us with the weights in L2, 20.0 out of HBM (42.5
+// MB, 6.4 us at the copy rate: latencies of a short kernel, the quantiser before it and the cluster's join are the
+// rest); 4096 rows 147 us, 30 of them the quantiser's, 5.3 PFLOP/s in the product, tensor pipe active 54 % of the
+// time. There the operands' way into the SMs bounds it: 757 cycles for a stage's 51 KB (68 bytes a cycle and SM, the
+// four stages that shared memory holds all in flight), its MMAs 318.
 //
 // Warp roles: 0 weight codes, 1 tensor-memory allocation and MMA issue, 2 weight scales, 3
 // activation codes and scales, 4..7 epilogue (warp w reads
@@ -51,6 +52,7 @@ constexpr int kLThreads = 256;
 constexpr int kABytes = kLM * kLK / 2;       // 16 KB of weight codes per stage
 constexpr int kSfChunk = 4 * 512;            // scales of 128 rows x 256 codes: four 512-byte blocks
 constexpr int kMaxSplits = 8;
+constexpr int kGroup = 16;        // activation tiles that share a pass over long weights
 constexpr uint32_t kTmemCols = 512;
 
 template <int NT>
@@ -73,10 +75,11 @@ struct LTile {
 struct LinearSched {
   int nt;       // activation rows per tile
   int mt;       // weight tiles
-  int tiles;    // all tiles; tile t: weight tile t % mt, activation tile t / mt
+  int tiles;    // all tiles: mt times the activation tiles
   int nkb;      // stages per tile
   int splits;   // CTAs per tile (a cluster along k); 1: persistent
   bool pair;    // persistent in pairs: a tile is two neighbouring weight tiles, mt counts those
+  bool group;   // activation tiles in groups
 };
 
 struct LinearParams {
@@ -180,7 +183,7 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // ------------------------------------------------------------------------------- kernel
-template <int NT, bool SPLIT, bool PAIR>
+template <int NT, bool SPLIT, bool PAIR, bool GROUP>
 __global__ void __launch_bounds__(kLThreads, 1)
     linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const LinearParams p, const LinearSched c) {
@@ -202,8 +205,19 @@ __global__ void __launch_bounds__(kLThreads, 1)
   const uint32_t rank = SPLIT || PAIR ? cta_rank() : 0u;
   const int t0 = SPLIT ? static_cast<int>(blockIdx.x) / c.splits : static_cast<int>(blockIdx.x) >> (PAIR ? 1 : 0);
   const int step = SPLIT ? c.tiles : static_cast<int>(gridDim.x) >> (PAIR ? 1 : 0);
-  // first weight row and activation tile of tile t (a pair's CTAs take neighbouring weight tiles)
-  auto tile_row = [&](int t) { return (t % c.mt * (PAIR ? 2 : 1) + (PAIR ? static_cast<int>(rank) : 0)) * kLM; };
+  // Tile t: every weight tile in turn for each activation tile, or (GROUP) for each kGroup activation tiles.
+  auto weight_tile = [&](int t) {
+    if constexpr (!GROUP) return t % c.mt;
+    const int g = t / (c.mt * kGroup), left = c.tiles / c.mt - g * kGroup;
+    return (t - g * c.mt * kGroup) / (left < kGroup ? left : kGroup);
+  };
+  auto x_tile = [&](int t) {
+    if constexpr (!GROUP) return t / c.mt;
+    const int g = t / (c.mt * kGroup), left = c.tiles / c.mt - g * kGroup;
+    return g * kGroup + (t - g * c.mt * kGroup) % (left < kGroup ? left : kGroup);
+  };
+  // first weight row of tile t (a pair's CTAs take neighbouring weight tiles)
+  auto tile_row = [&](int t) { return (weight_tile(t) * (PAIR ? 2 : 1) + (PAIR ? static_cast<int>(rank) : 0)) * kLM; };
   const int kb0 = SPLIT ? static_cast<int>(rank) * c.nkb / c.splits : 0;
   const int nkb = (SPLIT ? (static_cast<int>(rank) + 1) * c.nkb / c.splits : c.nkb) - kb0;
 
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     Ring<kStages> r;
     bool ok = true;
     for (int t = t0; t < c.tiles && ok; t += step) {
-      const int xt = t / c.mt;
+      const int xt = x_tile(t);
       const uint8_t* sf = p.x_sf + (static_cast<size_t>(xt) * kChunks * (p.kp / 64) + kb0 * 4) * 512;
       for (int kb = kb0; kb < kb0 + nkb; ++kb, sf += kSfChunk) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.s]), r.ph ^ 1u));
@@ -382,12 +396,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
     // 16 bytes of a row a lane, each row took two requests: 16 rows of 12288 -> 6144,
     // weights out of HBM, 23.1 us instead of 20.9.)
     // Buffer: row r's 16-byte piece g at 64 r + 16 (g ^ ((r >> 1) & 3)), so that neither side has bank conflicts.
-    constexpr int kGroup = 4, kBufs = TL::kSfBufs;
-    int ft = t0, fkb = kb0, fb = 0;  // the next stage to fetch, and its buffer
+    constexpr int kFetch = 4, kBufs = TL::kSfBufs;
+    int ft = t0, frow = tile_row(t0), fkb = kb0, fb = 0;  // the next stage to fetch, and its buffer
     auto fetch = [&] {
       const int g = lane & 3;
       const bool on = ft < c.tiles && fkb + g < kb0 + nkb;
-      const int row0 = on ? tile_row(ft) + (lane >> 2) : 0;
+      const int row0 = on ? frow + (lane >> 2) : 0;
       const uint8_t* src = p.w_bs + (on ? static_cast<size_t>(fkb + g) * 16 : 0);
       const uint32_t dst = smem_addr(sf_raw) + fb * TL::kSfBytes;
 #pragma unroll
@@ -401,10 +415,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       if (++fb == kBufs) fb = 0;
-      fkb += kGroup;
+      fkb += kFetch;
       if (fkb >= kb0 + nkb) {
         fkb = kb0;
         ft += step;
+        if (ft < c.tiles) frow = tile_row(ft);
       }
     };
 #pragma unroll
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     bool ok = true;
     int ub = 0;
     for (int t = t0; t < c.tiles && ok; t += step)
-      for (int kb = 0; kb < nkb && ok; kb += kGroup) {
+      for (int kb = 0; kb < nkb && ok; kb += kFetch) {
         __syncwarp();  // the buffer that the next fetch fills has been read by every lane
         fetch();
         asm volatile("cp.async.wait_group %0;" ::"n"(kBufs - 1) : "memory");
@@ -421,7 +436,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         const uint32_t src = smem_addr(sf_raw) + ub * TL::kSfBytes + lane * 64;
         if (++ub == kBufs) ub = 0;
 #pragma unroll
-        for (int g = 0; g < kGroup; ++g)
+        for (int g = 0; g < kFetch; ++g)
           if (kb + g < nkb && ok) {
             uint4 d[4];
 #pragma unroll
@@ -453,7 +468,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     int n = 0;
     for (int t = t0; t < c.tiles; t += step, ++n) {
       const int buf = n & 1;
-      const int row = tile_row(t) + 32 * q + lane, r0 = (t / c.mt) * NT;
+      const int row = tile_row(t) + 32 * q + lane, r0 = x_tile(t) * NT;
       const float rw = row < p.N ? __ldg(p.w_rs + row) : 0.0f;
       float* rx = rx_all + q * NT;
       load_rx(rx, r0);
@@ -489,7 +504,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     float* slots = reinterpret_cast<float*>(smem);
     bool done = true;
     // the scales of the first CTA's epilogue, under the last MMAs
-    const int row = tile_row(t0) + 32 * q + lane, r0 = (t0 / c.mt) * NT;
+    const int row = tile_row(t0) + 32 * q + lane, r0 = x_tile(t0) * NT;
     float rw = 0.0f;
     float* rx = rx_all + q * NT;
     if (epi) {
@@ -590,6 +605,10 @@ LinearSched make_sched(int R, int N, int kp, int sm_count) {
     c.tiles = c.tiles / c.mt * ((c.mt + 1) / 2);
     c.mt = (c.mt + 1) / 2;
   }
+  // Weights beyond half of L2 are passed over once for kGroup activation tiles (154880 x 6144, 256 rows: 137 us, with
+  // a pass for each tile 183); shorter ones stay there while the activations go by (the groups' divisions cost 2 us
+  // of 90 at 2048 rows of 6144 -> 12288).
+  c.group = c.pair && static_cast<int64_t>(N) * kp * 9 / 16 > (64 << 20);
   return c;
 }
 
@@ -615,12 +634,12 @@ size_t bind(LinearWs* w, uint8_t* p, int R, int K) {
   return static_cast<size_t>(p - p0);
 }
 
-template <int NT, bool SPLIT, bool PAIR>
+template <int NT, bool SPLIT, bool PAIR, bool GROUP = false>
 cudaError_t launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const LinearParams& p, const LinearSched& c,
                         int sm_count, cudaStream_t stream) {
   static std::mutex mu;
   static bool done[64] = {};
-  const void* kernel = reinterpret_cast<const void*>(linear_fp4_kernel<NT, SPLIT, PAIR>);
+  const void* kernel = reinterpret_cast<const void*>(linear_fp4_kernel<NT, SPLIT, PAIR, GROUP>);
   constexpr size_t smem = LTile<NT>::kSmem;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -662,7 +681,9 @@ cudaError_t launch_nt(const CUtensorMap& tw, const CUtensorMap& tx, const Linear
                       int sm_count, cudaStream_t stream) {
   if (c.splits > 1) return launch_tile<NT, true, false>(tw, tx, p, c, sm_count, stream);
   if constexpr (NT >= 128)
-    if (c.pair) return launch_tile<NT, false, true>(tw, tx, p, c, sm_count, stream);
+    if (c.pair)
+      return c.group ? launch_tile<NT, false, true, true>(tw, tx, p, c, sm_count, stream)
+                     : launch_tile<NT, false, true>(tw, tx, p, c, sm_count, stream);
   return launch_tile<NT, false, false>(tw, tx, p, c, sm_count, stream);
 }
 

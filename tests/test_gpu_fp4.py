@@ -335,6 +335,21 @@ def test_linear_graph_replay_on_new_rows():
         check_linear(x, w4, y)
 
 
+def test_linear_long_weights():
+    """Weights that do not stay in L2 (69 MB) and 18 activation tiles: the schedule that passes over them once for
+    each group of 16, the last group short and the last weight tile ragged; sampled rows and columns."""
+    R, N, K = 4000, 120003, 1000
+    g = torch.Generator(DEV).manual_seed(8)
+    x = torch.randn(R, K, device=DEV, generator=g).bfloat16()
+    w4, _ = make_copy((torch.randn(N, K, device=DEV, generator=g) * 0.02).bfloat16())
+    y = torch.full((R, N), 1e30, dtype=torch.bfloat16, device=DEV)
+    m.mtp_head_linear_fp4(x, *w4, y, m.linear_fp4_workspace(R, N, K, DEV))
+    rows = torch.arange(0, R, 31, device=DEV)
+    cols = torch.cat([torch.arange(0, N, 523, device=DEV), torch.arange(N - 140, N, device=DEV)])
+    check_linear(x[rows].contiguous(), tuple(t[cols].contiguous() for t in w4), y[rows][:, cols])
+    assert not bool((y == 1e30).any())
+
+
 def test_linear_calls_in_flight_together():
     """Calls of every schedule (k split, whole tiles, pairs) on streams of their own at once, with workspaces of
     their own, and graphs of them replayed beside: the bits of the plain calls."""
