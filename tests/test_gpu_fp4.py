@@ -69,6 +69,28 @@ def test_quantize_bits(V, H):
     assert np.array_equal(q, ref.pack(codes))
 
 
+@pytest.mark.parametrize("V,H", [(20000, 40), (9800, 1536), (20, 1544), (5000, 2056), (20, 6144), (2600, 6152),
+                                 (20, 12288), (1300, 12296), (3, 24576), (3, 24584), (1500, 1001)])
+def test_quantize_and_back_on_both_sides_of_every_form(V, H):
+    """Row lengths around the changes of threads per row, and more rows than run at once; sampled rows."""
+    g = torch.Generator(DEV).manual_seed(V + H)
+    w = (torch.randn(V, H, device=DEV, generator=g) * 0.02).bfloat16()
+    w4, st = make_copy(w)
+    assert st == 0
+    rows = torch.cat([torch.arange(0, V, max(1, V // 9)), torch.tensor([V - 1])]).to(DEV)
+    codes, sc, rs = ref.quantize(vals(w[rows]))
+    q, bs, r = host(tuple(t[rows] for t in w4))
+    assert np.array_equal(r.view(np.uint32), rs.view(np.uint32))
+    assert np.array_equal(bs, sc)
+    assert np.array_equal(q, ref.pack(codes))
+    out = torch.full((V, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    m.mtp_head_dequantize_fp4(*w4, out)
+    v = torch.from_numpy((ref.E2M1[codes & 7] * np.where(codes > 7, -1.0, 1.0) *
+                          np.repeat(ref.E4M3[bs], 16, axis=1))[:, :H].astype(np.float32) * r[:, None]).bfloat16()
+    assert torch.equal(out[rows].cpu(), v)
+    assert not bool((out == 7.0).any())
+
+
 @pytest.mark.parametrize("kind", ["outliers", "ties", "tiny", "huge", "wide", "signs"])
 @pytest.mark.parametrize("V,H", [(40, 272), (1300, 72), (13, 101)])
 def test_quantize_bits_hard_rows(kind, V, H):
@@ -97,7 +119,7 @@ def test_quantize_nonfinite_rows_become_zeros(V):
     assert np.array_equal(q[2:3], ref.pack(codes)) and r[2] == rs[0]
 
 
-@pytest.mark.parametrize("V,H", [(1, 1), (3, 17), (5, 24), (33, 256), (70, 1000), (4, 4099)])
+@pytest.mark.parametrize("V,H", [(1, 1), (3, 8), (3, 17), (5, 24), (33, 256), (70, 1000), (4, 4099)])
 @pytest.mark.parametrize("kind", ["normal", "wide", "huge"])
 def test_dequantize(V, H, kind):
     w4, _ = make_copy(bf16(rng_matrix(V, H, 11, kind)))

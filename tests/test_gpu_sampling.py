@@ -285,6 +285,27 @@ def test_graph_replay_with_new_numbers():
         check(l, (token, prob, None), u.tolist(), par)
 
 
+@pytest.mark.parametrize("R", [14, 15, 18, 19, 36, 37, 39, 151, 152, 153])
+@pytest.mark.parametrize("which", ["Tp", "Tkp"])
+def test_cluster_borders(R, which):
+    """Row counts on both sides of every change of the CTAs per row and of what shared memory holds."""
+    V = 9001
+    l = logits(R, V, R, R % 2 == 0)
+    u = np.random.default_rng(R).random(R).astype(np.float32).tolist()
+    par = params(R, R + 1, which)
+    check(l, sample(l, u, par), u, par, rows=[0, R // 2, R - 1])
+
+
+@pytest.mark.parametrize("R,V", [(2, 688127), (2, 688129), (20, 172031), (20, 172033), (40, 57343), (40, 57345),
+                                 (40, 172033), (152, 43007), (152, 43009)])
+def test_slice_borders(R, V):
+    """Rows about as long as what the cluster's CTAs hold in shared memory, one by one or two on an SM."""
+    l = logits(R, V, V)
+    u = np.random.default_rng(V).random(R).astype(np.float32).tolist()
+    par = params(R, V, "Tp")
+    check(l, sample(l, u, par), u, par, rows=[0, R - 1])
+
+
 def test_longest_row():
     """2^31 - 1 tokens: equal logits share evenly (every weight is one, so the token is floor(u V) exactly); a
     few planted ones, the last index among them, are found."""
@@ -431,6 +452,32 @@ def test_verify(B, D, V, greedy):
     if greedy:
         x = q.argmax(2).to(torch.int32)
     check_verify(p, None if greedy else q, x, u)
+
+
+@pytest.mark.parametrize("B", [4, 5, 9, 10, 19, 20, 38, 39, 76, 77, 200])
+def test_verify_cluster_borders(B):
+    p, q, x, u = distributions(B, 2, 9001, B)
+    check_verify(p, q, x, u)
+
+
+def test_verify_past_32_bits():
+    """Distributions of more than 2^31 numbers. Equal shares of 2^-24 are exact: every draft is accepted and the
+    token is floor(u V); in the last sequence the drafter knows the first half only, its draft is refused
+    (0.75 * 2 > 1) and the token comes from the second half."""
+    B, D, V = 16, 9, 1 << 24
+    p = torch.full((B, D + 1, V), 2.0 ** -24, device=DEV)
+    q = torch.full((B, D, V), 2.0 ** -24, device=DEV)
+    q[B - 1, 0, : V // 2] = 2.0 ** -23
+    q[B - 1, 0, V // 2:] = 0.0
+    x = torch.full((B, D), 5, dtype=torch.int32, device=DEV)
+    u = torch.rand(B, D + 1, generator=torch.Generator().manual_seed(2))
+    u[B - 1, 0] = 0.75
+    tokens, acc, prob = run_verify(p, q, x, u.to(DEV))
+    assert acc.tolist() == [D] * (B - 1) + [0]
+    last = (u[:, D].double() * V).floor().long()
+    last[B - 1] = V // 2 + int((u[B - 1, D].double() * (V // 2)).floor())
+    assert [int(tokens[b, a]) for b, a in enumerate(acc.tolist())] == last.tolist()
+    assert prob.tolist() == [2.0 ** -24] * (B - 1) + [2.0 ** -23]
 
 
 def test_verify_lengths():
