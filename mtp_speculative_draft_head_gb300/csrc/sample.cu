@@ -60,6 +60,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// "This CTA runs" (its shared memory may be written), said early; and the wait for all of them to have said it,
+// before the first write to another's (one full barrier between the pass over the row and the exchange less: one
+// row 12.4 -> 12.0 us, the acceptance of four sequences 9.4 -> 9.0).
+__device__ __forceinline__ void cluster_here() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_here() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Address of this CTA's shared variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
   uint32_t r;
@@ -350,6 +355,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     loc.n[b] = 0u;
   }
   if (tid == 0) s.found = 0u;
+  if (nc > 1) cluster_here();
   pdl_wait_prior_grid();
 
   // ---- the row's parameters
@@ -461,8 +467,8 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     s.wmax[warp] = hi;
     s.wmin[warp] = lo;
   }
-  if (nc > 1) cluster_sync_all();  // (also: every CTA of the cluster runs, its shared memory may be written)
-  else __syncthreads();
+  __syncthreads();
+  if (nc > 1) cluster_wait_here();
   if (warp == 0) {
     hi = __reduce_max_sync(0xffffffffu, lane < kW ? s.wmax[lane] : 0u);
     lo = __reduce_min_sync(0xffffffffu, lane < kW ? s.wmin[lane] : 0xFFFFFFFFu);
@@ -1001,6 +1007,7 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
   const int64_t b = blockIdx.x / nc;
   const int64_t V = a.V, D = a.D;
   const int64_t i0 = rank * slice, i1 = i0 + slice < V ? i0 + slice : V, seg = slice / kW;
+  if (nc > 1) cluster_here();
   pdl_wait_prior_grid();
   int n = a.draft_len ? a.draft_len[b] : a.D;
   const float ud = a.u[b * (D + 1) + D];
@@ -1010,6 +1017,7 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
   bool bad = n < 0 || n > a.D || !unit(ud);
   for (int i = lane; !bad && i < n; i += 32) bad = !unit(a.u[b * (D + 1) + i]);
   if (__any_sync(0xffffffffu, bad)) {
+    if (nc > 1) cluster_wait_here();
     if (rank == 0) {
       for (int i = tid; i <= a.D; i += kT) a.tokens[b * (D + 1) + i] = -1;
       if (tid == 0) {
@@ -1111,7 +1119,10 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
     __syncthreads();
     u64 mine = 0ull;
     for (int w = 0; w < kW; ++w) mine += s.wsum[w];
-    if (nc > 1) cluster_sync_all();  // the peers run, and have read the previous pass's masses
+    if (nc > 1) {  // the peers run, and have read the previous pass's masses
+      if (pass == 0) cluster_wait_here();
+      else cluster_sync_all();
+    }
     if (tid < nc) {
       if (nc > 1) st_peer(peer(&s.cta[rank], tid), mine);
       else s.cta[0] = mine;
