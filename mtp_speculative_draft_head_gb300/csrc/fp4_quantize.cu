@@ -28,6 +28,7 @@ namespace mtp {
 namespace {
 
 constexpr int kQThreads = 256;
+constexpr int kWaves = 16;  // CTAs per one that runs, at most
 constexpr float kUp = 1.0f + 0x1p-21f, kDn = 1.0f - 0x1p-21f;
 constexpr float kSmallRs = 0x1p-100f;  // below: s_j rs or its reciprocal may leave the normal range
 
@@ -265,10 +266,11 @@ __device__ __forceinline__ uint4 ld_now(const uint4* p) {
 // Rows that TPR threads hold in registers, kHeld blocks of 16 columns a thread: one read of the matrix.
 // TPR = 32: a warp per row, eight rows a CTA; otherwise a CTA per row. Threads per SM over registers per
 // thread: at H = 6144, V = 154880 768 threads (80 registers) took 516 us, 1,024 (64) 473, 1,280 (48, a few
-// spilled) 458: 5.3 TB/s of bytes read and written; the two-pass kernel below 539.
+// spilled) 458, and 415 with the grid in many waves (launch_held): 5.9 TB/s of bytes read and written.
 constexpr int kHeld = 3;
+constexpr int kHeldThreads = 1280;  // per SM
 template <int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, (TPR == 128 || TPR == 256 ? 1280 : 1024) / (TPR == 32 ? 256 : TPR))
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, kHeldThreads / (TPR == 32 ? 256 : TPR))
     fp4_quantize_held_kernel(const uint16_t* __restrict__ w, uint8_t* __restrict__ q, uint8_t* __restrict__ bs,
                              float* __restrict__ rs_out, int32_t* __restrict__ status, const int32_t* __restrict__ valid,
                              int rows, int k, int tile) {
@@ -333,44 +335,42 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, (TPR == 128 || TPR == 2
 
 // bf16( fp32( code * s_j * rs ) ): eight columns (a 4-byte load, a 16-byte store) a thread, kUnits at a
 // time, neighbouring lanes neighbouring columns. per_row: eights of a row; magic = floor(2^64 / per_row) + 1
-// (its product with a 32-bit number has the quotient in the upper half).
+// (its product with a 32-bit number has the quotient in the upper half). A chunk a block, as many blocks as that
+// takes: lm_head 368 us (6.6 TB/s), by 1,216 blocks in a loop 410.
 constexpr int kUnits = 4;
 __global__ void __launch_bounds__(kQThreads) fp4_dequantize_vec_kernel(const Fp4Matrix m, uint16_t* __restrict__ w,
                                                                        uint32_t total, uint32_t per_row,
                                                                        unsigned long long magic, int kp) {
   pdl_wait_prior_grid();
   const int lane = threadIdx.x & 31;
-  const uint64_t step = static_cast<uint64_t>(gridDim.x) * kQThreads * kUnits;
-  for (uint64_t i0 = (static_cast<uint64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5)) * 32 * kUnits + lane; i0 < total;
-       i0 += step) {
-    uint32_t c[kUnits], s[kUnits];
-    float rs[kUnits];
+  const uint64_t i0 = (static_cast<uint64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5)) * 32 * kUnits + lane;
+  uint32_t c[kUnits], s[kUnits];
+  float rs[kUnits];
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const uint64_t i = i0 + 32 * j;
-      if (i < total) {
-        const uint32_t row = static_cast<uint32_t>(__umul64hi(i, magic)), b = static_cast<uint32_t>(i) - row * per_row;
-        c[j] = __ldcs(reinterpret_cast<const uint32_t*>(m.q + static_cast<size_t>(row) * (kp / 2)) + b);
-        s[j] = m.bs[static_cast<size_t>(row) * (kp / kFp4Block) + (b >> 1)];
-        rs[j] = m.rs[row];
-      }
+  for (int j = 0; j < kUnits; ++j) {
+    const uint64_t i = i0 + 32 * j;
+    if (i < total) {
+      const uint32_t row = static_cast<uint32_t>(__umul64hi(i, magic)), b = static_cast<uint32_t>(i) - row * per_row;
+      c[j] = __ldcs(reinterpret_cast<const uint32_t*>(m.q + static_cast<size_t>(row) * (kp / 2)) + b);
+      s[j] = m.bs[static_cast<size_t>(row) * (kp / kFp4Block) + (b >> 1)];
+      rs[j] = m.rs[row];
     }
+  }
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-      const uint64_t i = i0 + 32 * j;
-      if (i < total) {
-        const uint32_t s2 = e4m3x2_to_f16x2(s[j] * 0x0101u);
-        uint32_t v[4], o[4];
-        e2m1x8_to_f16x2x4(c[j], v);
+  for (int j = 0; j < kUnits; ++j) {
+    const uint64_t i = i0 + 32 * j;
+    if (i < total) {
+      const uint32_t s2 = e4m3x2_to_f16x2(s[j] * 0x0101u);
+      uint32_t v[4], o[4];
+      e2m1x8_to_f16x2x4(c[j], v);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t p = f16x2_mul(v[t], s2);  // exact
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-              : "=r"(o[t])
-              : "f"(__fmul_rn(f16_hi(p), rs[j])), "f"(__fmul_rn(f16_lo(p), rs[j])));
-        }
-        __stcs(reinterpret_cast<uint4*>(w) + i, make_uint4(o[0], o[1], o[2], o[3]));
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t p = f16x2_mul(v[t], s2);  // exact
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+            : "=r"(o[t])
+            : "f"(__fmul_rn(f16_hi(p), rs[j])), "f"(__fmul_rn(f16_lo(p), rs[j])));
       }
+      __stcs(reinterpret_cast<uint4*>(w) + i, make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
   // (no early launch: a sweep that follows may read w, as its lm_head, before its own wait)
@@ -412,7 +412,10 @@ template <int TPR>
 cudaError_t launch_held(const DeviceInfo& di, int rows, cudaStream_t stream, void** args) {
   constexpr int kThreads = TPR == 32 ? 256 : TPR;
   const int64_t blocks = (static_cast<int64_t>(rows) * TPR + kThreads - 1) / kThreads;
-  const int64_t cap = static_cast<int64_t>(di.sm_count) * (2048 / kThreads);
+  // Many more CTAs than run at once, of a few rows each: rows that take longer (more boundaries inside their
+  // brackets) and the last wave even out (lm_head 458 us with 1.6 waves of CTAs, 415 with 16; one row a CTA
+  // is slower for short rows).
+  const int64_t cap = static_cast<int64_t>(di.sm_count) * (kHeldThreads / kThreads) * kWaves;
   return launch_pdl(reinterpret_cast<const void*>(fp4_quantize_held_kernel<TPR>),
                     dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(kThreads), 0, stream, args);
 }
@@ -442,7 +445,7 @@ cudaError_t launch_fp4_quantize(const uint16_t* w, uint8_t* q, uint8_t* bs, floa
                                  : reinterpret_cast<const void*>(fp4_quantize_kernel<32, false>));
   const int per_block = wide ? 1 : kQThreads / 32;
   int64_t blocks = (static_cast<int64_t>(rows) + per_block - 1) / per_block;
-  if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
+  if (blocks > 8 * kWaves * di.sm_count) blocks = 8 * kWaves * di.sm_count;
   return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kQThreads), 0, stream, args);
 }
 
@@ -458,8 +461,7 @@ cudaError_t launch_fp4_dequantize(const Fp4Matrix& m, uint16_t* w, int rows, int
     unsigned long long magic = per_row == 1 ? 0ull : ~0ull / per_row + 1;
     int kp = fp4_padded(k);
     if (per_row > 1) {
-      int64_t blocks = (eights + kQThreads * kUnits - 1) / (kQThreads * kUnits);
-      if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
+      const int64_t blocks = (eights + kQThreads * kUnits - 1) / (kQThreads * kUnits);
       void* args[] = {&mm, &w, &total, &per_row, &magic, &kp};
       return launch_pdl(reinterpret_cast<const void*>(fp4_dequantize_vec_kernel), dim3(static_cast<unsigned>(blocks)),
                         dim3(kQThreads), 0, stream, args);
@@ -467,7 +469,7 @@ cudaError_t launch_fp4_dequantize(const Fp4Matrix& m, uint16_t* w, int rows, int
   }
   const int64_t total = static_cast<int64_t>(rows) * ((k + kFp4Block - 1) / kFp4Block);
   int64_t blocks = (total + kQThreads - 1) / kQThreads;
-  if (blocks > 8 * di.sm_count) blocks = 8 * di.sm_count;
+  if (blocks > 8 * kWaves * di.sm_count) blocks = 8 * kWaves * di.sm_count;
   void* args[] = {&mm, &w, &rows, &k};
   return launch_pdl(reinterpret_cast<const void*>(fp4_dequantize_kernel), dim3(static_cast<unsigned>(blocks)),
                     dim3(kQThreads), 0, stream, args);

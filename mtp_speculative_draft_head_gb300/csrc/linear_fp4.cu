@@ -25,7 +25,7 @@
 //
 // Measured, 12288 -> 6144, with the rows' quantisation: 16 rows 18.0 us with the weights in L2, 20.0 out of HBM (42.5
 // MB, 6.4 us at the copy rate: latencies of a short kernel, the quantiser before it and the cluster's join are the
-// rest); 4096 rows 147 us, 30 of them the quantiser's, 5.3 PFLOP/s in the product, tensor pipe active 54 % of the
+// rest); 4096 rows 145 us, 26 of them the quantiser's, 5.2 PFLOP/s in the product, tensor pipe active 54 % of the
 // time. There the operands' way into the SMs bounds it: 757 cycles for a stage's 51 KB (68 bytes a cycle and SM, the
 // four stages that shared memory holds all in flight), its MMAs 318.
 //
