@@ -25,9 +25,8 @@
 //
 // Measured, 12288 -> 6144, with the rows' quantisation: 16 rows 18.0 us with the weights in L2, 20.0 out of HBM (42.5
 // MB, 6.4 us at the copy rate: latencies of a short kernel, the quantiser before it and the cluster's join are the
-// rest); 4096 rows 145 us, 26 of them the quantiser's, 5.2 PFLOP/s in the product, tensor pipe active 54 % of the
-// time. There the operands' way into the SMs bounds it: 757 cycles for a stage's 51 KB (68 bytes a cycle and SM, the
-// four stages that shared memory holds all in flight), its MMAs 318.
+// rest); 4096 rows 149 us, 26 of them the quantiser's. There the operands' way into the SMs bounds it: each SM takes
+// 51 KB a stage, and the four stages that shared memory holds are all in flight.
 //
 // Warp roles: 0 weight codes, 1 tensor-memory allocation and MMA issue, 2 weight scales, 3
 // activation codes and scales, 4..7 epilogue (warp w reads
@@ -78,8 +77,7 @@ struct LinearSched {
   int tiles;    // all tiles: mt times the activation tiles
   int nkb;      // stages per tile
   int splits;   // CTAs per tile (a cluster along k); 1: persistent
-  bool pair;    // persistent in pairs: a tile is two neighbouring weight tiles, mt counts those
-  bool group;   // activation tiles in groups
+  bool group;   // persistent, activation tiles in groups
 };
 
 struct LinearParams {
@@ -114,28 +112,6 @@ __device__ __forceinline__ uint64_t sf_desc(uint32_t smem) {
 // Those rows to four TMEM columns, repeated in all four 32-lane quarters.
 __device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-// Copies to the same place in both CTAs of a pair, each completing on its own CTA's barrier.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y, uint32_t bar, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(pol)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_copy_pair(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1], %2, [%3], %4, %5;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "h"(static_cast<uint16_t>(3)), "l"(pol)
-      : "memory");
-}
-// Arrive on the barrier at this place in both CTAs of a pair when this thread's MMAs so far are done.
-__device__ __forceinline__ void umma_commit_pair(uint32_t mbar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
 }
 // A position in the ring of stages: slot and the parity of its current round.
 template <int STAGES>
@@ -183,7 +159,7 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // ------------------------------------------------------------------------------- kernel
-template <int NT, bool SPLIT, bool PAIR, bool GROUP>
+template <int NT, bool SPLIT, bool GROUP>
 __global__ void __launch_bounds__(kLThreads, 1)
     linear_fp4_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const LinearParams p, const LinearSched c) {
@@ -202,9 +178,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this CTA's tiles t0, t0 + step, ... and its stages kb0 .. kb0 + nkb of each
-  const uint32_t rank = SPLIT || PAIR ? cta_rank() : 0u;
-  const int t0 = SPLIT ? static_cast<int>(blockIdx.x) / c.splits : static_cast<int>(blockIdx.x) >> (PAIR ? 1 : 0);
-  const int step = SPLIT ? c.tiles : static_cast<int>(gridDim.x) >> (PAIR ? 1 : 0);
+  const uint32_t rank = SPLIT ? cta_rank() : 0u;
+  const int t0 = SPLIT ? static_cast<int>(blockIdx.x) / c.splits : static_cast<int>(blockIdx.x);
+  const int step = SPLIT ? c.tiles : static_cast<int>(gridDim.x);
   // Tile t: every weight tile in turn for each activation tile, or (GROUP) for each kGroup activation tiles.
   auto weight_tile = [&](int t) {
     if constexpr (!GROUP) return t % c.mt;
@@ -216,15 +192,14 @@ __global__ void __launch_bounds__(kLThreads, 1)
     const int g = t / (c.mt * kGroup), left = c.tiles / c.mt - g * kGroup;
     return g * kGroup + (t - g * c.mt * kGroup) % (left < kGroup ? left : kGroup);
   };
-  // first weight row of tile t (a pair's CTAs take neighbouring weight tiles)
-  auto tile_row = [&](int t) { return (weight_tile(t) * (PAIR ? 2 : 1) + (PAIR ? static_cast<int>(rank) : 0)) * kLM; };
+  auto tile_row = [&](int t) { return weight_tile(t) * kLM; };  // first weight row of tile t
   const int kb0 = SPLIT ? static_cast<int>(rank) * c.nkb / c.splits : 0;
   const int nkb = (SPLIT ? (static_cast<int>(rank) + 1) * c.nkb / c.splits : c.nkb) - kb0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&full[i]), 3);  // the two producers and the scale warp
-      mbar_init(smem_addr(&empty[i]), PAIR ? 2 : 1);
+      mbar_init(smem_addr(&empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&acc_full[i]), 1);
@@ -238,7 +213,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmemCols);
   tmem_fence_before_sync();
   __syncthreads();
-  if constexpr (PAIR) cluster_barrier();  // the pair's barriers are ready for each other's arrivals
   tmem_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   auto aborted = [&] { return *reinterpret_cast<volatile int*>(&abort_flag) != 0; };
@@ -328,21 +302,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
           const uint32_t bar = smem_addr(&full[r.s]);
           const uint32_t st = smem_addr(smem) + r.s * TL::kStageBytes + kABytes;
           mbar_arrive_expect_tx(bar, TL::kBBytes + kSfChunk * kChunks);
-          if constexpr (PAIR) {
-            // each CTA of the pair fetches half of the rows and of the scales for both
-            tma_load_2d_pair(st + rank * (TL::kBBytes / 2), &tm_x, kb * (kLK / 2), xt * NT + static_cast<int>(rank) * (NT / 2),
-                             bar, pol);
-            constexpr uint32_t kHalf = kSfChunk * kChunks / 2;  // of the chunks' scales taken in a row
-            const int ch = static_cast<int>(rank * kHalf) / kSfChunk;
-            bulk_copy_pair(st + TL::kBBytes + kSfChunk + rank * kHalf,
-                           sf + static_cast<size_t>(ch) * (p.kp / 64) * 512 + rank * kHalf % kSfChunk, kHalf, bar, pol);
-          } else {
-            tma_load_2d(st, &tm_x, kb * (kLK / 2), xt * NT, bar, pol);
+          tma_load_2d(st, &tm_x, kb * (kLK / 2), xt * NT, bar, pol);
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch)
-              bulk_copy_g2s(st + TL::kBBytes + kSfChunk * (1 + ch), sf + static_cast<size_t>(ch) * (p.kp / 64) * 512,
-                            kSfChunk, bar, pol);
-          }
+          for (int ch = 0; ch < kChunks; ++ch)
+            bulk_copy_g2s(st + TL::kBBytes + kSfChunk * (1 + ch), sf + static_cast<size_t>(ch) * (p.kp / 64) * 512, kSfChunk,
+                          bar, pol);
         }
         r.next();
       }
@@ -378,9 +342,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             for (int ch = 0; ch < kChunks; ++ch) tmem_copy_sf(sfb + 4 * ch, ds + (kSfChunk / 16) * (1 + ch) + 32 * k);
             umma_fp4(acc, da + 2 * k, db + 2 * k, idesc, sfa, sfb, (kb | k) != 0 ? 1u : 0u);
           }
-          // the stage is free once these have read it (a pair fills the stages of both: both say so)
-          if constexpr (PAIR) umma_commit_pair(smem_addr(&empty[r.s]));
-          else umma_commit(smem_addr(&empty[r.s]));
+          umma_commit(smem_addr(&empty[r.s]));  // the stage is free once these have read it
         }
         r.next();
       }
@@ -554,7 +516,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
   }
   tmem_fence_before_sync();
   __syncthreads();
-  if constexpr (PAIR) cluster_barrier();  // neither CTA leaves while the other may still write to it
   if (warp == 1) {
     // after a timeout the epilogue may have stopped early: tensor memory is released only once the
     // MMAs issued into it are done (normally this returns at once)
@@ -598,17 +559,10 @@ LinearSched make_sched(int R, int N, int kp, int sm_count) {
       c.splits = splits;
     }
   }
-  // Whole tiles on a full grid run in pairs of CTAs that share the activations' copies: without, the
-  // operands' way from L2 to the SMs is the bound (4096 rows of 12288 -> 6144: 195 us, with 169).
-  c.pair = c.splits == 1 && c.nt >= 128 && c.tiles >= sm_count;
-  if (c.pair) {
-    c.tiles = c.tiles / c.mt * ((c.mt + 1) / 2);
-    c.mt = (c.mt + 1) / 2;
-  }
   // Weights beyond half of L2 are passed over once for kGroup activation tiles (154880 x 6144, 256 rows: 137 us, with
   // a pass for each tile 183); shorter ones stay there while the activations go by (the groups' divisions cost 2 us
   // of 90 at 2048 rows of 6144 -> 12288).
-  c.group = c.pair && static_cast<int64_t>(N) * kp * 9 / 16 > (64 << 20);
+  c.group = c.splits == 1 && c.nt >= 128 && c.tiles >= sm_count && static_cast<int64_t>(N) * kp * 9 / 16 > (64 << 20);
   return c;
 }
 
@@ -634,12 +588,12 @@ size_t bind(LinearWs* w, uint8_t* p, int R, int K) {
   return static_cast<size_t>(p - p0);
 }
 
-template <int NT, bool SPLIT, bool PAIR, bool GROUP = false>
+template <int NT, bool SPLIT, bool GROUP>
 cudaError_t launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const LinearParams& p, const LinearSched& c,
                         int sm_count, cudaStream_t stream) {
   static std::mutex mu;
   static bool done[64] = {};
-  const void* kernel = reinterpret_cast<const void*>(linear_fp4_kernel<NT, SPLIT, PAIR, GROUP>);
+  const void* kernel = reinterpret_cast<const void*>(linear_fp4_kernel<NT, SPLIT, GROUP>);
   constexpr size_t smem = LTile<NT>::kSmem;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -658,9 +612,8 @@ cudaError_t launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const Line
   LinearSched cc = c;
   void* args[] = {&w, &x, &pp, &cc};
   cudaLaunchConfig_t cfg = {};
-  const int places = PAIR ? sm_count / 2 : sm_count;
-  const int cluster = SPLIT ? c.splits : (PAIR ? 2 : 1);
-  cfg.gridDim = dim3(static_cast<unsigned>((SPLIT || c.tiles < places ? c.tiles : places) * cluster));
+  const int cluster = SPLIT ? c.splits : 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT || c.tiles < sm_count ? c.tiles * cluster : sm_count));
   cfg.blockDim = dim3(kLThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -681,9 +634,7 @@ cudaError_t launch_nt(const CUtensorMap& tw, const CUtensorMap& tx, const Linear
                       int sm_count, cudaStream_t stream) {
   if (c.splits > 1) return launch_tile<NT, true, false>(tw, tx, p, c, sm_count, stream);
   if constexpr (NT >= 128)
-    if (c.pair)
-      return c.group ? launch_tile<NT, false, true, true>(tw, tx, p, c, sm_count, stream)
-                     : launch_tile<NT, false, true>(tw, tx, p, c, sm_count, stream);
+    if (c.group) return launch_tile<NT, false, true>(tw, tx, p, c, sm_count, stream);
   return launch_tile<NT, false, false>(tw, tx, p, c, sm_count, stream);
 }
 
@@ -715,7 +666,7 @@ cudaError_t launch_linear_fp4(const Fp4LinearArgs& a, cudaStream_t stream) {
   const int kp = fp4_padded(a.K);
   const LinearSched c = make_sched(a.R, a.N, kp, di.sm_count);
   CUtensorMap tw, tx;
-  if (!code_map(&tw, a.w.q, a.N, kp, kLM, enc) || !code_map(&tx, w.q, a.R, kp, c.pair ? c.nt / 2 : c.nt, enc)) return cudaErrorNotSupported;
+  if (!code_map(&tw, a.w.q, a.N, kp, kLM, enc) || !code_map(&tx, w.q, a.R, kp, c.nt, enc)) return cudaErrorNotSupported;
   err = launch_fp4_quantize(a.x, w.q, w.sf, w.rs, a.status, a.valid, a.R, a.K, stream, c.nt);
   if (err != cudaSuccess) return err;
   const LinearParams p{a.w.bs, a.w.rs, w.sf, w.rs, a.y, a.status, a.R, a.N, kp};
