@@ -487,8 +487,8 @@ int mtp_head_sample(const void* logits, int logits_dtype, int64_t ld, const floa
  * and prob 0. A draft outside [0, V) that is reached is rejected (MTP_ERR_TOKEN_RANGE); a sequence
  * with draft_len outside 0..D, or u outside [0, 1) at any i < n or at D, gives accepted 0, tokens -1
  * and prob 0 (MTP_ERR_ARG).
- * 1 <= B <= 65536, 1 <= D <= 1024, 1 <= V < 2^31. No workspace. `tokens` must not overlap
- * draft_tokens (MTP_ERR_ARG).
+ * 1 <= B <= 65536, 1 <= D <= 1024, 1 <= V < 2^31. No workspace. No output may overlap an input or
+ * another output (MTP_ERR_ARG): accepted in the place of draft_len, for one, is refused.
  * ---------------------------------------------------------------------------------------- */
 int mtp_head_verify(const float* target_probs, const float* draft_probs,
                     const int32_t* draft_tokens, const int32_t* draft_len, const float* u,

@@ -46,8 +46,13 @@ int mtp_head_verify(const float* target_probs, const float* draft_probs, const i
   if (!aligned(target_probs, 4) || bad4(draft_probs) || !aligned(draft_tokens, 4) || bad4(draft_len) ||
       !aligned(u, 4) || !aligned(tokens, 4) || !aligned(accepted, 4) || bad4(prob) || bad4(status))
     return MTP_ERR_ALIGN;
-  const size_t b = static_cast<size_t>(B);
-  if (overlap(tokens, b * (D + 1) * 4, draft_tokens, b * D * 4)) return MTP_ERR_ARG;
+  // (the CTAs of a sequence read its length, its numbers and its drafts in their own time: one that found another's
+  // result in their place would take part in other exchanges than its peers)
+  const size_t b = static_cast<size_t>(B), d = static_cast<size_t>(D), v = static_cast<size_t>(V);
+  const Span outs[] = {{tokens, b * (d + 1) * 4}, {accepted, b * 4}, {prob, b * 4}, {status, 4}};
+  const Span ins[] = {{target_probs, b * (d + 1) * v * 4}, {draft_probs, b * d * v * 4}, {draft_tokens, b * d * 4},
+                      {draft_len, b * 4}, {u, b * (d + 1) * 4}};
+  if (outputs_overlap(outs, ins)) return MTP_ERR_ARG;
   return guarded([&] {
     VerifyArgs a{target_probs, draft_probs, draft_tokens, draft_len, u, tokens, accepted, prob, status, B, D, V};
     return map_cuda(launch_verify(a, static_cast<cudaStream_t>(stream)));

@@ -18,6 +18,23 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a != nullptr && b != nullptr && x < y + nb && y < x + na;
 }
 
+// An array that a call reads or writes (either may be absent), and whether two of them share a byte, or one of
+// `outs` shares one with any other array.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+template <size_t N, size_t M>
+bool outputs_overlap(const Span (&outs)[N], const Span (&ins)[M]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (size_t j = i + 1; j < N; ++j)
+      if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+    for (const Span& in : ins)
+      if (overlap(outs[i].p, outs[i].bytes, in.p, in.bytes)) return true;
+  }
+  return false;
+}
+
 inline int check_eps(float eps) { return (eps >= 0.0f && !isinf(eps)) ? MTP_OK : MTP_ERR_ARG; }
 
 inline int map_cuda(cudaError_t e) {

@@ -128,6 +128,22 @@ def test_outputs_on_their_inputs_are_refused(lib):
         assert lib.mtp_head_verify(A, A, A, None, A, tokens, A, None, None, B, D, V, None) == m.ERR_ARG
 
 
+@pytest.mark.parametrize("out", ["tokens", "accepted", "prob", "status"])
+@pytest.mark.parametrize("other", ["p", "q", "x", "n", "u", "tokens", "accepted", "prob", "status"])
+def test_verify_outputs_on_any_other_array_are_refused(lib, out, other):
+    """Every output of the acceptance against every other array, on its first byte and on its last."""
+    B, D, V = 2, 3, 100
+    size = dict(p=B * (D + 1) * V, q=B * D * V, x=B * D, n=B, u=B * (D + 1), tokens=B * (D + 1), accepted=B, prob=B, status=1)
+    base = {k: A + 0x100000 * i for i, k in enumerate(size)}
+    if out == other:
+        return
+    for at in (base[other], base[other] + 4 * (size[other] - 1), base[other] - 4 * (size[out] - 1)):
+        a = dict(base)
+        a[out] = at
+        assert lib.mtp_head_verify(a["p"], a["q"], a["x"], a["n"], a["u"], a["tokens"], a["accepted"], a["prob"],
+                                   a["status"], B, D, V, None) == m.ERR_ARG
+
+
 def test_binding_refuses_host_tensors_and_wrong_ranks():
     bf, i32 = torch.bfloat16, torch.int32
     w4 = m.fp4_empty(4, 64, "cpu")
