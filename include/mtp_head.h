@@ -464,7 +464,8 @@ int mtp_head_sample(const void* logits, int logits_dtype, int64_t ld, const floa
 
 /* ------------------------------------------------------------------------------------------
  * Acceptance of drafts by rejection sampling: the emitted tokens are distributed as if each had
- * been drawn from the target.
+ * been drawn from the target -- when the numbers in u are independent of the ones that drew the
+ * drafts (with u[b, i] used for both, an accepted token comes up too often or too rarely).
  *
  *   target_probs  [B, D + 1, V] fp32  the target's distribution at each draft position and after
  *   draft_probs   [B, D, V]     fp32  the distributions that the drafts were drawn from; NULL for

@@ -527,7 +527,8 @@ def mtp_head_sample(logits, u=None, token=None, prob=None, probs=None, temperatu
 def mtp_head_verify(target_probs, draft_probs, draft_tokens, u, tokens, accepted, prob=None, draft_len=None,
                     status=None, stream=None) -> None:
     """Drafts [B, D] accepted against target_probs [B, D + 1, V]; draft_probs [B, D, V], or None for
-    greedy drafts. tokens [B, D + 1], accepted [B] and prob [B] (optional) are outputs."""
+    greedy drafts. tokens [B, D + 1], accepted [B] and prob [B] (optional) are outputs. u [B, D + 1] is
+    independent of the numbers that drew the drafts."""
     (B, D1, V), dev = _first(target_probs, "target_probs", 3)
     D = D1 - 1
     _call(dev, stream, "mtp_head_verify", _t(target_probs, "target_probs", _F32, (B, D1, V), dev),

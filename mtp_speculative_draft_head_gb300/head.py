@@ -164,7 +164,8 @@ class MtpDraftHead:
 
     def verify(self, target_probs, draft_probs, draft_tokens, u, draft_len=None, status=None, stream=None):
         """Drafts [B, D] against the target's distributions [B, D + 1, V], as mtp_head_verify
-        (draft_probs None for greedy drafts): returns (tokens [B, D + 1], accepted [B])."""
+        (draft_probs None for greedy drafts): returns (tokens [B, D + 1], accepted [B]). The numbers in u are not
+        the ones that drew the drafts."""
         B, D = draft_tokens.shape
         tokens = torch.empty((B, D + 1), dtype=torch.int32, device=target_probs.device)
         accepted = torch.empty(B, dtype=torch.int32, device=target_probs.device)
