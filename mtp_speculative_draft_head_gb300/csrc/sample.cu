@@ -1044,13 +1044,17 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
       x = a.draft_tokens[b * D + i];
       if (x >= 0 && x < V) {
         const float u = a.u[b * (D + 1) + i];
-        const float p = a.target_probs[(b * (D + 1) + i) * V + x];
-        const float q = a.draft_probs ? a.draft_probs[(b * D + i) * V + x] : 1.0f;
+        // both taken into [0, 1] (NaN saturates to 0), but a NaN q refuses the draft: nothing is known of how it was
+        // drawn, and what is emitted then comes from p alone
+        const float p = __saturatef(a.target_probs[(b * (D + 1) + i) * V + x]);
+        const float qr = a.draft_probs ? a.draft_probs[(b * D + i) * V + x] : 1.0f;
+        const float q = __saturatef(qr);
         // u q < p exactly: the rounded product, and its error where it ties (in fp64, which is slow here, only
         // where the error may leave the fp32 range)
         const float h = __fmul_rn(u, q);
         ok = h < p || (h == p && __fmaf_rn(u, q, -h) < 0.0f);
         if (h < 1e-30f && p < 1e-30f) ok = static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p);
+        ok = ok && qr == qr;
       }
     }
     const uint32_t no = __ballot_sync(0xffffffffu, !ok);
