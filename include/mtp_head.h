@@ -485,7 +485,9 @@ int mtp_head_sample(const void* logits, int logits_dtype, int64_t ld, const floa
  * max(p_a - q_a, 0) when a < n (from p_a itself if that has no mass), from p_n when all are
  * accepted: the lowest index whose cumulative mass exceeds u_D times the whole. Probabilities are
  * taken into [0, 1] (NaN as 0), for the acceptance too, and need not sum to one; a draft whose
- * q_i(x_i) is NaN is rejected. A distribution without mass gives token -1 and prob 0. A draft outside [0, V) that is reached is rejected (MTP_ERR_TOKEN_RANGE); a sequence
+ * q_i(x_i) is NaN is rejected. A distribution without mass gives token -1 and prob 0; any mass, down
+ * to a subnormal number, is drawn from (the roundings of a row's masses together stay below 2^-22 of
+ * its whole). A draft outside [0, V) that is reached is rejected (MTP_ERR_TOKEN_RANGE); a sequence
  * with draft_len outside 0..D, or u outside [0, 1) at any i < n or at D, gives accepted 0, tokens -1
  * and prob 0 (MTP_ERR_ARG).
  * 1 <= B <= 65536, 1 <= D <= 1024, 1 <= V < 2^31. No workspace. No output may overlap an input or

@@ -1005,6 +1005,11 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
 // token after the a accepted ones comes from max(p_a - q_a, 0), or from p_n when all are accepted,
 // by inversion with u_D. Emitted tokens are then distributed as the target's. Bound by the read of
 // one row of p and one of q per sequence.
+//
+// Masses are whole numbers, 2^f times the residual, each off by half a unit at most. f = frac leaves room for V
+// ones; where the whole then has fewer than V 2^21 units (a row scaled far below one, a residual in p's last bits, a
+// row beyond 2^20 tokens), and the roundings together could pass 2^-22 of it, the row is summed once more with
+// the f that its sum allows, up to 2^149, at which every fp32 number is whole.
 __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int nc, int64_t slice, int frac) {
   __shared__ Shared s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1071,23 +1076,43 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
   const bool all = acc == n;
   const float* p = a.target_probs + (b * (D + 1) + acc) * V;
   const float* q = !all && a.draft_probs ? a.draft_probs + (b * D + acc) * V : nullptr;
-  bool plain = false;  // the residual is empty: the target's own row
   auto left_of = [&](float pv, float qv, int64_t i) -> float {
     if (!q) qv = i == rejected_token ? 1.0f : 0.0f;
-    qv = plain || all ? 0.0f : __saturatef(qv);  // (NaN saturates to 0)
+    qv = all ? 0.0f : __saturatef(qv);  // (NaN saturates to 0)
     return __saturatef(__fsub_rn(__saturatef(pv), qv));
   };
-  auto mass_of = [&](float pv, float qv, int64_t i) -> u64 {
-    const uint32_t r = __float_as_uint(left_of(pv, qv, i));
-    // (a subnormal's mantissa gets a bit too much here, and rounds to nothing all the same)
-    return shift_round((r & 0x7FFFFFu) | 0x800000u, static_cast<int>(r >> 23) - 150 + frac);
+  // 2^bits r to the nearest whole number (a subnormal's mantissa, and a zero's, get a bit too much here: they round
+  // to nothing all the same while bits <= 63)
+  auto whole = [](float r, int bits) -> u64 {
+    const uint32_t u = __float_as_uint(r);
+    return shift_round((u & 0x7FFFFFu) | 0x800000u, static_cast<int>(u >> 23) - 150 + bits);
   };
-  auto residual = [&](int64_t i) -> float { return left_of(__ldg(p + i), q ? __ldg(q + i) : 0.0f, i); };
   const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
-  u64 z = 0ull;
-  for (int pass = 0; pass < 2; ++pass) {
+  const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
+  // The row's mass from the lanes' sums; s.wsum and s.cta keep the warps' and the CTAs'.
+  auto share = [&](u64 sum, bool first) -> u64 {
+    sum = warp_sum(sum);
+    if (lane == 0) s.wsum[warp] = sum;
+    __syncthreads();
+    u64 mine = 0ull;
+    for (int w = 0; w < kW; ++w) mine += s.wsum[w];
+    if (nc > 1) {  // the peers run, and have read the previous pass's masses
+      if (first) cluster_wait_here();
+      else cluster_sync_all();
+    }
+    if (tid < nc) {
+      if (nc > 1) st_peer(peer(&s.cta[rank], tid), mine);
+      else s.cta[0] = mine;
+    }
+    if (nc > 1) cluster_sync_all();
+    else __syncthreads();
+    u64 z = 0ull;
+    for (int r = 0; r < nc; ++r) z += s.cta[r];
+    return z;
+  };
+  u64 z;
+  {
     u64 sum = 0ull;
-    const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
     // steps of 128 elements, two steps' loads under the work on the two before
     auto load4 = [&](const float* row, int64_t i) {
       if (wide && i + 4 <= w1) return __ldg(reinterpret_cast<const float4*>(row + i));
@@ -1106,6 +1131,7 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
         qn[j] = q ? load4(q, i + 128 * j) : none;
       }
     };
+    auto mass = [&](float pv, float qv, int64_t i) { return whole(left_of(pv, qv, i), frac); };
     fetch(w0 + 4 * lane);
 #pragma unroll 1
     for (int64_t i = w0 + 4 * lane; i - 4 * lane < w1; i += 128 * kBatch) {
@@ -1119,29 +1145,42 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int64_t at = i + 128 * j;  // (past the end the loads gave zeros)
-        sum += mass_of(pv[j].x, qv[j].x, at) + mass_of(pv[j].y, qv[j].y, at + 1) + mass_of(pv[j].z, qv[j].z, at + 2) +
-               mass_of(pv[j].w, qv[j].w, at + 3);
+        sum += mass(pv[j].x, qv[j].x, at) + mass(pv[j].y, qv[j].y, at + 1) + mass(pv[j].z, qv[j].z, at + 2) +
+               mass(pv[j].w, qv[j].w, at + 3);
       }
     }
-    sum = warp_sum(sum);
-    if (lane == 0) s.wsum[warp] = sum;
-    __syncthreads();
-    u64 mine = 0ull;
-    for (int w = 0; w < kW; ++w) mine += s.wsum[w];
-    if (nc > 1) {  // the peers run, and have read the previous pass's masses
-      if (pass == 0) cluster_wait_here();
-      else cluster_sync_all();
+    z = share(sum, true);
+  }
+  // Too coarse: again, with what the sum leaves room for. f is the fraction bits of the masses that z, s.wsum and
+  // s.cta hold; a residual is lifted out of the subnormal range first where f needs it. (A loop of its own: one loop
+  // for both cost the ordinary row 5 to 9 %.)
+  constexpr int kExact = 149, kLift = 86;
+  const u64 enough = static_cast<u64>(V) << 21;
+  bool plain = false;  // the residual is empty: the target's own row
+  int f = frac;
+  auto residual = [&](int64_t i) -> float {
+    const float pv = __ldg(p + i);
+    return plain ? __saturatef(pv) : left_of(pv, q ? __ldg(q + i) : 0.0f, i);
+  };
+  auto mass_at = [&](int64_t i) -> u64 {
+    const float r = residual(i);
+    return f > 62 ? whole(__fmul_rn(r, 0x1p86f), f - kLift) : whole(r, f);
+  };
+#pragma unroll 1
+  while (z < enough) {  // the same on every CTA
+    if (f < kExact) {   // z + V is more than the sum, and 2^61 is room enough
+      const int room = 61 - (64 - __clzll(static_cast<long long>(z + static_cast<u64>(V))));
+      f = f + room < kExact ? f + room : kExact;
+    } else if (z == 0ull && !all && !plain) {
+      plain = true;
+      f = frac;
+    } else {
+      break;
     }
-    if (tid < nc) {
-      if (nc > 1) st_peer(peer(&s.cta[rank], tid), mine);
-      else s.cta[0] = mine;
-    }
-    if (nc > 1) cluster_sync_all();
-    else __syncthreads();
-    z = 0ull;
-    for (int r = 0; r < nc; ++r) z += s.cta[r];
-    if (z != 0ull || all || plain) break;
-    plain = true;
+    u64 sum = 0ull;
+#pragma unroll 4
+    for (int64_t i = w0 + lane; i < w1; i += 32) sum += mass_at(i);
+    z = share(sum, false);
   }
   if (rank == 0) {
     for (int i = tid; i <= a.D; i += kT)
@@ -1157,12 +1196,12 @@ __global__ void __launch_bounds__(kT, 2) verify_kernel(const VerifyArgs a, int n
   }
   if (z != 0ull)
     locate(s, rank, scale_floor(ud, z), i0, seg, i1,
-           [&](int64_t i) { return mass_of(__ldg(p + i), q ? __ldg(q + i) : 0.0f, i); },
+           mass_at,
            [&](int64_t i) {
              a.tokens[b * (D + 1) + acc] = static_cast<int32_t>(i);
              if (a.prob)
                a.prob[b] = static_cast<float>(static_cast<double>(residual(i)) *
-                                              __longlong_as_double(static_cast<long long>(1023 + frac) << 52) /
+                                              __longlong_as_double(static_cast<long long>(1023 + f) << 52) /
                                               static_cast<double>(z));
            });
 }

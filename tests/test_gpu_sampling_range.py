@@ -57,3 +57,87 @@ def test_verify_takes_probabilities_into_range_before_it_compares():
             left = np.maximum(w - np.clip(np.nan_to_num(q[b, 0].double().cpu().numpy(), nan=0.0, posinf=1.0), 0.0, 1.0), 0.0)
             w = left if left.sum() > 0 else w
         assert int(tokens[b, a]) == int((np.cumsum(w) <= 0.5 * w.sum()).sum()), b
+
+
+def drawn(w, u, token, prob):
+    """The token drawn from the weights w (fp64, not normalised) by u, and its probability, are right."""
+    c = np.cumsum(w) / w.sum()
+    assert 0 <= token < w.size and w[token] > 0
+    assert (c[token - 1] if token else 0.0) - WIDEN <= u < c[token] + WIDEN, (token, u, c[token])
+    assert abs(prob - w[token] / w.sum()) <= 2.0 ** -20 * w[token] / w.sum()
+
+
+def draw_from(p, q, x, u, n):
+    """verify of one draft a sequence, with tokens, accepted and prob on the host."""
+    B = x.shape[0]
+    tokens = torch.zeros(B, 2, dtype=torch.int32, device=DEV)
+    acc, prob = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(B, device=DEV)
+    m.mtp_head_verify(p, q, x, u, tokens, acc, prob, draft_len=n)
+    return tokens.tolist(), acc.tolist(), prob.tolist()
+
+
+@pytest.mark.parametrize("V", [3, 700, 154880])
+@pytest.mark.parametrize("scale", [0.9, 1e-3, 1e-10, 1e-20, 1e-30, 1e-38, 1e-41])
+def test_verify_rows_far_below_one(V, scale):
+    """Probabilities need not sum to one: a row scaled down draws as the row itself (as fp32 holds it), however
+    little mass it has."""
+    g = np.random.default_rng(V)
+    w = np.exp(2.0 * g.standard_normal((4, 2, V)))
+    p = (w / w.max(-1, keepdims=True) * scale).astype(np.float32)
+    u = g.random((4, 2)).astype(np.float32)
+    up = lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    n = torch.zeros(4, dtype=torch.int32, device=DEV)
+    tokens, acc, prob = draw_from(up(p), None, torch.zeros(4, 1, dtype=torch.int32, device=DEV), up(u), n)
+    for b in range(4):
+        assert acc[b] == 0 and tokens[b][1] == -1
+        drawn(p[b, 0].astype(np.float64), float(u[b, 1]), tokens[b][0], prob[b])
+
+
+@pytest.mark.parametrize("V", [700, 154880])
+@pytest.mark.parametrize("top", [1e-2, 1e-6, 1e-12, 1e-30])
+def test_verify_small_residuals(V, top):
+    """After a rejection little of the target is left: nearly all of it on the rejected token (greedy drafts), or a
+    drafter that differs in the last bits only. The residual is drawn from all the same, not the target's row."""
+    g = np.random.default_rng(V + 1)
+    B, at = 6, V // 3
+    w = np.exp(3.0 * g.standard_normal((B, V)))
+    p = (w / w.max(-1, keepdims=True) * top / V).astype(np.float32)
+    p[:, at] = np.float32(0.75)
+    u = g.random((B, 2)).astype(np.float32)
+    u[:, 0] = 0.875
+    full = np.stack((p, p), 1)
+    up = lambda a: torch.from_numpy(a).to(DEV)  # noqa: E731
+    x = torch.full((B, 1), at, dtype=torch.int32, device=DEV)
+    tokens, acc, prob = draw_from(up(full), None, x, up(u), None)
+    rest = p.astype(np.float64)
+    rest[:, at] = 0.0
+    for b in range(B):
+        assert acc[b] == 0
+        drawn(rest[b], float(u[b, 1]), tokens[b][0], prob[b])
+    # q one or two steps below p or above it, and all but certain of the draft
+    q = (p * (1.0 + 2.0 ** -23 * g.integers(-2, 3, p.shape))).astype(np.float32)
+    q[:, at] = 1.0
+    tokens, acc, prob = draw_from(up(full), up(q[:, None].copy()), x, up(u), None)
+    rest = np.maximum(p.astype(np.float64) - q.astype(np.float64), 0.0)
+    for b in range(B):
+        assert acc[b] == 0
+        drawn(rest[b], float(u[b, 1]), tokens[b][0], prob[b])
+
+
+def test_verify_long_rows():
+    """2^28 tokens whose probabilities, 2^-28 and a little more, are in two halves that a step of 2^-34 would round
+    apart: the draw crosses the middle where the exact halves do."""
+    V, B = 2 ** 28, 3
+    lo, hi = np.float32(2.0 ** -28 * (1 + 0.3 / 64)), np.float32(2.0 ** -28 * (1 + 0.6 / 64))
+    p = torch.full((B, 2, V), float(lo), device=DEV)
+    p[:, :, V // 2:] = float(hi)
+    u = torch.tensor([[0.5, 0.25], [0.5, 0.4985], [0.5, 0.9]], device=DEV)
+    n = torch.zeros(B, dtype=torch.int32, device=DEV)
+    tokens, acc, prob = draw_from(p, None, torch.zeros(B, 1, dtype=torch.int32, device=DEV), u, n)
+    z = (float(lo) + float(hi)) * (V // 2)
+    for b in range(B):
+        t = tokens[b][0]
+        c = (min(t, V // 2) * float(lo) + max(t - V // 2, 0) * float(hi)) / z
+        assert abs(c - float(u[b, 1])) <= WIDEN, (t, c)
+        w = float(lo if t < V // 2 else hi) / z
+        assert abs(prob[b] - w) <= 2.0 ** -20 * w
