@@ -451,7 +451,9 @@ size_t mtp_head_context_fp4_workspace_bytes(int R, int H); /* 0 for invalid shap
  * prefix: the first top_k; of those, the ones whose preceding mass is less than top_p times the mass
  * of all of those; of those, the ones with l_i >= m + temperature * ln(min_p). At least one is
  * kept. The token is the lowest index whose cumulative kept mass, in index order, exceeds u times
- * the whole. Masses are summed in 64-bit fixed point: results do not vary from run to run.
+ * the whole. Masses are summed in 64-bit fixed point: results do not vary from run to run, and the
+ * roundings of a row's masses together stay below 2^-22 of its whole. (A distance m - l_i, or a
+ * reciprocal of the temperature, beyond the fp32 range counts as infinite.)
  * 1 <= R <= 65536, 1 <= V < 2^31. No workspace. logits and probs need their elements' alignment only;
  * probs must not overlap logits (MTP_ERR_ARG).
  * ---------------------------------------------------------------------------------------- */

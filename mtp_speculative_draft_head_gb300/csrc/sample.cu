@@ -21,7 +21,8 @@
 //
 // Masses are 64-bit fixed-point numbers (2^62 / 2^ceil(log2 V) for a weight of one), so sums do not
 // depend on the order of the atomics or of the threads: the same inputs give the same token
-// whatever the cluster size. Weights are formed in fp32 from an exponent kept as a double-float:
+// whatever the cluster size. Each is off by half a unit at most, all together by V^2 2^-62 of a whole of at
+// least one; beyond 2^20 tokens, where that passes 2^-22, a first sum of the row tells how much room it takes. Weights are formed in fp32 from an exponent kept as a double-float:
 // relative error ~2^-23, against the 2^-24 of the given random numbers.
 //
 // A cluster of CTAs shares a row; maxima, histograms and masses are combined through distributed
@@ -331,7 +332,9 @@ __device__ void sort_desc(u64* key, int size) {
   __syncthreads();
 }
 
-template <bool BF16, bool RES>
+// LONG: a row of more than kLongRow tokens.
+constexpr int64_t kLongRow = 1 << 20;
+template <bool BF16, bool RES, bool LONG>
 __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int nc, int64_t slice, int frac) {
   extern __shared__ __align__(128) uint8_t dyn[];
   Shared& s = *reinterpret_cast<Shared*>(dyn);
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
     for (int64_t i = b + 4 * q + tid; i < e; i += kT) dst[i] = 0.0f;
   };
   // 2^frac / z, for one thread
-  auto inverse = [frac](u64 z) {
+  auto inverse = [&frac](u64 z) {
     return static_cast<float>(__longlong_as_double(static_cast<long long>(1023 + frac) << 52) / static_cast<double>(z));
   };
 
@@ -521,6 +524,34 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
   weigh.ch = s.ch;
   weigh.cl = s.cl;
   weigh.frac = frac;
+  // This thread's part of the row's mass into s.wsum and s.cta (every CTA's, on every CTA); the row's.
+  auto share_mass = [&](u64 sum) -> u64 {
+    sum = warp_sum(sum);
+    if (lane == 0) s.wsum[warp] = sum;
+    __syncthreads();
+    u64 mine = 0ull;
+    for (int q = 0; q < kW; ++q) mine += s.wsum[q];
+    if (tid < nc) {
+      if (nc > 1) st_peer(peer(&s.cta[rank], tid), mine);
+      else s.cta[0] = mine;
+    }
+    sync();
+    u64 z = 0ull;
+    for (int r = 0; r < nc; ++r) z += s.cta[r];
+    return z;
+  };
+  if constexpr (LONG) {
+    u64 sum = 0ull;
+    const int64_t w0 = i0 + warp * seg, w1 = w0 + seg < i1 ? w0 + seg : i1;
+    walk(w0, w0 + 4 * lane, 128, w1, [&](const float4& v, int64_t) {
+      sum += weigh.mass(v.x) + weigh.mass(v.y) + weigh.mass(v.z) + weigh.mass(v.w);
+    });
+    // (z + V is more than the sum, V roundings included; a unit is then at most 2^-60 of the whole)
+    const u64 z = share_mass(sum) + static_cast<u64>(V);
+    frac += 62 - (64 - __clzll(static_cast<long long>(z)));
+    weigh.frac = frac;
+    sync();  // s.cta has been read everywhere before it is written again
+  }
   auto counted = [&](float l) { return inf ? l == m : l > -INFINITY; };
   auto weight = [&](float l) -> float { return counted(l) ? weigh(l) : 0.0f; };
   auto key64 = [&](float l, int64_t i) -> u64 {
@@ -946,18 +977,7 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       for (int j = 0; j < 4; ++j) sum += on[j] ? w[j] : 0ull;
     });
   }
-  sum = warp_sum(sum);
-  if (lane == 0) s.wsum[warp] = sum;
-  __syncthreads();
-  u64 mine = 0ull;
-  for (int q = 0; q < kW; ++q) mine += s.wsum[q];
-  if (tid < nc) {
-    if (nc > 1) st_peer(peer(&s.cta[rank], tid), mine);
-    else s.cta[0] = mine;
-  }
-  sync();  // the last exchange: after it every CTA reads its own shared memory only
-  u64 z = 0ull;
-  for (int r = 0; r < nc; ++r) z += s.cta[r];
+  const u64 z = share_mass(sum);  // the last exchange: after it every CTA reads its own shared memory only
   if (tid == 0) s.inv_z = inverse(z);
   __syncthreads();
   const float inv_z = s.inv_z;
@@ -1249,6 +1269,7 @@ cudaError_t launch_cluster(const void* kernel, unsigned grid, int nc, size_t sme
 
 // Longest slice that a CTA keeps in shared memory: of 227 KB, or of half of an SM's (two CTAs).
 constexpr int64_t kHeldSlice = static_cast<int64_t>((227 * 1024 - kFixedSmem) / 4 / kSliceUnit * kSliceUnit);
+static_assert(kMaxC * kHeldSlice <= kLongRow, "a long row is never held");
 constexpr int64_t kHeldSliceOfTwo = static_cast<int64_t>((113 * 1024 - kFixedSmem) / 4 / kSliceUnit * kSliceUnit);
 
 int64_t slice_of(int64_t V, int nc) { return ((V + nc - 1) / nc + kSliceUnit - 1) / kSliceUnit * kSliceUnit; }
@@ -1299,10 +1320,13 @@ cudaError_t launch_sample(const SampleArgs& in, cudaStream_t stream) {
   const bool one_each = static_cast<int64_t>(a.R) * nc <= di.sm_count || nc == 1;
   const bool res = slice <= (one_each ? kHeldSlice : kHeldSliceOfTwo);
   int frac = mass_bits(a.V);
-  const void* kern = a.bf16 ? (res ? reinterpret_cast<const void*>(sample_kernel<true, true>)
-                                   : reinterpret_cast<const void*>(sample_kernel<true, false>))
-                            : (res ? reinterpret_cast<const void*>(sample_kernel<false, true>)
-                                   : reinterpret_cast<const void*>(sample_kernel<false, false>));
+  const bool is_long = a.V > kLongRow;  // (more than any cluster holds: never with res)
+  const void* kern = a.bf16 ? (is_long ? reinterpret_cast<const void*>(sample_kernel<true, false, true>)
+                               : res   ? reinterpret_cast<const void*>(sample_kernel<true, true, false>)
+                                       : reinterpret_cast<const void*>(sample_kernel<true, false, false>))
+                            : (is_long ? reinterpret_cast<const void*>(sample_kernel<false, false, true>)
+                               : res   ? reinterpret_cast<const void*>(sample_kernel<false, true, false>)
+                                       : reinterpret_cast<const void*>(sample_kernel<false, false, false>));
   void* args[] = {&a, &nc, &slice, &frac};
   return launch_cluster(kern, static_cast<unsigned>(a.R) * nc, nc,
                         kFixedSmem + (res ? static_cast<size_t>(slice) * 4 : 0), stream, args);

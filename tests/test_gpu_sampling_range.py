@@ -141,3 +141,41 @@ def test_verify_long_rows():
         assert abs(c - float(u[b, 1])) <= WIDEN, (t, c)
         w = float(lo if t < V // 2 else hi) / z
         assert abs(prob[b] - w) <= 2.0 ** -20 * w
+
+
+@pytest.mark.parametrize("V", [2 ** 20, 2 ** 20 + 1, 3_000_001])
+@pytest.mark.parametrize("which", ["T", "Tp", "Tkp", "Tkpm"])
+def test_rows_of_about_a_million(V, which):
+    """Both sides of the length from which a row's masses are scaled by its sum."""
+    for bf in (False, True):
+        l = logits(2, V, V + bf, bf)
+        u = np.random.default_rng(V + 1).random(2).astype(np.float32).tolist()
+        par = params(2, V + 2, which)
+        if which == "Tkp":
+            par["k"] = [400000, 1000]
+        check(l, sample(l, u, par), u, par)
+
+
+@pytest.mark.parametrize("V,bits", [(2 ** 26 + 1, 37), (2 ** 28 + 3, 35), (2 ** 30 + 1, 33)])
+def test_long_rows_keep_small_weights(V, bits):
+    """One token of weight one and all the others just below 2^-bits of it: each less than half a step of a sum
+    that has room for V ones, and together 2^-11 to 2^-3 of the mass."""
+    l = torch.full((1, V), -(bits * math.log(2.0) + 0.1), device=DEV)
+    w = math.exp(float(l[0, 1]))
+    l[0, 0] = 0.0
+    z = 1.0 + w * (V - 1)
+    tail = (z - 1.0) / z
+    assert tail > 2.0 ** -12
+    t, pr, _ = sample(l, [0.5], probs=False)
+    assert int(t) == 0 and abs(float(pr) * z - 1.0) <= PROB
+    for f in (0.9, 0.5, 0.01):
+        u = float(np.float32(1.0 - f * tail))
+        t, pr, _ = sample(l, [u], probs=False)
+        assert abs((1.0 + w * (int(t) - 1)) / z - u) <= WIDEN
+        assert abs(float(pr) * z / w - 1.0) <= PROB
+    # top_p cuts among the ties, at an index
+    p = float(np.float32(1.0 - 0.5 * tail))
+    _, pr, dist = sample(l, [0.0], dict(p=[p]))
+    n = int((dist > 0).sum())
+    assert abs((1.0 + w * (n - 1)) / z - p) <= WIDEN and bool((dist[0, :n] > 0).all())
+    assert abs(float(pr) * (1.0 + w * (n - 1)) - 1.0) <= PROB
