@@ -9,7 +9,8 @@
 //
 // No sort of the row: a prefix is { i : key_i >= cut } for one 64-bit key (the logit's order bits,
 // then the complement of the index). Two ways to the cut:
-//  * top_k up to half the cluster's threads (the usual case): the k-th largest of the threads' own maxima
+//  * a top_k whose entries fit one list (the usual case; up to 780 with four CTAs a row, 910 with 16, half the
+//    threads of a single one): the k-th largest of the threads' own maxima
 //    is a bound that the k-th largest logit cannot be below, and little more than k entries reach it.
 //    These are gathered and sorted by one CTA, which finishes the row on the sorted list: no weight is
 //    formed for any other entry, and shared-memory atomics (~50 cycles for a warp's worth, the cost
@@ -765,7 +766,13 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       __syncthreads();
     };
 
-    if (use_k && 2 * k <= static_cast<int64_t>(nc) * kT) {
+    // Of n threads, n ln(n / (n - k)) entries reach the k-th largest maximum on average: at most k + 2/3 k^2 / n where
+    // that is near the list's length (k below n / 2.6; with fewer threads the list is long enough for any k up to n / 2).
+    // The rest of the list is for the spread and the bin's width. (A list that does not fit costs
+    // its row the passes made for it: with k = 1024 and no such rule 80 rows took 236 us and one row 44.7, by the
+    // histogram at once 206 and 37.3; at k = 700 with a list 57, without 203.)
+    const int64_t n_threads = static_cast<int64_t>(nc) * kT;
+    if (use_k && 2 * k <= n_threads && k <= kGather && k * (3 * n_threads + 2 * k) <= 3 * (kGather - 44) * n_threads) {
       // ---- the whole row on one sorted list: the bins of the threads' maxima first
       if (live(most)) atomicAdd(&loc.n[bin1(most)], 1u);
       share_bins(false);

@@ -179,3 +179,13 @@ def test_long_rows_keep_small_weights(V, bits):
     n = int((dist > 0).sum())
     assert abs((1.0 + w * (n - 1)) / z - p) <= WIDEN and bool((dist[0, :n] > 0).all())
     assert abs(float(pr) * (1.0 + w * (n - 1)) - 1.0) <= PROB
+
+
+@pytest.mark.parametrize("k", [256, 512, 640, 800, 1024, 1025, 2048, 4096, 4097])
+def test_top_k_around_the_length_of_the_list(k):
+    """top_k up to, at and beyond what one sorted list holds, in clusters of 16 and of 4 and with single CTAs."""
+    for R, V in ((2, 154880), (24, 50257), (160, 9000)):
+        l = logits(R, V, k + R)
+        u = np.random.default_rng(k).random(R).astype(np.float32).tolist()
+        par = dict(k=[k] * R, p=[1.0 if r % 2 else 0.96875 for r in range(R)], T=[0.5 + r % 3 for r in range(R)])
+        check(l, sample(l, u, par), u, par, rows=range(0, R, max(1, R // 6)))
