@@ -110,9 +110,9 @@ __device__ __forceinline__ u64 warp_inclusive(u64 v, int lane) {
 }
 
 // ------------------------------------------------------------------------------- numbers
-// floor(u * z) for u in [0, 1).
+// floor(u * z) for u in [0, 1); -0 is 0.
 __device__ __forceinline__ u64 scale_floor(float u, u64 z) {
-  const uint32_t b = __float_as_uint(u);
+  const uint32_t b = __float_as_uint(u) & 0x7FFFFFFFu;
   const int e = static_cast<int>(b >> 23);
   const u64 m = e == 0 ? (b & 0x7FFFFFu) : ((b & 0x7FFFFFu) | 0x800000u);
   const int sh = 150 - (e == 0 ? 1 : e);  // u = m 2^-sh, sh >= 24
@@ -124,7 +124,7 @@ __device__ __forceinline__ u64 scale_floor(float u, u64 z) {
 
 // Whether part < p * whole, for 0 <= p < 1, exactly: part <= floor(p whole) unless p whole is whole.
 __device__ __forceinline__ u64 scale_ceil(float p, u64 z) {
-  const uint32_t b = __float_as_uint(p);
+  const uint32_t b = __float_as_uint(p) & 0x7FFFFFFFu;
   const int e = static_cast<int>(b >> 23);
   const u64 m = e == 0 ? (b & 0x7FFFFFu) : ((b & 0x7FFFFFu) | 0x800000u);
   const int sh = 150 - (e == 0 ? 1 : e);

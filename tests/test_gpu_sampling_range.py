@@ -189,3 +189,23 @@ def test_top_k_around_the_length_of_the_list(k):
         u = np.random.default_rng(k).random(R).astype(np.float32).tolist()
         par = dict(k=[k] * R, p=[1.0 if r % 2 else 0.96875 for r in range(R)], T=[0.5 + r % 3 for r in range(R)])
         check(l, sample(l, u, par), u, par, rows=range(0, R, max(1, R // 6)))
+
+
+def test_negative_zero_is_zero():
+    """-0 as a random number, top_p, min_p or temperature is 0."""
+    l = logits(6, 5000, 41)
+    par = dict(T=[1.0, 0.0, 0.7, 1.0, 1.0, 1.0], p=[1.0, 1.0, 0.0, 0.0, 1.0, 0.9], k=[0, 0, 0, 40, 900, 0], mp=[0.0] * 6)
+    neg = {n: [-0.0 if v == 0.0 and n != "k" else v for v in vs] for n, vs in par.items()}
+    a, b = sample(l, [0.0] * 6, par), sample(l, [-0.0] * 6, neg)
+    check(l, a, [0.0] * 6, par)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+    p = torch.softmax(logits(4, 5000, 42), 1).view(2, 2, 5000).contiguous()
+    x = torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    out = []
+    for z in (0.0, -0.0):
+        u = torch.full((2, 2), z, device=DEV)
+        t, acc = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+        m.mtp_head_verify(p, p[:, :1].contiguous(), x, u, t, acc)
+        out.append((t.tolist(), acc.tolist()))
+    assert out[0] == out[1]
