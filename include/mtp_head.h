@@ -365,7 +365,8 @@ int mtp_head_quantize_fp8(const uint16_t* w, uint8_t* q, float* row_scale, int32
  * to Hp are zeros. An all-zero row (or one so small that row_scale rounds to 0) gives zeros, and so
  * does an all-zero block. A NaN or Inf weight stores MTP_ERR_NONFINITE in `status` (required here)
  * and makes that row zeros. 1 <= H <= 131072 (an eh_proj row of the longest head). q and
- * block_scale must be 16-byte aligned.
+ * block_scale must be 16-byte aligned. In this and the next four calls an output or a workspace on an
+ * input that is still read, or on another output, is MTP_ERR_ARG.
  * mtp_head_dequantize_fp4 writes the BF16 matrix that a copy stands for:
  *   w[v, k] = bf16( fp32( q * block_scale * row_scale ) ), w [V, H] BF16.
  * ---------------------------------------------------------------------------------------- */
@@ -404,7 +405,7 @@ size_t mtp_head_fp4_workspace_bytes(int B, int H, int V); /* 0 for invalid shape
  *   status      optional: MTP_ERR_NONFINITE when a row of x holds a NaN or Inf (its y row is zeros)
  *   workspace   at least mtp_head_linear_fp4_workspace_bytes(R, N, K) bytes, no initialisation
  *               needed; calls that may run at the same time need different ones
- *   1 <= R <= 65536, 1 <= N, 1 <= K <= 131072
+ *   1 <= R <= 65536, 1 <= N, 1 <= K <= 131072; y may take the place of x
  * ---------------------------------------------------------------------------------------- */
 int mtp_head_linear_fp4(const uint16_t* x, const uint8_t* q, const uint8_t* block_scale,
                         const float* row_scale, uint16_t* y, int32_t* status, void* workspace,
@@ -415,7 +416,8 @@ size_t mtp_head_linear_fp4_workspace_bytes(int R, int N, int K); /* 0 for invali
 /* Context-row input stage (mtp_head_context_rows) with an FP4 copy of eh_proj ([H, 2H]): the
  * normalised concat rows, then mtp_head_linear_fp4 over them. A row whose token is outside [0, V)
  * is zeros and status (optional) gets MTP_ERR_TOKEN_RANGE. 1 <= R <= 65536 rows (a draft step's
- * sequences or a prompt's rows alike); H a multiple of 8 (MTP_ERR_NOT_IMPLEMENTED otherwise).
+ * sequences or a prompt's rows alike); H a multiple of 8 (MTP_ERR_NOT_IMPLEMENTED otherwise). x_out
+ * may take the place of target_hidden.
  * workspace: at least mtp_head_context_fp4_workspace_bytes(R, H) bytes, no initialisation. */
 int mtp_head_context_rows_fp4(const uint16_t* embed, const uint16_t* enorm_w,
                               const uint16_t* hnorm_w, const uint8_t* eh_q,

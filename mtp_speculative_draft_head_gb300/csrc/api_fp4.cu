@@ -18,6 +18,16 @@ bool bad_fp4(const uint8_t* q, const uint8_t* bs, const float* rs) {
   return !aligned(q, 16) || !aligned(bs, 16) || !aligned(rs, 4);
 }
 
+// The arrays of a copy of [rows, k].
+struct CopySpans {
+  Span q, bs, rs;
+  CopySpans(const uint8_t* qp, const uint8_t* bp, const float* rp, int rows, int k)
+      : q{qp, static_cast<size_t>(rows) * (fp4_padded(k) / 2)},
+        bs{bp, static_cast<size_t>(rows) * (fp4_padded(k) / kFp4Block)},
+        rs{rp, static_cast<size_t>(rows) * 4} {}
+};
+Span bf16_span(const uint16_t* p, int rows, int k) { return {p, static_cast<size_t>(rows) * k * 2}; }
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace of the context-row path: the concat [R, 2H] BF16, the row flags, then the linear's.
@@ -36,6 +46,9 @@ int mtp_head_quantize_fp4(const uint16_t* w, uint8_t* q, uint8_t* block_scale, f
   if (!w || !q || !block_scale || !row_scale || !status) return MTP_ERR_ARG;
   if (V < 1 || H < 1 || H > kMaxFp4K) return MTP_ERR_SHAPE;
   if (!aligned(w, 16) || bad_fp4(q, block_scale, row_scale) || !aligned(status, 4)) return MTP_ERR_ALIGN;
+  const CopySpans c(q, block_scale, row_scale, V, H);
+  const Span outs[] = {c.q, c.bs, c.rs, {status, 4}}, ins[] = {bf16_span(w, V, H)};
+  if (outputs_overlap(outs, ins)) return MTP_ERR_ARG;
   return guarded([&] {
     return map_cuda(launch_fp4_quantize(w, q, block_scale, row_scale, status, nullptr, V, H,
                                         static_cast<cudaStream_t>(stream)));
@@ -47,6 +60,9 @@ int mtp_head_dequantize_fp4(const uint8_t* q, const uint8_t* block_scale, const 
   if (!w || !q || !block_scale || !row_scale) return MTP_ERR_ARG;
   if (V < 1 || H < 1 || H > kMaxFp4K) return MTP_ERR_SHAPE;
   if (!aligned(w, 16) || bad_fp4(q, block_scale, row_scale)) return MTP_ERR_ALIGN;
+  const CopySpans c(q, block_scale, row_scale, V, H);
+  const Span outs[] = {bf16_span(w, V, H)}, ins[] = {c.q, c.bs, c.rs};
+  if (outputs_overlap(outs, ins)) return MTP_ERR_ARG;
   return guarded([&] {
     return map_cuda(launch_fp4_dequantize(Fp4Matrix{q, block_scale, row_scale}, w, V, H,
                                           static_cast<cudaStream_t>(stream)));
@@ -70,6 +86,11 @@ int mtp_head_logits_argmax_fp4(const uint16_t* x, const uint16_t* final_norm_w, 
       (workspace && !aligned(workspace, 16)))
     return MTP_ERR_ALIGN;
   if (!workspace || workspace_bytes < fp4_sweep_workspace_bytes(B, H)) return MTP_ERR_WORKSPACE;
+  const CopySpans c(q, block_scale, row_scale, V, H);
+  const Span ws[] = {{workspace, fp4_sweep_workspace_bytes(B, H)}};
+  const Span outs[] = {{logits, static_cast<size_t>(B) * V * 4}, {draft, static_cast<size_t>(B) * 4}, {status, 4}, ws[0]};
+  const Span copy[] = {c.q, c.bs, c.rs}, ins[] = {bf16_span(x, B, H), bf16_span(final_norm_w, 1, H)};
+  if (outputs_overlap(outs, copy) || outputs_overlap(ws, ins)) return MTP_ERR_ARG;
   return guarded([&] {
     Fp4SweepArgs a{x, final_norm_w, Fp4Matrix{q, block_scale, row_scale}, logits, draft, status,
                    static_cast<uint8_t*>(workspace), B, H, V, eps};
@@ -91,6 +112,11 @@ int mtp_head_linear_fp4(const uint16_t* x, const uint8_t* q, const uint8_t* bloc
       (workspace && !aligned(workspace, 16)))
     return MTP_ERR_ALIGN;
   if (!workspace || workspace_bytes < fp4_linear_workspace_bytes(R, N, K)) return MTP_ERR_WORKSPACE;
+  const CopySpans c(q, block_scale, row_scale, N, K);
+  const Span side[] = {{status, 4}, {workspace, fp4_linear_workspace_bytes(R, N, K)}};
+  const Span outs[] = {bf16_span(y, R, N), side[0], side[1]}, copy[] = {c.q, c.bs, c.rs}, ins[] = {bf16_span(x, R, K)};
+  // (y on x is fine: x has been quantised when the first row of y is written)
+  if (outputs_overlap(outs, copy) || outputs_overlap(side, ins)) return MTP_ERR_ARG;
   return guarded([&] {
     Fp4LinearArgs a{x, nullptr, Fp4Matrix{q, block_scale, row_scale}, y, status, static_cast<uint8_t*>(workspace),
                     R, N, K};
@@ -117,6 +143,15 @@ int mtp_head_context_rows_fp4(const uint16_t* embed, const uint16_t* enorm_w, co
     return MTP_ERR_ALIGN;
   if (H % 8 != 0) return MTP_ERR_NOT_IMPLEMENTED;
   if (!workspace || workspace_bytes < mtp_head_context_fp4_workspace_bytes(R, H)) return MTP_ERR_WORKSPACE;
+  {
+    const CopySpans c(eh_q, eh_block_scale, eh_row_scale, H, 2 * H);
+    const Span side[] = {{status, 4}, {workspace, mtp_head_context_fp4_workspace_bytes(R, H)}};
+    const Span outs[] = {bf16_span(x_out, R, H), side[0], side[1]}, copy[] = {c.q, c.bs, c.rs};
+    const Span ins[] = {bf16_span(embed, V, H), bf16_span(enorm_w, 1, H), bf16_span(hnorm_w, 1, H),
+                        {tokens, static_cast<size_t>(R) * 4}, bf16_span(target_hidden, R, H)};
+    // (x_out on target_hidden is fine: the concat rows are made when the first row of x_out is written)
+    if (outputs_overlap(outs, copy) || outputs_overlap(side, ins)) return MTP_ERR_ARG;
+  }
   return guarded([&] {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     ContextArgs c{};

@@ -144,6 +144,50 @@ def test_verify_outputs_on_any_other_array_are_refused(lib, out, other):
                                    a["status"], B, D, V, None) == m.ERR_ARG
 
 
+def _refused(call, size, pairs):
+    """call(addresses) is refused with MTP_ERR_ARG whenever the first array of a pair shares the first or the last
+    bytes of the second (arrays are 16-byte aligned, so are the shifts)."""
+    base = {k: A + 0x10000000 * i for i, k in enumerate(size)}
+    for out, other in pairs:
+        last = (size[other] - 1) // 16 * 16
+        for at in (base[other], base[other] + last, base[other] - (size[out] - 1) // 16 * 16):
+            assert call(dict(base, **{out: at})) == m.ERR_ARG, (out, other)
+
+
+COPY = ("q", "bs", "rs")
+
+
+def test_fp4_outputs_on_what_is_still_read_are_refused(lib):
+    V, H = 40, 500
+    copy = dict(q=V * 256, bs=V * 32, rs=V * 4)
+    _refused(lambda a: lib.mtp_head_quantize_fp4(a["w"], a["q"], a["bs"], a["rs"], a["st"], V, H, None),
+             dict(copy, w=V * H * 2, st=4),
+             [(o, i) for o in (*COPY, "st") for i in ("w", *COPY, "st") if o != i])
+    _refused(lambda a: lib.mtp_head_dequantize_fp4(a["q"], a["bs"], a["rs"], a["w"], V, H, None),
+             dict(copy, w=V * H * 2), [("w", i) for i in COPY])
+    B = 3
+    ws = m.mtp_head_fp4_workspace_bytes(B, H, V)
+    _refused(lambda a: lib.mtp_head_logits_argmax_fp4(a["x"], a["fw"], a["q"], a["bs"], a["rs"], a["lg"], a["d"], a["st"],
+                                                      a["ws"], ws, B, H, V, ctypes.c_float(1e-6), None),
+             dict(copy, x=B * H * 2, fw=H * 2, lg=B * V * 4, d=B * 4, st=4, ws=ws),
+             [(o, i) for o in ("lg", "d", "st", "ws") for i in (*COPY, "lg", "d", "st", "ws") if o != i] +
+             [("ws", "x"), ("ws", "fw")])
+    R = 5
+    wl = m.mtp_head_linear_fp4_workspace_bytes(R, V, H)
+    _refused(lambda a: lib.mtp_head_linear_fp4(a["x"], a["q"], a["bs"], a["rs"], a["y"], a["st"], a["ws"], wl, R, V, H,
+                                               None),
+             dict(copy, x=R * H * 2, y=R * V * 2, st=4, ws=wl),
+             [(o, i) for o in ("y", "st", "ws") for i in (*COPY, "y", "st", "ws") if o != i] + [("ws", "x"), ("st", "x")])
+    h, v = 64, 40
+    wc = m.mtp_head_context_fp4_workspace_bytes(R, h)
+    _refused(lambda a: lib.mtp_head_context_rows_fp4(a["e"], a["en"], a["hn"], a["q"], a["bs"], a["rs"], a["t"], a["h"],
+                                                     a["x"], a["st"], a["ws"], wc, R, h, v, ctypes.c_float(1e-6), None),
+             dict(q=h * 128, bs=h * 16, rs=h * 4, e=v * h * 2, en=h * 2, hn=h * 2, t=R * 4, h=R * h * 2, x=R * h * 2, st=4,
+                  ws=wc),
+             [(o, i) for o in ("x", "st", "ws") for i in (*COPY, "x", "st", "ws") if o != i] +
+             [("ws", i) for i in ("e", "en", "hn", "t", "h")])
+
+
 def test_binding_refuses_host_tensors_and_wrong_ranks():
     bf, i32 = torch.bfloat16, torch.int32
     w4 = m.fp4_empty(4, 64, "cpu")
