@@ -456,8 +456,9 @@ size_t mtp_head_context_fp4_workspace_bytes(int R, int H); /* 0 for invalid shap
  * the whole. Masses are summed in 64-bit fixed point: results do not vary from run to run, and the
  * roundings of a row's masses together stay below 2^-22 of its whole. (A distance m - l_i, or a
  * reciprocal of the temperature, beyond the fp32 range counts as infinite.)
- * 1 <= R <= 65536, 1 <= V < 2^31. No workspace. logits and probs need their elements' alignment only;
- * probs must not overlap logits (MTP_ERR_ARG).
+ * 1 <= R <= 65536, 1 <= V < 2^31. No workspace. logits and probs need their elements' alignment only.
+ * No output may overlap an input or another output (MTP_ERR_ARG), but token and prob may take the place
+ * of a row parameter or of u.
  * ---------------------------------------------------------------------------------------- */
 enum { MTP_LOGITS_FP32 = 0, MTP_LOGITS_BF16 = 1 };
 

@@ -28,9 +28,16 @@ int mtp_head_sample(const void* logits, int logits_dtype, int64_t ld, const floa
   if (!aligned(logits, logits_dtype == MTP_LOGITS_FP32 ? 4 : 2) || bad4(temperature) || bad4(top_k) || bad4(top_p) ||
       bad4(min_p) || bad4(u) || bad4(token) || bad4(prob) || bad4(probs) || bad4(status))
     return MTP_ERR_ALIGN;
-  // (the rows are read more than once)
-  const size_t item = logits_dtype == MTP_LOGITS_FP32 ? 4 : 2;
-  if (overlap(logits, (static_cast<size_t>(R - 1) * ld + V) * item, probs, static_cast<size_t>(R) * V * 4)) return MTP_ERR_ARG;
+  // The rows of logits are read more than once; a row's parameters by its own CTAs alone, before anything is written,
+  // so token and prob may take exactly the place of one.
+  const size_t item = logits_dtype == MTP_LOGITS_FP32 ? 4 : 2, r = static_cast<size_t>(R);
+  const Span outs[] = {{token, r * 4}, {prob, r * 4}, {probs, r * V * 4}, {status, 4}};
+  const Span row[] = {{logits, (static_cast<size_t>(R - 1) * ld + V) * item}};
+  if (outputs_overlap(outs, row)) return MTP_ERR_ARG;
+  for (const void* in : {static_cast<const void*>(temperature), static_cast<const void*>(top_k), static_cast<const void*>(top_p),
+                         static_cast<const void*>(min_p), static_cast<const void*>(u)})
+    for (const Span& o : outs)
+      if ((o.p != in || o.bytes != r * 4 || o.p == status) && overlap(o.p, o.bytes, in, r * 4)) return MTP_ERR_ARG;
   return guarded([&] {
     SampleArgs a{logits, temperature, top_k, top_p, min_p, u, token, prob, probs, status, ld, R, V,
                  logits_dtype == MTP_LOGITS_BF16};

@@ -188,6 +188,22 @@ def test_fp4_outputs_on_what_is_still_read_are_refused(lib):
              [("ws", i) for i in ("e", "en", "hn", "t", "h")])
 
 
+def test_sampler_outputs_on_what_is_still_read_are_refused(lib):
+    R, V, ld = 7, 100, 128
+    par = ("t", "k", "tp", "mp", "u")
+    size = dict(l=((R - 1) * ld + V) * 2, token=R * 4, prob=R * 4, probs=R * V * 4, st=4, **{p: R * 4 for p in par})
+    call = lambda a: lib.mtp_head_sample(a["l"], m.LOGITS_BF16, ld, *(a[p] for p in par), a["token"], a["prob"],  # noqa: E731
+                                         a["probs"], a["st"], R, V, None)
+    outs = ("token", "prob", "probs", "st")
+    _refused(call, size, [(o, i) for o in outs for i in ("l", *outs) if o != i] +
+             [(o, p) for o in ("probs", "st") for p in par])
+    base = {k: A + 0x10000000 * i for i, k in enumerate(size)}
+    for o in ("token", "prob"):  # one row off: another row's parameter
+        for p in par:
+            for shift in (4, -4, 4 * (R - 1)):
+                assert call(dict(base, **{o: base[p] + shift})) == m.ERR_ARG
+
+
 def test_binding_refuses_host_tensors_and_wrong_ranks():
     bf, i32 = torch.bfloat16, torch.int32
     w4 = m.fp4_empty(4, 64, "cpu")

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mtp_speculative_draft_head_gb300 as m
-from test_gpu_sampling import DEV, PROB, WIDEN, check, logits, params, sample
+from test_gpu_sampling import DEV, PROB, WIDEN, check, logits, params, sample, tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -209,3 +209,19 @@ def test_negative_zero_is_zero():
         m.mtp_head_verify(p, p[:, :1].contiguous(), x, u, t, acc)
         out.append((t.tolist(), acc.tolist()))
     assert out[0] == out[1]
+
+
+@pytest.mark.parametrize("R,V", [(3, 60000), (40, 20000), (200, 3000)])
+def test_token_and_prob_in_the_place_of_parameters(R, V):
+    l = logits(R, V, R)
+    u = np.random.default_rng(R).random(R).astype(np.float32).tolist()
+    par = params(R, R + 1)
+    par["T"][R - 1] = -1.0  # a refused row among them
+    token, prob, _ = sample(l, u, par, ok=False)
+    for at in ("top_k", "u"):
+        tp = tensors(par)
+        ut = torch.tensor(u, dtype=torch.float32, device=DEV)
+        t2 = tp["top_k"] if at == "top_k" else torch.zeros_like(token)
+        p2 = ut if at == "u" else tp["min_p"]
+        m.mtp_head_sample(l, ut, t2, p2, **tp)
+        assert torch.equal(t2, token) and torch.equal(p2, prob)
