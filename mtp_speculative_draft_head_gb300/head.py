@@ -123,6 +123,8 @@ class MtpDraftHead:
                 status=None, stream=None, fp4: bool = False):
         """One draft step for B sequences (device buffers): returns (x, logits|None, draft)."""
         B = tokens.numel()
+        if fp8 and fp4:
+            raise ValueError("fp8 and fp4 exclude each other")
         if fp4:
             x = self.input(tokens, hidden, x, status, stream, fp4=True)
             return (x, *self.logits_argmax(x, fp8, logits, draft, status, stream, fp4=True))

@@ -220,3 +220,11 @@ def test_binding_refuses_host_tensors_and_wrong_ranks():
     with pytest.raises(ValueError, match="dimensions"):
         m.mtp_head_verify(torch.zeros(2, 10), None, torch.zeros(2, 1, dtype=i32), torch.zeros(2, 2),
                           torch.zeros(2, 2, dtype=i32), torch.zeros(2, dtype=i32))
+
+
+def test_head_refuses_two_weight_formats_before_any_launch(monkeypatch):
+    """forward(fp8=True, fp4=True): nothing of the step has run when it is refused."""
+    head = object.__new__(m.MtpDraftHead)
+    monkeypatch.setattr(m.MtpDraftHead, "input", lambda *a, **k: pytest.fail("the input stage was launched"))
+    with pytest.raises(ValueError, match="exclude"):
+        head.forward(torch.zeros(2, dtype=torch.int32), torch.zeros(2, 64, dtype=torch.bfloat16), fp8=True, fp4=True)
