@@ -39,19 +39,16 @@
 #include "common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
+#include "linear_fp4_sched.h"
 #include "tc.cuh"
 
 namespace mtp {
 
 namespace {
 
-constexpr int kLM = 128;          // weight rows per tile
-constexpr int kLK = 256;          // codes per stage: four MMAs of 64
 constexpr int kLThreads = 256;
 constexpr int kABytes = kLM * kLK / 2;       // 16 KB of weight codes per stage
 constexpr int kSfChunk = 4 * 512;            // scales of 128 rows x 256 codes: four 512-byte blocks
-constexpr int kMaxSplits = 8;
-constexpr int kGroup = 16;        // activation tiles that share a pass over long weights
 constexpr uint32_t kTmemCols = 512;
 
 template <int NT>
@@ -69,15 +66,6 @@ struct LTile {
                                   4 * NT * 4 + kSfBufs * kSfBytes;
   static_assert(NT % 16 == 0 && NT <= 256, "N of an M = 128 MMA");
   static_assert(kSfbCol + 16 * kChunks <= kTmemCols, "tensor memory");
-};
-
-struct LinearSched {
-  int nt;       // activation rows per tile
-  int mt;       // weight tiles
-  int tiles;    // all tiles: mt times the activation tiles
-  int nkb;      // stages per tile
-  int splits;   // CTAs per tile (a cluster along k); 1: persistent
-  bool group;   // persistent, activation tiles in groups
 };
 
 struct LinearParams {
@@ -531,41 +519,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
   // (no early launch: a stage that follows may read y, as its weights, before its own wait)
 }
 
-// ------------------------------------------------------------------------------- schedule
-// Few rows (up to one tile of them): the smallest N tile, and k split over clusters until the weight
-// tiles fill the SMs. More: the N tile whose waves cost the least (a wave's time goes with N).
-LinearSched make_sched(int R, int N, int kp, int sm_count) {
-  LinearSched c{};
-  c.mt = (N + kLM - 1) / kLM;
-  c.nkb = kp / kLK;
-  c.splits = 1;
-  static const int kTiles[] = {16, 32, 64, 128, 192, 224};
-  double best = 1e30;
-  for (int nt : kTiles) {
-    if (R > 128 && nt < 64) continue;  // (the workspace holds the scale blocks of no smaller tiles)
-    const int64_t tiles = static_cast<int64_t>(c.mt) * ((R + nt - 1) / nt);
-    int splits = 1;
-    while (splits < kMaxSplits && splits < c.nkb && tiles * (splits + 1) <= sm_count &&
-           static_cast<size_t>(splits) * nt * kLM * 4 <= 160 * 1024)
-      ++splits;
-    const int64_t waves = (tiles * splits + sm_count - 1) / sm_count;
-    const int kbs = (c.nkb + splits - 1) / splits;
-    // per stage: the MMAs (N 16 columns at a time), or the copy of 128 + nt rows of codes
-    const double cost = static_cast<double>(waves) * (kbs * (nt > 96 ? nt : 96 + nt / 16) + 400.0) + nt;
-    if (cost < best) {
-      best = cost;
-      c.nt = nt;
-      c.tiles = static_cast<int>(tiles);
-      c.splits = splits;
-    }
-  }
-  // Weights beyond half of L2 are passed over once for kGroup activation tiles (154880 x 6144, 256 rows: 137 us, with
-  // a pass for each tile 183); shorter ones stay there while the activations go by (the groups' divisions cost 2 us
-  // of 90 at 2048 rows of 6144 -> 12288).
-  c.group = c.splits == 1 && c.nt >= 128 && c.tiles >= sm_count && static_cast<int64_t>(N) * kp * 9 / 16 > (64 << 20);
-  return c;
-}
-
+// ------------------------------------------------------------------------------- host side
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct LinearWs {

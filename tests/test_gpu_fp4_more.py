@@ -1,11 +1,12 @@
 """The FP4 stages where their buffers meet: outputs in the place of inputs that have been read, and weights written by
-the call just before."""
+the call just before; and every schedule of the linear."""
 import pytest
 import torch
 
 import mtp_speculative_draft_head_gb300 as m
 import synth
-from test_gpu_fp4 import DEV, EPS, bf16, make_copy, rng_matrix
+from linear_fp4_schedule import schedule
+from test_gpu_fp4 import DEV, EPS, bf16, check_linear, make_copy, rng_matrix
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,48 @@ def test_dequantised_weights_are_swept_at_once():
         got = [step(i % 2, b, lambda: None) for i in range(20)]
         for i, (lg, d) in enumerate(got):
             assert torch.equal(lg, want[i % 2][0]) and torch.equal(d, want[i % 2][1])
+
+
+# Rows, columns and k, the activation rows a tile, and how the tiles are taken: k split over a cluster, one tile a
+# CTA, several (three at least) through two accumulators, or several in groups of activation tiles. On 152 SMs.
+SCHEDULES = [
+    (9, 60001, 700, 16, "many"),
+    (27, 60001, 700, 32, "many"),
+    (50, 60001, 700, 64, "many"),
+    (90, 3333, 700, 128, "split"),
+    (1345, 777, 100, 128, "one"),
+    (70, 60001, 700, 128, "many"),
+    (225, 20300, 1500, 128, "many"),
+    (99, 60001, 2100, 128, "groups"),
+    (1345, 777, 1024, 192, "split"),
+    (450, 5200, 100, 192, "one"),
+    (300, 20300, 700, 192, "many"),
+    (140, 60001, 2100, 192, "groups"),
+    (193, 5000, 2000, 224, "split"),
+    (1000, 3333, 100, 224, "one"),
+    (2001, 6200, 1000, 224, "many"),
+    (4001, 6200, 700, 224, "many"),
+    (201, 30200, 4100, 224, "groups"),
+]
+
+
+@pytest.mark.parametrize("R,N,K,nt,kind", SCHEDULES)
+def test_linear_schedules_against_fp64(R, N, K, nt, kind):
+    """Every tile width in every way it is run, with ragged last tiles of rows and of weights: sampled rows and
+    columns (the first and last of each tile border among them) against 64 bits, the others written."""
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        s = schedule(R, N, K)
+        assert s["nt"] == nt and kind == ("split" if s["splits"] > 1 else "groups" if s["group"] else
+                                          "one" if s["per_cta"] == 1 else "many")
+        assert kind != "many" or s["per_cta"] >= 3
+    g = torch.Generator(DEV).manual_seed(R + N)
+    x = torch.randn(R, K, device=DEV, generator=g).bfloat16()
+    w4, _ = make_copy((torch.randn(N, K, device=DEV, generator=g) * 0.02).bfloat16())
+    y = torch.full((R, N), 1e30, dtype=torch.bfloat16, device=DEV)
+    m.mtp_head_linear_fp4(x, *w4, y, m.linear_fp4_workspace(R, N, K, DEV))
+    rows = {r for t in range(0, R, nt) for r in (t, t + 1, t + nt // 2, t + 127, t + 128, t + nt - 1)} | {R - 1}
+    cols = {c for c in range(0, N, max(1, N // 300))} | {c for t in range(0, N, 128 * max(1, N // 12800)) for c in (t, t + 127)}
+    cols |= set(range(max(0, N - 140), N))
+    rows, cols = (torch.tensor(sorted(i for i in v if i < n), device=DEV) for v, n in ((rows, R), (cols, N)))
+    check_linear(x[rows].contiguous(), tuple(t[cols].contiguous() for t in w4), y[rows][:, cols])
+    assert not bool((y == 1e30).any())
