@@ -766,13 +766,8 @@ __global__ void __launch_bounds__(kT, 2) sample_kernel(const SampleArgs a, int n
       __syncthreads();
     };
 
-    // Of n threads, n ln(n / (n - k)) entries reach the k-th largest maximum on average: at most k + 2/3 k^2 / n where
-    // that is near the list's length (k below n / 2.6; with fewer threads the list is long enough for any k up to n / 2).
-    // The rest of the list is for the spread and the bin's width. (A list that does not fit costs
-    // its row the passes made for it: with k = 1024 and no such rule 80 rows took 236 us and one row 44.7, by the
-    // histogram at once 206 and 37.3; at k = 700 with a list 57, without 203.)
-    const int64_t n_threads = static_cast<int64_t>(nc) * kT;
-    if (use_k && 2 * k <= n_threads && k <= kGather && k * (3 * n_threads + 2 * k) <= 3 * (kGather - 44) * n_threads) {
+    // (list_k is not above nc kT / 2; asked of k alone, the code around came out 0.4 us slower for one row)
+    if (use_k && 2 * k <= static_cast<int64_t>(nc) * kT && k <= a.list_k) {
       // ---- the whole row on one sorted list: the bins of the threads' maxima first
       if (live(most)) atomicAdd(&loc.n[bin1(most)], 1u);
       share_bins(false);
@@ -1305,6 +1300,18 @@ int sample_cluster(int64_t rows, int64_t V, bool top_k, int sm_count) {
   return nc;
 }
 
+// The largest top_k that is finished on one sorted list. Of a cluster's n threads, n ln(n / (n - k)) entries reach the
+// k-th largest maximum on average: at most k + 2/3 k^2 / n where that is near the list's length (k below n / 2.6; with
+// fewer threads the list is long enough for any k up to n / 2). The rest of the list is for the spread and the bin's
+// width. (A list that does not fit costs its row the passes made for it: with k = 1024 and no such rule 80 rows took
+// 236 us and one row 44.7, by the histogram at once 206 and 37.3; at k = 700 with a list 57, without 203.)
+int list_limit(int nc) {
+  const int64_t n = static_cast<int64_t>(nc) * kT;
+  int64_t k = n / 2 < kGather ? n / 2 : kGather;
+  while (k * (3 * n + 2 * k) > 3 * (kGather - 44) * n) --k;
+  return static_cast<int>(k);
+}
+
 // CTAs per sequence of the acceptance: one on each SM. 16 sequences at V = 154880 take 17.7 us with 16 CTAs each
 // (two waves), 14.8 with 8, 14.4 with 4; 80 at V = 32000 take 12.0 with one CTA and 14.5 with two.
 int verify_cluster(int64_t rows, int64_t V, int sm_count) {
@@ -1321,6 +1328,7 @@ cudaError_t launch_sample(const SampleArgs& in, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   SampleArgs a = in;
   int nc = sample_cluster(a.R, a.V, a.top_k != nullptr, di.sm_count);
+  a.list_k = list_limit(nc);
   int64_t slice = slice_of(a.V, nc);
   // A slice is kept in shared memory where that leaves room for as many CTAs per SM as there are to run (two hide
   // each other's loads: 80 rows with top_k and top_p, out of HBM, 66 us, and 74 with one and its slice held).

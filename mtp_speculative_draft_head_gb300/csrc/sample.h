@@ -20,6 +20,7 @@ struct SampleArgs {
   int64_t ld;
   int R, V;
   bool bf16;
+  int list_k;                // set by launch_sample
 };
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t stream);
 
