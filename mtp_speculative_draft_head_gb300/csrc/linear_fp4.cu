@@ -11,7 +11,7 @@
 // The weights are the MMA's M operand (128 rows a tile) and the activation rows its N operand (16 to
 // 224 a tile): one row of activations costs an eighth of a 128-row tile instead of filling one, so
 // the same kernel serves a draft step's few sequences, bound by the read of the weights, and a
-// prompt's thousands of rows, bound by the tensor cores. Codes arrive by 2-D TMA (256 codes = 128
+// prompt's thousands of rows, bound by its operands' way into the SMs. Codes arrive by 2-D TMA (256 codes = 128
 // bytes a row and stage, 128-byte swizzle). The weights' scales are rows of 16 bytes a stage in the
 // copy's plain layout; one warp loads them and stores the four words of a row into the four
 // 32 x 16-byte blocks that tcgen05.cp spreads over tensor memory (the scales of rows r, r + 32,
@@ -25,8 +25,9 @@
 //
 // Measured, 12288 -> 6144, with the rows' quantisation: 16 rows 18.0 us with the weights in L2, 20.0 out of HBM (42.5
 // MB, 6.4 us at the copy rate: latencies of a short kernel, the quantiser before it and the cluster's join are the
-// rest); 4096 rows 149 us, 26 of them the quantiser's. There the operands' way into the SMs bounds it: each SM takes
-// 51 KB a stage, and the four stages that shared memory holds are all in flight.
+// rest); 4096 rows 141 us, 26 of them the quantiser's. There the operands' way into the SMs bounds it: 745 cycles for a
+// stage's 51 KB (69 bytes a cycle and SM, the four stages that shared memory holds all in flight); its MMAs take 318
+// at the nominal rate, and their pipe counts as active for 58 % of the time, 430.
 //
 // Warp roles: 0 weight codes, 1 tensor-memory allocation and MMA issue, 2 weight scales, 3
 // activation codes and scales, 4..7 epilogue (warp w reads

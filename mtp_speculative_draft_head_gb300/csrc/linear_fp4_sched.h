@@ -47,9 +47,9 @@ inline LinearSched make_sched(int R, int N, int kp, int sm_count) {
       c.splits = splits;
     }
   }
-  // Weights beyond half of L2 are passed over once for kGroup activation tiles (154880 x 6144, 256 rows: 137 us, with
-  // a pass for each tile 183); shorter ones stay there while the activations go by (the groups' divisions cost 2 us
-  // of 90 at 2048 rows of 6144 -> 12288).
+  // Weights beyond half of L2 are passed over once for kGroup activation tiles (154880 x 6144, 256 rows: 139 us, with
+  // a pass for each tile 180; 2048 rows 944 and 1033); shorter ones stay there while the activations go by (2048 rows
+  // of 6144 -> 12288: 77 us, in groups 108; 4096 rows of 12288 -> 6144: 141 and 147).
   c.group = c.splits == 1 && c.nt >= 128 && c.tiles >= sm_count && static_cast<int64_t>(N) * kp * 9 / 16 > (64 << 20);
   return c;
 }

@@ -30,10 +30,10 @@
 // shared memory. A slice is kept in shared memory where it fits beside the histograms, and is read
 // again, from L2 mostly, where it does not (many rows).
 //
-// Measured at V = 154880: one row with top_k and top_p 12.0 us, 16 BF16 rows with top_p 51 us (the distribution
-// stored), 80 rows with both 50 us; bound by latency: exchanges of the cluster (1 to 1.5 us each), and with top_p
-// alone the histogram (8 us of a row's 23: two atomics or one per entry, 1 to 1.5 cycles a lane). 16 sequences of
-// the acceptance 14.7 us.
+// Measured at V = 154880: one row with top_k and top_p 12.6 to 16.6 us (as long as its list makes it), 16 BF16 rows
+// with top_p 50 to 55 us (the distribution stored), 80 rows with both 49 us; bound by latency: exchanges of the cluster
+// (1 to 1.5 us each), and with top_p alone the histogram (8 us of a row's 23: two atomics or one per entry, 1 to 1.5
+// cycles a lane). A row of 2,000,000 with top_p 177 us, 35 of them its first sum. 16 sequences of the acceptance 14.6 us.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
