@@ -23,7 +23,8 @@
 // Masses are 64-bit fixed-point numbers (2^62 / 2^ceil(log2 V) for a weight of one), so sums do not
 // depend on the order of the atomics or of the threads: the same inputs give the same token
 // whatever the cluster size. Each is off by half a unit at most, all together by V^2 2^-62 of a whole of at
-// least one; beyond 2^20 tokens, where that passes 2^-22, a first sum of the row tells how much room it takes. Weights are formed in fp32 from an exponent kept as a double-float:
+// least one; beyond 2^20 tokens, where that passes 2^-22, a first sum of the row tells how much room it takes
+// (a filter keeps the n largest weights of such a row; their n half units stay below V 2^-61 of their own sum). Weights are formed in fp32 from an exponent kept as a double-float:
 // relative error ~2^-23, against the 2^-24 of the given random numbers.
 //
 // A cluster of CTAs shares a row; maxima, histograms and masses are combined through distributed

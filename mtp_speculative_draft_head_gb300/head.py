@@ -58,7 +58,8 @@ class MtpDraftHead:
     def quantize_fp4(self) -> int:
         """Build the FP4 copies of lm_head and eh_proj, (q, block_scale, row_scale) each; returns the
         device status (0, or MTP_ERR_NONFINITE when a weight is NaN/Inf -- both are then dropped).
-        eh_proj gets a copy when H is a multiple of 8 (the input stage then runs over it)."""
+        eh_proj gets a copy when H is a multiple of 8 (the input stage then runs over it, for up to max_batch rows;
+        mtp_head_context_rows_fp4 takes a prompt's)."""
         st = torch.zeros(1, dtype=torch.int32, device=self.device)
         lm = _lib.fp4_empty(self.V, self.H, self.device)
         _lib.mtp_head_quantize_fp4(self.lm_head, *lm, st)
