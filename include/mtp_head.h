@@ -504,6 +504,130 @@ int mtp_head_verify(const float* target_probs, const float* draft_probs,
                     int V, void* stream);
 
 /* ------------------------------------------------------------------------------------------
+ * The attention half of a draft layer. The layer between the two stages is the identity in this
+ * library ("glm5next_mtp_head.rs", `forward_one`: the block call); the calls below are what its
+ * attention half is made of, together with mtp_head_linear_fp4 for its projections: the residual norm,
+ * a paged cache of keys and values in four bits, attention over it for a step's rows, and attention
+ * over whole prompts. In all of them an output or a workspace on an input that is still read, or on
+ * another output, is MTP_ERR_ARG, but for what is stated. They need no wait limit: none of their waits
+ * is for another kernel, and mtp_head_attention_prompt's, for its own copies and products, take 2 s.
+ *
+ * Residual norm. For each of R rows of H columns:
+ *   total = bf16( x + delta )              the real sum rounded once; x itself when delta is NULL
+ *   y     = bf16( total * w / sqrt(mean(total^2) + eps) )                     (rms_norm_vanilla)
+ *   q_scale = fp32( max |y| / 448 ),  q = e4m3_rne_satfinite( fp32( y / q_scale ) )
+ * the scale of the whole row (group 0: q_scale [R]) or of each 128 columns of it (group 128: q_scale
+ * [R, ceil(H / 128)]). For group 0 that is mtp_head_quantize_fp8 of y.
+ *   x, delta [R, H] BF16 (delta may be NULL), w [H] BF16
+ *   total, y [R, H] BF16, q [R, H] uint8: each optional, one at least; total and y may take the place
+ *            of x or of delta
+ *   status   required with q: MTP_ERR_NONFINITE when the columns of a scale hold a NaN or Inf in y
+ *            (their codes and the scale are zeros); y itself follows the formula
+ *   1 <= R <= 65536, 1 <= H <= 65536; any H (multiples of 8 are fastest)
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_norm_residual(const uint16_t* x, const uint16_t* delta, const uint16_t* w,
+                           uint16_t* total, uint16_t* y, uint8_t* q, float* q_scale,
+                           int32_t* status, int R, int H, int group, float eps, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Paged FP4 cache of keys and values. A page holds `page` tokens (a power of two, 16 to 256) of every
+ * head, keys first:
+ *   q            [pages, 2, heads, page, D/2]   uint8   E2M1 codes, column 2i in the low half of byte i
+ *   block_scale  [pages, 2, heads, page, D/16]  uint8   E4M3 scale of each 16 columns
+ *   row_scale    [pages, 2, heads, page]        fp32
+ * Each row (a token's key or value of one head) is a row of D columns in the format, and with the
+ * roundings, of mtp_head_quantize_fp4 (without its padding). D is 64 or 128 (others
+ * MTP_ERR_NOT_IMPLEMENTED). All three arrays are 16-byte aligned.
+ *
+ * Which rows: T packed rows, sequence b's at row_start[b] .. row_start[b + 1) of them (row_start [B + 1]
+ * int32, ascending), the first at position[b] of the sequence; position p is token p % page of page
+ * block_table[b, p / page] (block_table [B, max_pages] int32). row_start, position and block_table are
+ * device arrays. Rows outside every sequence are neither read into the cache nor written from it. A
+ * position outside 0 .. max_pages * page, or a page outside 0 .. pages: MTP_ERR_ARG in status
+ * (optional), and the row is left out (write) or zeros (read).
+ *
+ * write   k, v [T, heads, D] BF16 -> the cache; a row's heads are dense, rows lie ld_k (ld_v) elements
+ *         apart (a multiple of 8, at least heads * D). A row of a head that holds a NaN or Inf becomes
+ *         zeros (MTP_ERR_NONFINITE). Two rows of one call for the same place in the cache are the
+ *         caller's error (the place then holds parts of either).
+ * read    the cache -> k, v [T, heads, D] BF16: bf16( fp32( q * block_scale * row_scale ) ). k and v may
+ *         lie side by side in the same rows.
+ * 1 <= T <= 2^22, 1 <= B <= 65536, 1 <= heads <= 1024, max_pages * page <= 2^30.
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_cache_write_fp4(const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v,
+                             const int32_t* row_start, const int32_t* position,
+                             const int32_t* block_table, uint8_t* q, uint8_t* block_scale,
+                             float* row_scale, int32_t* status, int T, int B, int heads, int D,
+                             int pages, int page, int max_pages, void* stream);
+
+int mtp_head_cache_read_fp4(const uint8_t* q, const uint8_t* block_scale, const float* row_scale,
+                            const int32_t* row_start, const int32_t* position,
+                            const int32_t* block_table, uint16_t* k, int64_t ld_k, uint16_t* v,
+                            int64_t ld_v, int32_t* status, int T, int B, int heads, int D, int pages,
+                            int page, int max_pages, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Attention of a step's rows over the cache: one row of each sequence (a draft step), or several (the
+ * verification of drafts).
+ *
+ *   query    [B, Q, q_heads, D] BF16   the (b, i) rows ld_q elements apart (a multiple of 8)
+ *   length   [B] int32   tokens of the sequence in the cache, the query rows' own among them
+ *   rows     [B] int32   optional: query rows of each sequence, 0 .. Q (NULL: Q each)
+ *   out      [B, Q, q_heads, D] BF16   the (b, i) rows ld_out elements apart
+ *   lse      [B, Q, q_heads] fp32      optional: ln sum_j exp(scale q . k_j)
+ *   status   [1] int32   optional; MTP_ERR_ARG: a length outside 0 .. max_pages * page or rows outside
+ *                        0 .. Q (that sequence's Q rows are zeros, their lse -Inf), or a page outside
+ *                        0 .. pages (its tokens count as rows of zeros)
+ *   cache, block_table, pages, page, max_pages   as above; q_heads a multiple of kv_heads (at most 1024
+ *                        each): query head h reads key head h / (q_heads / kv_heads)
+ *
+ * With n = rows[b], row i < n sees the first length[b] - n + i + 1 tokens:
+ *   out = sum_j p_j v_j,  p = softmax_j( scale q . k_j ),  scale finite and > 0
+ * A row that sees no token gives zeros and lse -Inf. Rows i >= n are left as they were. What the pages hold
+ * behind a sequence's tokens does not matter. Products take 16-bit operands (keys, values and query rows
+ * exactly, weights in f16), sums are fp32; results do not vary from run to run.
+ *   workspace   at least mtp_head_attention_fp4_workspace_bytes(B, Q, q_heads, kv_heads, D, max_pages *
+ *               page) bytes, zero-filled once before its first use (the kernel leaves its counters zero); all
+ *               of workspace_bytes may be written. One workspace serves every call of no larger B, Q,
+ *               head counts, D and max_pages * page. Two calls that may run at the same time need
+ *               different ones.
+ *   1 <= Q <= 1024, 1 <= B <= 65536, B * kv_heads * ceil(Q (q_heads / kv_heads) / 16) <= 2^23
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_attention_fp4(const uint16_t* query, int64_t ld_q, const uint8_t* q,
+                           const uint8_t* block_scale, const float* row_scale,
+                           const int32_t* block_table, const int32_t* length, const int32_t* rows,
+                           uint16_t* out, int64_t ld_out, float* lse, int32_t* status,
+                           void* workspace, size_t workspace_bytes, int B, int Q, int q_heads,
+                           int kv_heads, int D, int pages, int page, int max_pages, float scale,
+                           void* stream);
+
+/* 0 for invalid shapes */
+size_t mtp_head_attention_fp4_workspace_bytes(int B, int Q, int q_heads, int kv_heads, int D,
+                                              int64_t max_len);
+
+/* ------------------------------------------------------------------------------------------
+ * Causal attention over packed prompts (the context rows of mtp_head_context_rows, as a layer sees
+ * them): T rows, sequence b's at row_start[b] .. row_start[b + 1) (device array [B + 1], ascending);
+ * row i of a sequence sees its rows 0 .. i.
+ *
+ *   q [T, q_heads, D], k, v [T, kv_heads, D] BF16   a row's heads are dense, rows ld_q, ld_k, ld_v elements
+ *                        apart (multiples of 8: q, k and v may be columns of one projection's rows)
+ *   out [T, q_heads, D] BF16   rows ld_out elements apart
+ *   lse [T, q_heads] fp32      optional: ln sum_j exp(scale q . k_j)
+ *   status   [1] int32   optional; MTP_ERR_ARG: a sequence that does not lie in 0 .. T or starts before the
+ *                        one in front of it ends (rows of such a call are undefined, never out of
+ *                        bounds); MTP_ERR_TIMEOUT: a wait ran out
+ * Rows outside every sequence are left as they were, and what they hold does not matter. Weights are
+ * BF16, sums fp32; results do not vary from run to run.
+ *   1 <= T <= 2^22, 1 <= B <= 65536, q_heads a multiple of kv_heads (at most 1024 each), D 64 or 128 (others
+ *   MTP_ERR_NOT_IMPLEMENTED), scale finite and > 0. No workspace.
+ * ---------------------------------------------------------------------------------------- */
+int mtp_head_attention_prompt(const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k,
+                              const uint16_t* v, int64_t ld_v, const int32_t* row_start,
+                              uint16_t* out, int64_t ld_out, float* lse, int32_t* status, int T,
+                              int B, int q_heads, int kv_heads, int D, float scale, void* stream);
+
+/* ------------------------------------------------------------------------------------------
  * Give-up time of the kernels' stage waits (no counterpart on the source pages, which have no
  * device-side waits: this library's kernels wait on shared-memory barriers for their weight
  * copies and for each other's stages, and every such wait is bounded so that a stalled copy can

@@ -5,7 +5,9 @@ the fused input stage (embedding gather, enorm/hnorm RMSNorm, concat, eh_proj GE
 output stage (shared_head.norm, lm_head vocabulary sweep in BF16 or FP8 E4M3, argmax) and the
 FP8 quantiser, and the output stage over one vocabulary shard with the exact pick between
 shards; FP4 (E2M1, two-level scales) copies of lm_head and eh_proj with the stages over them, drafts
-drawn by sampling, and their acceptance against the target's distributions. ``_lib`` binds those entry points by name with ctypes; ``MtpDraftHead`` and
+drawn by sampling, and their acceptance against the target's distributions; and what the attention half
+of a layer between the stages is made of: a residual norm, a paged FP4 cache, attention over it and over prompts.
+``_lib`` binds those entry points by name with ctypes; ``MtpDraftHead``, ``DraftLayer`` and
 ``VocabShard`` own buffers around them. PyTorch provides device memory, streams and (between
 the ranks of a sharded head) the one MAX all-reduce of the pick keys.
 """
@@ -23,5 +25,8 @@ from ._lib import (  # noqa: F401
     mtp_head_context_fp4_workspace_bytes, mtp_head_context_rows_fp4, mtp_head_dequantize_fp4, mtp_head_fp4_padded,
     mtp_head_fp4_workspace_bytes, mtp_head_linear_fp4, mtp_head_linear_fp4_workspace_bytes,
     mtp_head_logits_argmax_fp4, mtp_head_quantize_fp4, mtp_head_sample, mtp_head_verify,
+    attention_fp4_workspace, cache_empty, mtp_head_attention_fp4, mtp_head_attention_fp4_workspace_bytes,
+    mtp_head_attention_prompt, mtp_head_cache_read_fp4, mtp_head_cache_write_fp4, mtp_head_norm_residual,
 )
 from .head import MtpDraftHead, VocabShard, exchange_picks, shard_geometry  # noqa: F401
+from .layer import DraftLayer, LayerCache  # noqa: F401

@@ -33,7 +33,7 @@ ERR_NOT_IMPLEMENTED = -8
 ERR_TIMEOUT = -9
 
 # name -> (restype, argtypes); mirrors include/mtp_head.h
-P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+P, I, F, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
 SIGNATURES = {
     "mtp_head_input_batched": (I, [P, P, P, P, P, P, P, P, I, I, I, F, P]),
     "mtp_head_input": (I, [P, P, P, P, P, P, P, P, I, I, F, P]),
@@ -65,6 +65,12 @@ SIGNATURES = {
     "mtp_head_context_fp4_workspace_bytes": (Z, [I, I]),
     "mtp_head_sample": (I, [P, I, ctypes.c_int64, P, P, P, P, P, P, P, P, P, I, I, P]),
     "mtp_head_verify": (I, [P, P, P, P, P, P, P, P, P, I, I, I, P]),
+    "mtp_head_norm_residual": (I, [P, P, P, P, P, P, P, P, I, I, I, F, P]),
+    "mtp_head_cache_write_fp4": (I, [P, L, P, L, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]),
+    "mtp_head_cache_read_fp4": (I, [P, P, P, P, P, P, P, L, P, L, P, I, I, I, I, I, I, I, P]),
+    "mtp_head_attention_fp4": (I, [P, L, P, P, P, P, P, P, P, L, P, P, P, Z, I, I, I, I, I, I, I, I, F, P]),
+    "mtp_head_attention_fp4_workspace_bytes": (Z, [I, I, I, I, I, L]),
+    "mtp_head_attention_prompt": (I, [P, L, P, L, P, L, P, P, L, P, P, I, I, I, I, I, F, P]),
 }
 
 _lib = None
@@ -536,3 +542,141 @@ def mtp_head_verify(target_probs, draft_probs, draft_tokens, u, tokens, accepted
           _t(draft_len, "draft_len", _I32, (B,), dev, True), _t(u, "u", _F32, (B, D1), dev),
           _t(tokens, "tokens", _I32, (B, D1), dev), _t(accepted, "accepted", _I32, (B,), dev),
           _t(prob, "prob", _F32, (B,), dev, True), _t(status, "status", _I32, (1,), dev, True), B, D, V)
+
+
+# ------------------------------------------------------------------ the attention half of a draft layer
+def mtp_head_norm_residual(x, w, delta=None, total=None, y=None, q=None, q_scale=None, status=None, group: int = 0,
+                           eps: float = 1e-6, stream=None) -> None:
+    """total [R, H] = x + delta, y [R, H] = its norm with weight w [H], q [R, H] the E4M3 codes of y with
+    q_scale [R] (group 0) or [R, ceil(H / 128)] (group 128). total, y and q are outputs, each optional."""
+    (R, H), dev = _first(x, "x", 2)
+    n = (R, H)
+    scales = (R,) if group == 0 else (R, -(-H // group)) if group > 0 else None
+    _call(dev, stream, "mtp_head_norm_residual", _t(x, "x", _BF16, n, dev), _t(delta, "delta", _BF16, n, dev, True),
+          _t(w, "w", _BF16, (H,), dev), _t(total, "total", _BF16, n, dev, True), _t(y, "y", _BF16, n, dev, True),
+          _t(q, "q", _U8, n, dev, True), _t(q_scale, "q_scale", _F32, scales, dev, True),
+          _t(status, "status", _I32, (1,), dev, True), R, H, group, eps)
+
+
+def cache_empty(pages: int, page: int, heads: int, head_dim: int, device=None):
+    """Zero-filled (q, block_scale, row_scale) of a paged FP4 cache."""
+    if pages < 1 or page < 16 or heads < 1 or head_dim < 16 or head_dim % 16:
+        raise MTPError(ERR_SHAPE, "cache_empty")
+    dev = device or "cuda"
+    return (torch.zeros((pages, 2, heads, page, head_dim // 2), dtype=torch.uint8, device=dev),
+            torch.zeros((pages, 2, heads, page, head_dim // 16), dtype=torch.uint8, device=dev),
+            torch.zeros((pages, 2, heads, page), dtype=torch.float32, device=dev))
+
+
+def _cache(q, block_scale, row_scale):
+    """The addresses of a cache, its sizes (pages, heads, page, head_dim) and its device."""
+    (pages, two, heads, page, half), dev = _first(q, "q", 5)
+    if two != 2:
+        raise ValueError("q must have shape (pages, 2, heads, page, head_dim / 2)")
+    at = (_t(q, "q", _U8, (pages, 2, heads, page, half), dev),
+          _t(block_scale, "block_scale", _U8, (pages, 2, heads, page, half // 8), dev),
+          _t(row_scale, "row_scale", _F32, (pages, 2, heads, page), dev))
+    return at, pages, heads, page, 2 * half, dev
+
+
+def _rows_of_heads(t, name, shape, dev):
+    """The address and row stride of a BF16 tensor [..., heads, head_dim] whose rows may lie apart: its
+    heads dense, the rows at equal distances."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    heads, dim = shape[-2:]
+    st = t.stride()
+    dense = (dim == 1 or st[-1] == 1) and (heads == 1 or st[-2] == dim)
+    ld = heads * dim
+    if len(shape) == 3:
+        ld = st[0] if shape[0] > 1 else ld
+    else:
+        if shape[1] > 1:
+            ld = st[1]
+            dense = dense and (shape[0] == 1 or st[0] == shape[1] * ld)
+        elif shape[0] > 1:
+            ld = st[0]
+    if not dense or ld < heads * dim:
+        raise ValueError(f"{name}: a row's heads must be dense, and its rows at equal distances")
+    return t.data_ptr(), ld
+
+
+def mtp_head_cache_write_fp4(k, v, row_start, position, block_table, q, block_scale, row_scale, status=None,
+                             stream=None) -> None:
+    """Rows k, v [T, heads, head_dim] (BF16, the rows may lie apart) into the cache: sequence b's rows
+    row_start[b] .. row_start[b + 1] at its positions from position[b] on."""
+    at, pages, heads, page, D, dev = _cache(q, block_scale, row_scale)
+    (T, _, _), _ = _first(k, "k", 3)
+    (B, max_pages), _ = _first(block_table, "block_table", 2)
+    shape = (T, heads, D)
+    _call(dev, stream, "mtp_head_cache_write_fp4", *_rows_of_heads(k, "k", shape, dev), *_rows_of_heads(v, "v", shape, dev),
+          _t(row_start, "row_start", _I32, (B + 1,), dev), _t(position, "position", _I32, (B,), dev),
+          _t(block_table, "block_table", _I32, (B, max_pages), dev), *at, _t(status, "status", _I32, (1,), dev, True),
+          T, B, heads, D, pages, page, max_pages)
+
+
+def mtp_head_cache_read_fp4(q, block_scale, row_scale, row_start, position, block_table, k, v, status=None,
+                            stream=None) -> None:
+    """The rows that a write of the same arguments filled, back as BF16 into k, v [T, heads, head_dim]."""
+    at, pages, heads, page, D, dev = _cache(q, block_scale, row_scale)
+    (T, _, _), _ = _first(k, "k", 3)
+    (B, max_pages), _ = _first(block_table, "block_table", 2)
+    shape = (T, heads, D)
+    _call(dev, stream, "mtp_head_cache_read_fp4", *at, _t(row_start, "row_start", _I32, (B + 1,), dev),
+          _t(position, "position", _I32, (B,), dev), _t(block_table, "block_table", _I32, (B, max_pages), dev),
+          *_rows_of_heads(k, "k", shape, dev), *_rows_of_heads(v, "v", shape, dev),
+          _t(status, "status", _I32, (1,), dev, True), T, B, heads, D, pages, page, max_pages)
+
+
+def mtp_head_attention_fp4_workspace_bytes(B: int, Q: int, q_heads: int, kv_heads: int, head_dim: int,
+                                           max_len: int) -> int:
+    return int(load().mtp_head_attention_fp4_workspace_bytes(B, Q, q_heads, kv_heads, head_dim, max_len))
+
+
+def attention_fp4_workspace(B: int, Q: int, q_heads: int, kv_heads: int, head_dim: int, max_len: int,
+                            device=None) -> torch.Tensor:
+    """A zero-filled workspace for mtp_head_attention_fp4 (max_len: max_pages * page), reusable across calls
+    of these sizes."""
+    n = mtp_head_attention_fp4_workspace_bytes(B, Q, q_heads, kv_heads, head_dim, max_len)
+    if n == 0:
+        raise MTPError(ERR_SHAPE, "attention_fp4_workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def mtp_head_attention_fp4(query, q, block_scale, row_scale, block_table, length, out, ws, rows=None, lse=None,
+                           scale: float | None = None, status=None, stream=None) -> None:
+    """out [B, Q, q_heads, head_dim] = attention of query (the same shape, BF16, rows may lie apart) over each
+    sequence's pages; length [B] counts the query rows' own tokens, rows [B] (optional) how many of the Q rows
+    a sequence has; lse [B, Q, q_heads] optional. scale: 1 / sqrt(head_dim) unless given."""
+    at, pages, heads, page, D, dev = _cache(q, block_scale, row_scale)
+    (B, Q, hq, _), _ = _first(query, "query", 4)
+    (_, max_pages), _ = _first(block_table, "block_table", 2)
+    shape = (B, Q, hq, D)
+    _call(dev, stream, "mtp_head_attention_fp4", *_rows_of_heads(query, "query", shape, dev), *at,
+          _t(block_table, "block_table", _I32, (B, max_pages), dev), _t(length, "length", _I32, (B,), dev),
+          _t(rows, "rows", _I32, (B,), dev, True), *_rows_of_heads(out, "out", shape, dev),
+          _t(lse, "lse", _F32, (B, Q, hq), dev, True), _t(status, "status", _I32, (1,), dev, True), *_ws(ws, dev),
+          B, Q, hq, heads, D, pages, page, max_pages, D ** -0.5 if scale is None else scale)
+
+
+def mtp_head_attention_prompt(q, k, v, row_start, out, lse=None, scale: float | None = None, status=None,
+                              stream=None) -> None:
+    """out [T, q_heads, head_dim] = causal attention of q (the same shape) over k, v [T, kv_heads, head_dim] within
+    each sequence row_start[b] .. row_start[b + 1] (BF16; rows may lie apart); lse [T, q_heads] optional. scale:
+    1 / sqrt(head_dim) unless given."""
+    (T, hq, D), dev = _first(q, "q", 3)
+    (_, heads, _), _ = _first(k, "k", 3)
+    (B1,), _ = _first(row_start, "row_start", 1)
+    _call(dev, stream, "mtp_head_attention_prompt", *_rows_of_heads(q, "q", (T, hq, D), dev),
+          *_rows_of_heads(k, "k", (T, heads, D), dev), *_rows_of_heads(v, "v", (T, heads, D), dev),
+          _t(row_start, "row_start", _I32, (B1,), dev), *_rows_of_heads(out, "out", (T, hq, D), dev),
+          _t(lse, "lse", _F32, (T, hq), dev, True), _t(status, "status", _I32, (1,), dev, True), T, B1 - 1, hq, heads, D,
+          D ** -0.5 if scale is None else scale)

@@ -1,0 +1,379 @@
+// The residual's addition, the norm of the sum, and an E4M3 copy of the normalised rows:
+//   s = bf16( x + delta )                                  (the real sum rounded once; s = x without a delta)
+//   y = bf16( s w / sqrt(mean s^2 + eps) )                 rms_norm_vanilla, as everywhere in this library
+//   scale = fp32( max |y| / 448 ),  q = e4m3( fp32( y / scale ) )    of each row, or of 128 columns of it
+//
+// One read of x and delta: a row stays in the registers of the threads that share it, between the
+// sum of its squares and the results. Sums of squares are double-floats of exact squares, 1/rms is
+// formed in fp64, and y is rounded once from a double-float: y is the same whatever the number of
+// threads. A row's squares leave the fp32 range beyond 2^64 or below 2^-75; such a row is taken
+// once more at 2^-80 or 2^80 of its size, which the norm divides out again.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "codes.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "layer.h"
+#include "tc.cuh"
+
+namespace mtp {
+
+namespace {
+
+// Eight columns from c0 of a row that starts at flat element `at` of a 16-byte aligned array; at + c0 is a
+// multiple of 8. Columns outside [0, H) are zeros and not read.
+__device__ __forceinline__ uint4 load8(const uint16_t* base, int64_t at, int c0, int H) {
+  const uint16_t* p = base + at + c0;
+  if (c0 >= 0 && c0 + 8 <= H) return __ldcs(reinterpret_cast<const uint4*>(p));
+  uint32_t u[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c0 + i >= 0 && c0 + i < H) u[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store8(uint16_t* base, int64_t at, int c0, int H, const uint32_t (&u)[4]) {
+  uint16_t* p = base + at + c0;
+  if (c0 >= 0 && c0 + 8 <= H) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c0 + i >= 0 && c0 + i < H) p[i] = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+}
+
+// bf16( a + b ) of two BF16 values: the fp32 sum decides unless it lies on a BF16 midpoint.
+__device__ __forceinline__ uint32_t add_pair(uint32_t a, uint32_t b) {
+  const float l = __fadd_rn(bf16_lo(a), bf16_lo(b)), h = __fadd_rn(bf16_hi(a), bf16_hi(b));
+  uint32_t o;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(h), "f"(l));
+  float s, e;
+  if ((__float_as_uint(l) & 0xFFFFu) == 0x8000u) {
+    two_sum(bf16_lo(a), bf16_lo(b), s, e);
+    o = (o & 0xFFFF0000u) | bf16_rne_df(s, e);
+  }
+  if ((__float_as_uint(h) & 0xFFFFu) == 0x8000u) {
+    two_sum(bf16_hi(a), bf16_hi(b), s, e);
+    o = (o & 0xFFFFu) | (static_cast<uint32_t>(bf16_rne_df(s, e)) << 16);
+  }
+  return o;
+}
+// A BF16 pair times a power of two (exact, but for results below the normal range).
+__device__ __forceinline__ uint32_t scale_pair(uint32_t a, float f) {
+  uint32_t o;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(__fmul_rn(bf16_hi(a), f)), "f"(__fmul_rn(bf16_lo(a), f)));
+  return o;
+}
+
+// Eight E4M3 codes of four BF16 pairs.
+__device__ __forceinline__ uint2 codes_e4m3(const uint32_t (&u)[4], float s) {
+  if (s == 0.0f) return make_uint2(0u, 0u);
+  uint32_t c[4];
+  if (s >= 1.17549435e-38f) {
+    const float r = __frcp_rn(s);
+    const float r_up = __fmul_rn(r, 1.0f + 0x1p-21f), r_dn = __fmul_rn(r, 1.0f - 0x1p-21f);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) c[t] = pair_codes(u[t], s, r_up, r_dn);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) c[t] = pair_codes_div(u[t], s);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Groups of a row that TPR threads hold in P pieces each, at most.
+constexpr int max_groups(int tpr, int p) { return tpr * p * 8 / kNormGroup + 2; }
+
+// TPR threads per row (a warp, or the whole CTA), P pieces of eight columns a thread. VEC: H is a
+// multiple of 8. Otherwise pieces follow the arrays' 16-byte boundaries: a row's first and last may
+// be partial, and w, q and the scales' groups are not aligned with them.
+template <int TPR, int P, bool VEC>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(const NormResidualArgs a) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  constexpr int kWarpsHere = kThreads / 32;
+  constexpr int kRows = kThreads / TPR;
+  constexpr int kMaxGroups = max_groups(TPR, P);
+  static_assert(TPR == 32 || kRows == 1, "a warp or a CTA per row");
+  __shared__ float red[2 * kWarpsHere + 2];
+  __shared__ uint32_t redm[kWarpsHere];
+  extern __shared__ uint32_t gmax[];  // not VEC, group > 0: [kRows][kMaxGroups]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = threadIdx.x % TPR;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
+  pdl_wait_prior_grid();
+  if (row >= a.R) return;  // (whole warps: only where no CTA barrier follows)
+  const int H = a.H;
+  const int64_t at = row * H;
+  const int off = VEC ? 0 : static_cast<int>(at & 7);
+  auto row_sync = [] {
+    if constexpr (TPR == 32)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+
+  // ---- s
+  uint32_t s[P][4];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c0 = 8 * (t + i * TPR) - off;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (c0 < H) v = load8(a.x, at, c0, H);
+    s[i][0] = v.x, s[i][1] = v.y, s[i][2] = v.z, s[i][3] = v.w;
+  }
+  if (a.delta != nullptr) {
+    uint4 d[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c0 = 8 * (t + i * TPR) - off;
+      d[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c0 < H) d[i] = load8(a.delta, at, c0, H);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      s[i][0] = add_pair(s[i][0], d[i].x);
+      s[i][1] = add_pair(s[i][1], d[i].y);
+      s[i][2] = add_pair(s[i][2], d[i].z);
+      s[i][3] = add_pair(s[i][3], d[i].w);
+    }
+  }
+  if (a.total != nullptr) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c0 = 8 * (t + i * TPR) - off;
+      if (c0 < H) store8(a.total, at, c0, H, s[i]);
+    }
+  }
+  if (a.y == nullptr && a.q == nullptr) return;
+
+  // ---- 1 / rms
+  auto sum_squares = [&]() -> DF {
+    DF2 acc{0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t f = bf16x2_to_f2(s[i][e]);
+        df2_add(acc, f2_mul(f, f));
+      }
+    DF v = df_add(df2_x(acc), df2_y(acc));
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v = df_add(v, shfl_xor_df(v, m));
+    if constexpr (TPR > 32) {
+      if (lane == 0) {
+        red[2 * warp] = v.hi;
+        red[2 * warp + 1] = v.lo;
+      }
+      __syncthreads();
+      v = DF{red[0], red[1]};
+      for (int i = 1; i < kWarpsHere; ++i) v = df_add(v, DF{red[2 * i], red[2 * i + 1]});
+    }
+    return v;
+  };
+  DF tot = sum_squares();
+  double factor2 = 1.0;  // what eps is multiplied by: the square of the row's factor
+  if (!(tot.hi >= 0x1p-100f && tot.hi < __int_as_float(0x7f800000))) {  // (the whole row alike)
+    const bool big = !(tot.hi < 0x1p-100f);
+    const float f = big ? 0x1p-80f : 0x1p80f;
+    factor2 = big ? 0x1p-160 : 0x1p160;
+    uint32_t nan = 0u, inf = 0u;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = s[i][e] & 0x7FFFu, hi = (s[i][e] >> 16) & 0x7FFFu;
+        nan |= (lo > 0x7F80u || hi > 0x7F80u) ? 1u : 0u;
+        inf |= (lo == 0x7F80u || hi == 0x7F80u) ? 1u : 0u;
+        s[i][e] = scale_pair(s[i][e], f);
+      }
+    if constexpr (TPR > 32) __syncthreads();  // red is read by all before it is written again
+    tot = sum_squares();
+    const uint32_t flags = __reduce_or_sync(0xffffffffu, nan | (inf << 1));
+    uint32_t all = flags;
+    if constexpr (TPR > 32) {
+      if (lane == 0) redm[warp] = flags;
+      __syncthreads();
+      for (int i = 0; i < kWarpsHere; ++i) all |= redm[i];
+      __syncthreads();
+    }
+    // an infinity makes the mean infinite (finite columns become 0), a NaN makes it NaN
+    if (all != 0u) tot = DF{__int_as_float((all & 1u) ? 0x7fc00000 : 0x7f800000), 0.0f};
+  }
+  float rh, rl;
+  {
+    double r = 0.0;
+    if (t == 0 || TPR == 32) {
+      // (one fp64 reciprocal root a row, not one a thread: rsqrt is within an ulp or two)
+      const double ms = (static_cast<double>(tot.hi) + static_cast<double>(tot.lo)) * a.inv_h;
+      r = rsqrt(ms + static_cast<double>(a.eps) * factor2);
+    }
+    rh = static_cast<float>(r);
+    rl = isinf(rh) ? 0.0f : static_cast<float>(r - static_cast<double>(rh));
+    if constexpr (TPR > 32) {
+      if (t == 0) {
+        red[2 * kWarpsHere] = rh;
+        red[2 * kWarpsHere + 1] = rl;
+      }
+      __syncthreads();
+      rh = red[2 * kWarpsHere];
+      rl = red[2 * kWarpsHere + 1];
+    }
+  }
+
+  // ---- y (in the place of s)
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int c0 = 8 * (t + i * TPR) - off;
+    if (c0 >= H) continue;
+    float wf[8];
+    if constexpr (VEC) {
+      const uint4 w4 = *reinterpret_cast<const uint4*>(a.w + c0);
+      const uint32_t wu[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wf[e] = (e & 1) ? bf16_hi(wu[e >> 1]) : bf16_lo(wu[e >> 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wf[e] = c0 + e >= 0 && c0 + e < H ? bf16_bits_to_f32(a.w[c0 + e]) : 0.0f;
+    }
+    const uint4 o = bf16x8_scaled_rne(s[i], wf, rh, rl);
+    s[i][0] = o.x, s[i][1] = o.y, s[i][2] = o.z, s[i][3] = o.w;
+    if constexpr (!VEC) {  // (a NaN factor leaves a NaN in the columns that are not the row's)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c0 + e < 0 || c0 + e >= H) s[i][e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+    if (a.y != nullptr) store8(a.y, at, c0, H, s[i]);
+  }
+  if (a.q == nullptr) return;
+
+  // ---- the 8-bit copy
+  auto scale_of = [&](uint32_t mx) {
+    if (mx >= 0x7F80u) {  // a NaN or Inf among the columns
+      store_status(a.status, MTP_ERR_NONFINITE);
+      return 0.0f;
+    }
+    return __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+  };
+  auto store_codes = [&](int c0, uint2 c) {
+    if constexpr (VEC) {
+      *reinterpret_cast<uint2*>(a.q + at + c0) = c;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c0 + e >= 0 && c0 + e < H) a.q[at + c0 + e] = static_cast<uint8_t>((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+    }
+  };
+  if (a.group == 0) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (8 * (t + i * TPR) - off < H) m = mag_max(m, make_uint4(s[i][0], s[i][1], s[i][2], s[i][3]));
+    }
+    uint32_t mx = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+    if constexpr (TPR > 32) {
+      if (lane == 0) redm[warp] = mx;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWarpsHere; ++i) mx = max(mx, redm[i]);
+    }
+    const float sc = mx >= 0x7F80u ? 0.0f : __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+    if (t == 0) a.q_scale[row] = scale_of(mx);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c0 = 8 * (t + i * TPR) - off;
+      if (c0 < H) store_codes(c0, codes_e4m3(s[i], sc));
+    }
+    return;
+  }
+  const int groups = (H + kNormGroup - 1) / kNormGroup;
+  float* scales = a.q_scale + row * groups;
+  if constexpr (VEC) {
+    // sixteen neighbouring lanes hold a group
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c0 = 8 * (t + i * TPR);
+      uint32_t m = 0u;
+      if (c0 < H) m = mag_max(0u, make_uint4(s[i][0], s[i][1], s[i][2], s[i][3]));
+      uint32_t mx = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+      for (int k = 8; k > 0; k >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+      const float sc = mx >= 0x7F80u ? 0.0f : __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+      if (c0 < H) {
+        if ((lane & 15) == 0) scales[c0 / kNormGroup] = scale_of(mx);
+        store_codes(c0, codes_e4m3(s[i], sc));
+      }
+    }
+  } else {
+    // a piece meets at most two groups; the groups' maxima in shared memory
+    uint32_t* gm = gmax + (threadIdx.x / TPR) * kMaxGroups;
+    for (int g = t; g < groups; g += TPR) gm[g] = 0u;
+    row_sync();
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c0 = 8 * (t + i * TPR) - off;
+      if (c0 >= H) continue;
+      const int g0 = c0 < 0 ? 0 : c0 / kNormGroup;
+      uint32_t m0 = 0u, m1 = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t v = (s[i][e >> 1] >> (16 * (e & 1))) & 0x7FFFu;
+        if (c0 + e < (g0 + 1) * kNormGroup)
+          m0 = max(m0, v);
+        else
+          m1 = max(m1, v);
+      }
+      atomicMax(&gm[g0], m0);
+      if (m1 != 0u) atomicMax(&gm[g0 + 1], m1);
+    }
+    row_sync();
+    for (int g = t; g < groups; g += TPR) scales[g] = scale_of(gm[g]);
+    auto at_group = [&](int g) {
+      const uint32_t mx = g < groups ? gm[g] : 0u;
+      return mx >= 0x7F80u ? 0.0f : __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+    };
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c0 = 8 * (t + i * TPR) - off;
+      if (c0 >= H) continue;
+      const int g0 = c0 < 0 ? 0 : c0 / kNormGroup;
+      uint2 c = codes_e4m3(s[i], at_group(g0));
+      const int n0 = (g0 + 1) * kNormGroup - c0;  // columns of the piece in its first group
+      if (n0 < 8) {
+        const uint2 d = codes_e4m3(s[i], at_group(g0 + 1));
+        const uint64_t keep = (1ull << (8 * n0)) - 1ull;
+        const uint64_t both = ((static_cast<uint64_t>(c.y) << 32 | c.x) & keep) | ((static_cast<uint64_t>(d.y) << 32 | d.x) & ~keep);
+        c = make_uint2(static_cast<uint32_t>(both), static_cast<uint32_t>(both >> 32));
+      }
+      store_codes(c0, c);
+    }
+  }
+}
+
+template <int TPR, int P>
+cudaError_t launch_form(const NormResidualArgs& a, cudaStream_t stream) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  const bool vec = a.H % 8 == 0;
+  const void* kern = vec ? reinterpret_cast<const void*>(norm_residual_kernel<TPR, P, true>)
+                                  : reinterpret_cast<const void*>(norm_residual_kernel<TPR, P, false>);
+  const int rows = kThreads / TPR;
+  const size_t smem = vec || a.group == 0 ? 0 : static_cast<size_t>(rows) * max_groups(TPR, P) * 4;
+  NormResidualArgs p = a;
+  void* args[] = {&p};
+  return launch_pdl(kern, dim3(static_cast<unsigned>((a.R + rows - 1) / rows)), dim3(kThreads), smem, stream, args);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_residual(const NormResidualArgs& a, cudaStream_t stream) {
+  DeviceInfo di;
+  const cudaError_t err = device_info(&di);
+  if (err != cudaSuccess) return err;
+  const int pieces = a.H % 8 == 0 ? a.H / 8 : (a.H + 14) / 8;  // of a row, at most
+  if (pieces > 1024) return launch_form<1024, 9>(a, stream);
+  if (a.R <= di.sm_count && pieces > 256) return launch_form<1024, 1>(a, stream);
+  if (pieces <= 128) return launch_form<32, 4>(a, stream);
+  return launch_form<256, 4>(a, stream);
+}
+
+}  // namespace mtp

@@ -8,20 +8,11 @@
 // Run once per weight load, not per draft: one warp per row, two passes over the row (the
 // second from L2), with several 16-byte loads in flight per lane in the first.
 //
-// The codes without a division per element. The code of the quotient depends only on which
-// pair of neighbouring E4M3 rounding boundaries the quotient lies between. With r = 1/s, the
-// products y_up = f * r (1 + 2^-21) and y_dn = f * r (1 - 2^-21) (each factor and product
-// rounded to nearest) bracket fp32(f / s) strictly: the four roundings move them by at most
-// 3 * 2^-24 relative, fp32(f / s) is within 2^-24 of f / s, and 2^-21 - 3 * 2^-24 > 2^-24.
-// The conversion to E4M3 (round to nearest even, saturating) is monotonic, so when y_up and
-// y_dn give the same code, fp32(f / s) gives it too. Otherwise (a boundary inside the bracket:
-// nearly always an exact tie, about 0.5 % of the elements of Gaussian rows) the code comes from
-// the division itself. Quotients below the
-// fp32 normal range convert to a signed zero on all three paths. Rows whose scale is not a
-// normal fp32 number take the division for every element.
+// The codes are made without a division per element (codes.cuh).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "codes.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -44,33 +35,6 @@ constexpr int kQThreads = 256;
 #endif
 constexpr int kLoadsMag = MTP_Q_LOADS;     // 16-byte loads in flight per lane, magnitude pass
 constexpr int kPiecesCode = MTP_Q_PIECES;  // 16-element pieces (32 bytes in, 16 out) per lane and step
-
-// Two E4M3 codes (round to nearest even, satfinite): byte 0 from lo, byte 1 from hi.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
-// max of the two 16-bit halves, lane by lane
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Codes of one bf16 pair (32-bit word) through the bracket, the division when it is open.
-__device__ __forceinline__ uint32_t pair_codes(uint32_t pair, float s, float r_up, float r_dn) {
-  const float a = bf16_lo(pair), b = bf16_hi(pair);
-  const uint32_t up = e4m3x2(__fmul_rn(a, r_up), __fmul_rn(b, r_up));
-  const uint32_t dn = e4m3x2(__fmul_rn(a, r_dn), __fmul_rn(b, r_dn));
-  if (up == dn) return up;
-  return e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s));
-}
-
-__device__ __forceinline__ uint32_t pair_codes_div(uint32_t pair, float s) {
-  return e4m3x2(__fdiv_rn(bf16_lo(pair), s), __fdiv_rn(bf16_hi(pair), s));
-}
 
 // Rows with H % 16 == 0: 16-byte loads and stores.
 __global__ void __launch_bounds__(kQThreads, MTP_Q_MINB) quantize_vec_kernel(const uint16_t* __restrict__ w,

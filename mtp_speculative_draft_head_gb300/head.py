@@ -5,7 +5,7 @@ It mirrors the source's `Glm5NextMtpHead` ("metrale_model_arch / glm5next_mtp_he
 weights it holds are ``embed_tokens``, ``eh_proj``, ``enorm``, ``hnorm``, ``final_norm`` and the
 target's ``lm_head`` (plus the optional FP8 copy of the `head_fp8` doc); its per-sequence scratch
 is the ``x`` / ``logits`` / ``draft`` buffers of the proposer state. The decoder layer between
-the two stages is the identity here. Every computation is a call into libmtphead.so.
+the two stages is the identity here, unless ``forward`` is given one (``DraftLayer``). Every computation is a call into libmtphead.so.
 """
 from __future__ import annotations
 
@@ -121,11 +121,16 @@ class MtpDraftHead:
         return logits, draft
 
     def forward(self, tokens, hidden, fp8: bool = False, logits=False, x=None, draft=None,
-                status=None, stream=None, fp4: bool = False):
-        """One draft step for B sequences (device buffers): returns (x, logits|None, draft)."""
+                status=None, stream=None, fp4: bool = False, layer=None):
+        """One draft step for B sequences (device buffers): returns (x, logits|None, draft). ``layer(x,
+        status=..., stream=...)``, if given, is the layer between the stages (``DraftLayer.step`` with its lengths
+        bound): it returns its output, which may be x itself."""
         B = tokens.numel()
         if fp8 and fp4:
             raise ValueError("fp8 and fp4 exclude each other")
+        if layer is not None:
+            x = layer(self.input(tokens, hidden, x, status, stream, fp4=fp4), status=status, stream=stream)
+            return (x, *self.logits_argmax(x, fp8, logits, draft, status, stream, fp4=fp4))
         if fp4:
             x = self.input(tokens, hidden, x, status, stream, fp4=True)
             return (x, *self.logits_argmax(x, fp8, logits, draft, status, stream, fp4=True))

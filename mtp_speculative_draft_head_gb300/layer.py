@@ -1,0 +1,141 @@
+"""``DraftLayer``: the attention half of the layer between the head's two stages, as a thin owner of
+buffers around the C ABI (include/mtp_head.h).
+
+In the source the drafter runs one decoder layer between the input and the output stage
+("glm5next_mtp_head.rs", `forward_one`: the block call over the drafter's own one-layer KV pool). The
+head here leaves it out unless it is given one: ``MtpDraftHead.forward(layer=...)`` calls it on the block input. Its
+projections run over FP4 copies, its keys and values live in a paged FP4 cache, and what is a model's
+own (the rotation of queries and keys, the second half of the layer) is passed in as functions.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+
+
+class LayerCache:
+    """A paged FP4 cache of keys and values for ``batch`` sequences of up to ``max_len`` tokens: the three
+    arrays, and a table that gives every sequence pages of its own (``table`` may be replaced by one that
+    shares or reorders them)."""
+
+    def __init__(self, batch: int, max_len: int, kv_heads: int, head_dim: int, page: int = 64, device=None):
+        self.max_pages = -(-max_len // page)
+        self.page, self.max_len = page, self.max_pages * page
+        self.kv_heads, self.head_dim, self.batch = kv_heads, head_dim, batch
+        self.arrays = _lib.cache_empty(batch * self.max_pages, page, kv_heads, head_dim, device)
+        self.device = self.arrays[0].device
+        self.table = torch.arange(batch * self.max_pages, dtype=torch.int32, device=self.device).view(batch, -1)
+
+    def write(self, k, v, row_start, position, status=None, stream=None) -> None:
+        """Packed rows k, v [T, kv_heads, head_dim] to the sequences' places, as mtp_head_cache_write_fp4."""
+        _lib.mtp_head_cache_write_fp4(k, v, row_start, position, self.table, *self.arrays, status, stream)
+
+    def read(self, row_start, position, rows: int, status=None, stream=None):
+        """``rows`` packed rows (k, v) back as BF16, as mtp_head_cache_read_fp4 (rows of no sequence: zeros)."""
+        k, v = (torch.zeros((rows, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+                for _ in range(2))
+        _lib.mtp_head_cache_read_fp4(*self.arrays, row_start, position, self.table, k, v, status, stream)
+        return k, v
+
+
+class DraftLayer:
+    """x <- x + o_proj . attention(qkv_proj . norm(x)), then, with ``mlp``, x <- x + mlp(norm(x)).
+
+    ``norm_w`` [H], ``qkv_proj`` [(q_heads + 2 kv_heads) head_dim, H], ``o_proj`` [H, q_heads head_dim] BF16: the
+    projections are copied to FP4 here. ``rotate(q, k, positions)``, if given, rotates the views q
+    [R, q_heads, head_dim] and k [R, kv_heads, head_dim] in place (positions [R] int32). ``mlp(y, q, q_scale)``, with
+    ``mlp_norm_w`` [H], takes the normalised rows in BF16 and in E4M3 (a scale per 128 columns) and returns what is
+    added to x. ``max_rows``: rows of a call at most."""
+
+    def __init__(self, norm_w, qkv_proj, o_proj, q_heads: int, kv_heads: int, cache: LayerCache, eps: float = 1e-6,
+                 max_rows: int = 16, rotate=None, mlp=None, mlp_norm_w=None):
+        self.H, self.D = norm_w.numel(), cache.head_dim
+        self.q_heads, self.kv_heads = q_heads, kv_heads
+        width = (q_heads + 2 * kv_heads) * self.D
+        if qkv_proj.shape != (width, self.H) or o_proj.shape != (self.H, q_heads * self.D):
+            raise ValueError("shapes: qkv_proj [(q_heads + 2 kv_heads) head_dim, H], o_proj [H, q_heads head_dim]")
+        if kv_heads != cache.kv_heads:
+            raise ValueError("the cache is for another number of key heads")
+        if (mlp is None) != (mlp_norm_w is None):
+            raise ValueError("mlp and mlp_norm_w go together")
+        self.norm_w, self.mlp_norm_w, self.eps = norm_w, mlp_norm_w, float(eps)
+        self.cache, self.rotate, self.mlp, self.max_rows = cache, rotate, mlp, max_rows
+        dev = self.device = cache.device
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.qkv_fp4 = _lib.fp4_empty(width, self.H, dev)
+        _lib.mtp_head_quantize_fp4(qkv_proj, *self.qkv_fp4, st)
+        self.o_fp4 = _lib.fp4_empty(self.H, q_heads * self.D, dev)
+        _lib.mtp_head_quantize_fp4(o_proj, *self.o_fp4, st)
+        if int(st.item()) != 0:
+            raise _lib.MTPError(int(st.item()), "DraftLayer")
+        self.ws_qkv = _lib.linear_fp4_workspace(max_rows, width, self.H, dev)
+        self.ws_o = _lib.linear_fp4_workspace(max_rows, self.H, q_heads * self.D, dev)
+        self.ws_step = None
+
+    def _project(self, x, status, stream):
+        R = x.shape[0]
+        if R > self.max_rows:
+            raise ValueError(f"{R} rows, made for {self.max_rows}")
+        y = torch.empty_like(x)
+        _lib.mtp_head_norm_residual(x, self.norm_w, y=y, eps=self.eps, stream=stream)
+        qkv = torch.empty((R, self.q_heads + 2 * self.kv_heads, self.D), dtype=torch.bfloat16, device=self.device)
+        _lib.mtp_head_linear_fp4(y, *self.qkv_fp4, qkv.view(R, -1), self.ws_qkv, status, stream)
+        return qkv.split([self.q_heads, self.kv_heads, self.kv_heads], 1)
+
+    def _finish(self, x, heads, status, stream):
+        delta = torch.empty_like(x)
+        _lib.mtp_head_linear_fp4(heads.view(x.shape[0], -1), *self.o_fp4, delta, self.ws_o, status, stream)
+        if self.mlp is None:
+            _lib.mtp_head_norm_residual(x, self.norm_w, delta, total=x, eps=self.eps, stream=stream)
+            return x
+        y = torch.empty_like(x)
+        q = torch.empty(x.shape, dtype=torch.uint8, device=self.device)
+        scale = torch.empty((x.shape[0], -(-self.H // 128)), dtype=torch.float32, device=self.device)
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        _lib.mtp_head_norm_residual(x, self.mlp_norm_w, delta, x, y, q, scale, status, 128, self.eps, stream)
+        _lib.mtp_head_norm_residual(x, self.mlp_norm_w, self.mlp(y, q, scale), total=x, eps=self.eps, stream=stream)
+        return x
+
+    def step(self, x, length, status=None, stream=None):
+        """The layer over the next rows of each sequence, in place: x [B Q, H] (Q rows of each of B sequences, the
+        first B of the cache), length [B] int32 the tokens that the cache holds with them. Their keys and values are
+        written to the cache first."""
+        B = length.numel()
+        if x.shape[0] % B != 0 or B > self.cache.batch:
+            raise ValueError("x: an equal number of rows for each sequence of the cache")
+        Q = x.shape[0] // B
+        with torch.cuda.stream(stream):
+            q, k, v = self._project(x, status, stream)
+            starts = torch.arange(0, (B + 1) * Q, Q, dtype=torch.int32, device=self.device)
+            first = length - Q
+            if self.rotate is not None:
+                self.rotate(q, k, (first.view(-1, 1) + torch.arange(Q, dtype=torch.int32, device=self.device)).view(-1))
+            table = self.cache.table[:B]
+            _lib.mtp_head_cache_write_fp4(k, v, starts, first, table, *self.cache.arrays, status, stream)
+            if self.ws_step is None:
+                self.ws_step = _lib.attention_fp4_workspace(min(self.cache.batch, self.max_rows), self.max_rows, self.q_heads,
+                                                            self.kv_heads, self.D, self.cache.max_len, self.device)
+            heads = torch.empty((B, Q, self.q_heads, self.D), dtype=torch.bfloat16, device=self.device)
+            _lib.mtp_head_attention_fp4(q.unflatten(0, (B, Q)), *self.cache.arrays, table, length, heads, self.ws_step,
+                                        status=status, stream=stream)
+            return self._finish(x, heads, status, stream)
+
+    def prompt(self, x, row_start, status=None, stream=None):
+        """The layer over whole prompts, in place: x [T, H], sequence b's rows row_start[b] .. row_start[b + 1]
+        (row_start [B + 1] int32), from its first position on. Their keys and values fill the cache."""
+        B = row_start.numel() - 1
+        if B > self.cache.batch:
+            raise ValueError("more sequences than the cache has")
+        with torch.cuda.stream(stream):
+            q, k, v = self._project(x, status, stream)
+            if self.rotate is not None:
+                row = torch.arange(x.shape[0], dtype=torch.int32, device=self.device)
+                which = torch.bucketize(row, row_start[1:], out_int32=True, right=True).clamp_(max=B - 1)
+                self.rotate(q, k, row - row_start[which.long()])
+            first = torch.zeros(B, dtype=torch.int32, device=self.device)
+            _lib.mtp_head_cache_write_fp4(k, v, row_start, first, self.cache.table[:B], *self.cache.arrays, status, stream)
+            heads = torch.zeros((x.shape[0], self.q_heads, self.D), dtype=torch.bfloat16, device=self.device)
+            _lib.mtp_head_attention_prompt(q, k, v, row_start, heads, status=status, stream=stream)
+            return self._finish(x, heads, status, stream)
