@@ -509,8 +509,8 @@ int mtp_head_verify(const float* target_probs, const float* draft_probs,
  * attention half is made of, together with mtp_head_linear_fp4 for its projections: the residual norm,
  * a paged cache of keys and values in four bits, attention over it for a step's rows, and attention
  * over whole prompts. In all of them an output or a workspace on an input that is still read, or on
- * another output, is MTP_ERR_ARG, but for what is stated. They need no wait limit: none of their waits
- * is for another kernel, and mtp_head_attention_prompt's, for its own copies and products, take 2 s.
+ * another output, is MTP_ERR_ARG, but for what is stated. Their kernels wait for
+ * their own copies and products only, 2 s at most.
  *
  * Residual norm. For each of R rows of H columns:
  *   total = bf16( x + delta )              the real sum rounded once; x itself when delta is NULL
@@ -577,7 +577,7 @@ int mtp_head_cache_read_fp4(const uint8_t* q, const uint8_t* block_scale, const 
  *   lse      [B, Q, q_heads] fp32      optional: ln sum_j exp(scale q . k_j)
  *   status   [1] int32   optional; MTP_ERR_ARG: a length outside 0 .. max_pages * page or rows outside
  *                        0 .. Q (that sequence's Q rows are zeros, their lse -Inf), or a page outside
- *                        0 .. pages (its tokens count as rows of zeros)
+ *                        0 .. pages (its tokens are left out); MTP_ERR_TIMEOUT: a wait ran out
  *   cache, block_table, pages, page, max_pages   as above; q_heads a multiple of kv_heads (at most 1024
  *                        each): query head h reads key head h / (q_heads / kv_heads)
  *

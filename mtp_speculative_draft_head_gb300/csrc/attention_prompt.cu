@@ -17,6 +17,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "codes.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
 #include "internal.h"
@@ -112,12 +113,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // All ones in the halves of a BF16 pair that are infinite or NaN.
 __device__ __forceinline__ uint32_t nonfinite(uint32_t pair) { return __vcmpeq2(pair & 0x7F807F80u, 0x7F807F80u); }
 

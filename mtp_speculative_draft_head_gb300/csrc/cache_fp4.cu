@@ -2,9 +2,9 @@
 //
 // A row (one token, one head, key or value) is quantised by itself, in the format and with the
 // roundings of the FP4 copies (codes.cuh): E2M1 codes, an E4M3 scale per 16 columns, an fp32 scale per
-// row. D / 16 threads share a row, one block of 16 columns each (32 bytes in, 8 bytes of codes and
-// one of scale out), so a row's maximum is a few shuffles and a warp's loads and stores are
-// contiguous over whole heads. Bound by bytes: 4 D in and 2 (D/2 + D/16 + 4) out for a token's key and
+// row. A warp takes a token (where it lives is found once for all its heads), D / 16 lanes a row, one block of
+// 16 columns each (32 bytes in, 8 bytes of codes and one of scale out), so a row's maximum is a few
+// shuffles and a warp's loads and stores are contiguous over whole heads. Bound by bytes: 4 D in and 2 (D/2 + D/16 + 4) out for a token's key and
 // value of one head, or the other way round.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -22,8 +22,7 @@ namespace {
 
 constexpr int kCThreads = 256;
 
-// Where row t of the packed rows lives: its place in the cache's rows of one head and kind, as
-// page * kind/head stride + offset. -1: the row belongs to no sequence; -2: its place does not exist.
+// Where row t of the packed rows lives. 0: found; -1: the row belongs to no sequence; -2: its place does not exist.
 struct Place {
   int page, off;
 };
@@ -46,94 +45,143 @@ __device__ __forceinline__ int find_place(const CacheRowsArgs& a, int t, Place& 
   return p.page < 0 || p.page >= a.c.pages ? -2 : 0;
 }
 
+// Row r of a token's 2 heads rows (keys first).
+struct RowOf {
+  int kind, h;
+  __device__ __forceinline__ RowOf(int r, int heads) : kind(r >= heads ? 1 : 0), h(r >= heads ? r - heads : r) {}
+};
+
+// `parts` warps share a token (1, or as many as keep the GPU busy when there are few tokens).
 template <int D>
-__global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsArgs a) {
-  constexpr int kB = D / kFp4Block;  // blocks (and threads) of a row
+__global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsArgs a, int parts) {
+  constexpr int kB = D / kFp4Block;  // blocks (and lanes) of a row
+  constexpr int kR = 32 / kB;        // rows of a warp at a time
+  constexpr int kAhead = 2;          // of these, loads in flight
   pdl_wait_prior_grid();
-  const int per_token = 2 * a.c.heads * kB;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kCThreads + threadIdx.x;
-  const int t = static_cast<int>(i / per_token), r = static_cast<int>(i % per_token);
-  const int j = r % kB, h = (r / kB) % a.c.heads, kind = r / (kB * a.c.heads);
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCThreads + threadIdx.x) >> 5;
+  const int t = static_cast<int>(wid / parts), part = static_cast<int>(wid % parts);
+  if (t >= a.T) return;
+  const int lane = threadIdx.x & 31, j = lane % kB;
   Place p{0, 0};
-  int found = -1;
-  uint4 u0 = make_uint4(0u, 0u, 0u, 0u), u1 = u0;
-  if (t < a.T) {
-    const uint16_t* src = (kind == 0 ? a.k_in + t * a.ld_k : a.v_in + t * a.ld_v) + h * D + j * kFp4Block;
-    u0 = __ldcs(reinterpret_cast<const uint4*>(src));
-    u1 = __ldcs(reinterpret_cast<const uint4*>(src) + 1);
-    found = find_place(a, t, p);
-  }
-  uint32_t m = mag_max(mag_max(0u, u0), u1);
-  uint32_t mx = max(m & 0xFFFFu, m >> 16);
-#pragma unroll
-  for (int k = kB / 2; k > 0; k >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+  const int found = find_place(a, t, p);
   if (found != 0) {
-    if (found == -2) store_status(a.status, MTP_ERR_ARG);
+    if (found == -2 && lane == 0) store_status(a.status, MTP_ERR_ARG);
     return;
   }
-  float rs = __fdiv_rn(bf16_bits_to_f32(mx), 2688.0f);
-  if (mx >= 0x7F80u) {  // a NaN or Inf in the row
-    if (j == 0) store_status(a.status, MTP_ERR_NONFINITE);
-    rs = 0.0f;
+  const int rows = 2 * a.c.heads;
+  const uint16_t* k = a.k_in + t * a.ld_k + j * kFp4Block;
+  const uint16_t* v = a.v_in + t * a.ld_v + j * kFp4Block;
+  const int64_t dst0 = static_cast<int64_t>(p.page) * 2 * a.c.heads * a.c.page + p.off;  // its first row in the page
+  for (int r0 = part * kR * kAhead + lane / kB; r0 - lane / kB < rows; r0 += parts * kR * kAhead) {
+    uint4 u[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kR;
+      const RowOf ro(r, a.c.heads);
+      u[i][0] = u[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        const uint4* src = reinterpret_cast<const uint4*>((ro.kind ? v : k) + ro.h * D);
+        u[i][0] = __ldcs(src);
+        u[i][1] = __ldcs(src + 1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kR;
+      const uint32_t m = mag_max(mag_max(0u, u[i][0]), u[i][1]);
+      uint32_t mx = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+      for (int s = kB / 2; s > 0; s >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+      if (r >= rows) continue;
+      float rs = __fdiv_rn(bf16_bits_to_f32(mx), 2688.0f);
+      if (mx >= 0x7F80u) {  // a NaN or Inf in the row
+        if (j == 0) store_status(a.status, MTP_ERR_NONFINITE);
+        rs = 0.0f;
+      }
+      BlockCodes o{0u, 0u, 0u};
+      if (rs > 0.0f) {
+        const float r6 = rs >= kSmallRs ? recip(__fmul_rn(6.0f, rs)) : 0.0f;
+        o = block_codes(u[i][0], u[i][1], rs, __fmul_rn(r6, kUp), __fmul_rn(r6, kDn));
+      }
+      const int64_t dst = dst0 + static_cast<int64_t>(r) * a.c.page;
+      *reinterpret_cast<uint2*>(a.c.q + dst * (D / 2) + j * 8) = make_uint2(o.c0, o.c1);
+      a.c.bs[dst * kB + j] = static_cast<uint8_t>(o.sc);
+      if (j == 0) a.c.rs[dst] = rs;
+    }
   }
-  BlockCodes o{0u, 0u, 0u};
-  if (rs > 0.0f) {
-    const float r6 = rs >= kSmallRs ? recip(__fmul_rn(6.0f, rs)) : 0.0f;
-    o = block_codes(u0, u1, rs, __fmul_rn(r6, kUp), __fmul_rn(r6, kDn));
-  }
-  const int64_t dst = ((static_cast<int64_t>(p.page) * 2 + kind) * a.c.heads + h) * a.c.page + p.off;
-  *reinterpret_cast<uint2*>(a.c.q + dst * (D / 2) + j * 8) = make_uint2(o.c0, o.c1);
-  a.c.bs[dst * kB + j] = static_cast<uint8_t>(o.sc);
-  if (j == 0) a.c.rs[dst] = rs;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kCThreads) cache_read_kernel(const CacheRowsArgs a) {
+__global__ void __launch_bounds__(kCThreads) cache_read_kernel(const CacheRowsArgs a, int parts) {
   constexpr int kB = D / kFp4Block;
+  constexpr int kR = 32 / kB;
+  constexpr int kAhead = 4;
   pdl_wait_prior_grid();
-  const int per_token = 2 * a.c.heads * kB;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kCThreads + threadIdx.x;
-  const int t = static_cast<int>(i / per_token), r = static_cast<int>(i % per_token);
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCThreads + threadIdx.x) >> 5;
+  const int t = static_cast<int>(wid / parts), part = static_cast<int>(wid % parts);
   if (t >= a.T) return;
-  const int j = r % kB, h = (r / kB) % a.c.heads, kind = r / (kB * a.c.heads);
+  const int lane = threadIdx.x & 31, j = lane % kB;
   Place p{0, 0};
   const int found = find_place(a, t, p);
   if (found == -1) return;
-  uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (found == 0) {
-    const int64_t src = ((static_cast<int64_t>(p.page) * 2 + kind) * a.c.heads + h) * a.c.page + p.off;
-    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(a.c.q + src * (D / 2) + j * 8));
-    const uint32_t s2 = e4m3x2_to_f16x2(a.c.bs[src * kB + j] * 0x0101u);
-    const float rs = a.c.rs[src];
+  if (found == -2 && lane == 0) store_status(a.status, MTP_ERR_ARG);
+  const int rows = 2 * a.c.heads;
+  uint16_t* k = a.k_out + t * a.ld_k + j * kFp4Block;
+  uint16_t* v = a.v_out + t * a.ld_v + j * kFp4Block;
+  const int64_t src0 = static_cast<int64_t>(p.page) * 2 * a.c.heads * a.c.page + p.off;
+  for (int r0 = part * kR * kAhead + lane / kB; r0 < rows; r0 += parts * kR * kAhead) {
+    uint2 c[kAhead];
+    uint32_t sc[kAhead];
+    float rs[kAhead];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t v[4], w[4];
-      e2m1x8_to_f16x2x4(e == 0 ? c.x : c.y, v);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t x = f16x2_mul(v[k], s2);  // exact
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-            : "=r"(w[k])
-            : "f"(__fmul_rn(f16_hi(x), rs)), "f"(__fmul_rn(f16_lo(x), rs)));
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kR;
+      const int64_t src = src0 + static_cast<int64_t>(r) * a.c.page;
+      c[i] = make_uint2(0u, 0u);  // (a row without a place: zeros)
+      sc[i] = 0u;
+      rs[i] = 0.0f;
+      if (r < rows && found == 0) {
+        c[i] = __ldcs(reinterpret_cast<const uint2*>(a.c.q + src * (D / 2) + j * 8));
+        sc[i] = a.c.bs[src * kB + j];
+        rs[i] = a.c.rs[src];
       }
-      o[e] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-  } else if (j == 0) {
-    store_status(a.status, MTP_ERR_ARG);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * kR;
+      if (r >= rows) continue;
+      const RowOf ro(r, a.c.heads);
+      const uint32_t s2 = e4m3x2_to_f16x2(sc[i] * 0x0101u);
+      uint4* dst = reinterpret_cast<uint4*>((ro.kind ? v : k) + ro.h * D);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t x[4], w[4];
+        e2m1x8_to_f16x2x4(e == 0 ? c[i].x : c[i].y, x);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t y = f16x2_mul(x[n], s2);  // exact
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+              : "=r"(w[n])
+              : "f"(__fmul_rn(f16_hi(y), rs[i])), "f"(__fmul_rn(f16_lo(y), rs[i])));
+        }
+        __stcs(dst + e, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
   }
-  uint16_t* dst = (kind == 0 ? a.k_out + t * a.ld_k : a.v_out + t * a.ld_v) + h * D + j * kFp4Block;
-  __stcs(reinterpret_cast<uint4*>(dst), o[0]);
-  __stcs(reinterpret_cast<uint4*>(dst) + 1, o[1]);
 }
 
-cudaError_t launch_rows(const void* kern, const CacheRowsArgs& a, cudaStream_t stream) {
+cudaError_t launch_rows(const void* kern, int rows_at_once, const CacheRowsArgs& a, cudaStream_t stream) {
   DeviceInfo di;
   const cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
-  const int64_t n = static_cast<int64_t>(a.T) * 2 * a.c.heads * (a.c.D / kFp4Block);
+  // few tokens: a warp for every batch of rows
+  int parts = (2 * a.c.heads + rows_at_once - 1) / rows_at_once;
+  const int64_t busy = static_cast<int64_t>(di.sm_count) * 32;
+  while (parts > 1 && a.T * static_cast<int64_t>(parts) > busy) parts = (parts + 1) / 2;
+  const int64_t warps = static_cast<int64_t>(a.T) * parts;
   CacheRowsArgs p = a;
-  void* args[] = {&p};
-  return launch_pdl(kern, dim3(static_cast<unsigned>((n + kCThreads - 1) / kCThreads)), dim3(kCThreads), 0, stream, args);
+  void* args[] = {&p, &parts};
+  return launch_pdl(kern, dim3(static_cast<unsigned>((warps * 32 + kCThreads - 1) / kCThreads)), dim3(kCThreads), 0, stream, args);
 }
 
 }  // namespace
@@ -141,12 +189,12 @@ cudaError_t launch_rows(const void* kern, const CacheRowsArgs& a, cudaStream_t s
 cudaError_t launch_cache_write(const CacheRowsArgs& a, cudaStream_t stream) {
   return launch_rows(a.c.D == 64 ? reinterpret_cast<const void*>(cache_write_kernel<64>)
                                  : reinterpret_cast<const void*>(cache_write_kernel<128>),
-                     a, stream);
+                     2 * 512 / a.c.D, a, stream);
 }
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t stream) {
   return launch_rows(a.c.D == 64 ? reinterpret_cast<const void*>(cache_read_kernel<64>)
                                  : reinterpret_cast<const void*>(cache_read_kernel<128>),
-                     a, stream);
+                     4 * 512 / a.c.D, a, stream);
 }
 
 }  // namespace mtp

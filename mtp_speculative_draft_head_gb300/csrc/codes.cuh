@@ -45,6 +45,34 @@ __device__ __forceinline__ uint32_t pair_codes_div(uint32_t pair, float s) {
   return e4m3x2(__fdiv_rn(bf16_lo(pair), s), __fdiv_rn(bf16_hi(pair), s));
 }
 
+// Eight codes e4m3( fp32( w / s ) ) of BF16 pairs, without a branch: with r = 1 / s rounded to nearest and q = w r, one
+// step q + r (w - q s), both by fused multiply-adds, is the correctly rounded quotient (Markstein); the remainder is exact
+// for s >= 2^-80 wherever the quotient reaches half of the smallest code. Smaller scales divide.
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint2 codes_e4m3x8(const uint32_t (&u)[4], float s) {
+  if (s == 0.0f) return make_uint2(0u, 0u);
+  uint32_t c[4];
+  if (s >= 0x1p-80f) {
+    const float r = __frcp_rn(s);
+    const uint64_t r2 = f2_pack(r, r), ns = f2_pack(-s, -s);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint64_t w = bf16x2_to_f2(u[t]);
+      const uint64_t q = f2_mul(w, r2);
+      const uint64_t y = f2_fma(f2_fma(q, ns, w), r2, q);
+      c[t] = e4m3x2(f2_lo(y), f2_hi(y));
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) c[t] = pair_codes_div(u[t], s);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 // ------------------------------------------------------------------------------------------ E2M1
 // The same for a block of 16 E2M1 codes and its E4M3 scale (the format is in fp4.cuh): with
 // r = 1 / (s_j rs), formed in fp32, the products |w| r (1 + 2^-21) and |w| r (1 - 2^-21) bracket

@@ -43,20 +43,12 @@ __device__ __forceinline__ void store8(uint16_t* base, int64_t at, int c0, int H
     if (c0 + i >= 0 && c0 + i < H) p[i] = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
 }
 
-// bf16( a + b ) of two BF16 values: the fp32 sum decides unless it lies on a BF16 midpoint.
+// bf16( a + b ) of two BF16 pairs. The fp32 sum in between does no harm: it is inexact only when one number is below
+// 2^-16 of the other, and then the sum is nowhere near a midpoint of BF16 values.
 __device__ __forceinline__ uint32_t add_pair(uint32_t a, uint32_t b) {
-  const float l = __fadd_rn(bf16_lo(a), bf16_lo(b)), h = __fadd_rn(bf16_hi(a), bf16_hi(b));
+  const uint64_t s = f2_add(bf16x2_to_f2(a), bf16x2_to_f2(b));
   uint32_t o;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(h), "f"(l));
-  float s, e;
-  if ((__float_as_uint(l) & 0xFFFFu) == 0x8000u) {
-    two_sum(bf16_lo(a), bf16_lo(b), s, e);
-    o = (o & 0xFFFF0000u) | bf16_rne_df(s, e);
-  }
-  if ((__float_as_uint(h) & 0xFFFFu) == 0x8000u) {
-    two_sum(bf16_hi(a), bf16_hi(b), s, e);
-    o = (o & 0xFFFFu) | (static_cast<uint32_t>(bf16_rne_df(s, e)) << 16);
-  }
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(f2_hi(s)), "f"(f2_lo(s)));
   return o;
 }
 // A BF16 pair times a power of two (exact, but for results below the normal range).
@@ -66,20 +58,32 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t a, float f) {
   return o;
 }
 
-// Eight E4M3 codes of four BF16 pairs.
-__device__ __forceinline__ uint2 codes_e4m3(const uint32_t (&u)[4], float s) {
-  if (s == 0.0f) return make_uint2(0u, 0u);
-  uint32_t c[4];
-  if (s >= 1.17549435e-38f) {
-    const float r = __frcp_rn(s);
-    const float r_up = __fmul_rn(r, 1.0f + 0x1p-21f), r_dn = __fmul_rn(r, 1.0f - 0x1p-21f);
+// bf16( x w (rh + rl) ) of eight columns, as bf16x8_scaled_rne: the fp32 product x w rh decides unless its low half is within
+// two units of a BF16 midpoint; such a cell is redone as a whole from double-floats, out of line.
+static __device__ __noinline__ uint4 scaled_exact(uint4 x, uint4 w01, uint4 w23, float rh, float rl) {
+  const uint32_t xu[4] = {x.x, x.y, x.z, x.w};
+  const float wf[8] = {__uint_as_float(w01.x), __uint_as_float(w01.y), __uint_as_float(w01.z), __uint_as_float(w01.w),
+                       __uint_as_float(w23.x), __uint_as_float(w23.y), __uint_as_float(w23.z), __uint_as_float(w23.w)};
+  return bf16x8_scaled_rne(xu, wf, rh, rl);
+}
+__device__ __forceinline__ uint4 scaled(const uint32_t (&x)[4], const uint64_t (&w)[4], float rh, float rl) {
+  const uint64_t r2 = f2_pack(rh, rh);
+  uint32_t o[4], near = 0xFFFFFFFFu;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) c[t] = pair_codes(u[t], s, r_up, r_dn);
-  } else {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) c[t] = pair_codes_div(u[t], s);
+  for (int t = 0; t < 4; ++t) {
+    const uint64_t y = f2_mul(f2_mul(bf16x2_to_f2(x[t]), w[t]), r2);
+    const uint32_t lo = static_cast<uint32_t>(y), hi = static_cast<uint32_t>(y >> 32);
+    near = min(near, min((lo - 0x7FFEu) << 16, (hi - 0x7FFEu) << 16));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[t]) : "f"(f2_hi(y)), "f"(f2_lo(y)));
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  if (near <= 0x40000u || !(rh >= 1.17549435e-38f))
+    return scaled_exact(make_uint4(x[0], x[1], x[2], x[3]),
+                        make_uint4(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
+                                   static_cast<uint32_t>(w[1] >> 32)),
+                        make_uint4(static_cast<uint32_t>(w[2]), static_cast<uint32_t>(w[2] >> 32), static_cast<uint32_t>(w[3]),
+                                   static_cast<uint32_t>(w[3] >> 32)),
+                        rh, rl);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Groups of a row that TPR threads hold in P pieces each, at most.
@@ -226,17 +230,17 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
   for (int i = 0; i < P; ++i) {
     const int c0 = 8 * (t + i * TPR) - off;
     if (c0 >= H) continue;
-    float wf[8];
+    uint64_t w[4];
     if constexpr (VEC) {
       const uint4 w4 = *reinterpret_cast<const uint4*>(a.w + c0);
-      const uint32_t wu[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wf[e] = (e & 1) ? bf16_hi(wu[e >> 1]) : bf16_lo(wu[e >> 1]);
+      w[0] = bf16x2_to_f2(w4.x), w[1] = bf16x2_to_f2(w4.y), w[2] = bf16x2_to_f2(w4.z), w[3] = bf16x2_to_f2(w4.w);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wf[e] = c0 + e >= 0 && c0 + e < H ? bf16_bits_to_f32(a.w[c0 + e]) : 0.0f;
+      for (int e = 0; e < 4; ++e)
+        w[e] = f2_pack(c0 + 2 * e >= 0 && c0 + 2 * e < H ? bf16_bits_to_f32(a.w[c0 + 2 * e]) : 0.0f,
+                       c0 + 2 * e + 1 >= 0 && c0 + 2 * e + 1 < H ? bf16_bits_to_f32(a.w[c0 + 2 * e + 1]) : 0.0f);
     }
-    const uint4 o = bf16x8_scaled_rne(s[i], wf, rh, rl);
+    const uint4 o = scaled(s[i], w, rh, rl);
     s[i][0] = o.x, s[i][1] = o.y, s[i][2] = o.z, s[i][3] = o.w;
     if constexpr (!VEC) {  // (a NaN factor leaves a NaN in the columns that are not the row's)
 #pragma unroll
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int c0 = 8 * (t + i * TPR) - off;
-      if (c0 < H) store_codes(c0, codes_e4m3(s[i], sc));
+      if (c0 < H) store_codes(c0, codes_e4m3x8(s[i], sc));
     }
     return;
   }
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
       const float sc = mx >= 0x7F80u ? 0.0f : __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
       if (c0 < H) {
         if ((lane & 15) == 0) scales[c0 / kNormGroup] = scale_of(mx);
-        store_codes(c0, codes_e4m3(s[i], sc));
+        store_codes(c0, codes_e4m3x8(s[i], sc));
       }
     }
   } else {
@@ -337,10 +341,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
       const int c0 = 8 * (t + i * TPR) - off;
       if (c0 >= H) continue;
       const int g0 = c0 < 0 ? 0 : c0 / kNormGroup;
-      uint2 c = codes_e4m3(s[i], at_group(g0));
+      uint2 c = codes_e4m3x8(s[i], at_group(g0));
       const int n0 = (g0 + 1) * kNormGroup - c0;  // columns of the piece in its first group
       if (n0 < 8) {
-        const uint2 d = codes_e4m3(s[i], at_group(g0 + 1));
+        const uint2 d = codes_e4m3x8(s[i], at_group(g0 + 1));
         const uint64_t keep = (1ull << (8 * n0)) - 1ull;
         const uint64_t both = ((static_cast<uint64_t>(c.y) << 32 | c.x) & keep) | ((static_cast<uint64_t>(d.y) << 32 | d.x) & ~keep);
         c = make_uint2(static_cast<uint32_t>(both), static_cast<uint32_t>(both >> 32));
@@ -370,9 +374,13 @@ cudaError_t launch_norm_residual(const NormResidualArgs& a, cudaStream_t stream)
   const cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   const int pieces = a.H % 8 == 0 ? a.H / 8 : (a.H + 14) / 8;  // of a row, at most
-  if (pieces > 1024) return launch_form<1024, 9>(a, stream);
+  if (pieces > 1024) return launch_form<512, 17>(a, stream);
   if (a.R <= di.sm_count && pieces > 256) return launch_form<1024, 1>(a, stream);
   if (pieces <= 128) return launch_form<32, 4>(a, stream);
+  // as few registers as hold the row: more rows of an SM are in flight
+  if (pieces <= 256) return launch_form<256, 1>(a, stream);
+  if (pieces <= 512) return launch_form<256, 2>(a, stream);
+  if (pieces <= 768) return launch_form<256, 3>(a, stream);
   return launch_form<256, 4>(a, stream);
 }
 
