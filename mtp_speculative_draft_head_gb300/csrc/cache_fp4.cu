@@ -62,18 +62,11 @@ __global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsA
   const int t = static_cast<int>(wid / parts), part = static_cast<int>(wid % parts);
   if (t >= a.T) return;
   const int lane = threadIdx.x & 31, j = lane % kB;
-  Place p{0, 0};
-  const int found = find_place(a, t, p);
-  if (found != 0) {
-    if (found == -2 && lane == 0) store_status(a.status, MTP_ERR_ARG);
-    return;
-  }
   const int rows = 2 * a.c.heads;
   const uint16_t* k = a.k_in + t * a.ld_k + j * kFp4Block;
   const uint16_t* v = a.v_in + t * a.ld_v + j * kFp4Block;
-  const int64_t dst0 = static_cast<int64_t>(p.page) * 2 * a.c.heads * a.c.page + p.off;  // its first row in the page
-  for (int r0 = part * kR * kAhead + lane / kB; r0 - lane / kB < rows; r0 += parts * kR * kAhead) {
-    uint4 u[kAhead][2];
+  uint4 u[kAhead][2];
+  auto load = [&](int r0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int r = r0 + i * kR;
@@ -85,6 +78,18 @@ __global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsA
         u[i][1] = __ldcs(src + 1);
       }
     }
+  };
+  const int first = part * kR * kAhead + lane / kB;
+  load(first);  // (under the search for the token's place)
+  Place p{0, 0};
+  const int found = find_place(a, t, p);
+  if (found != 0) {
+    if (found == -2 && lane == 0) store_status(a.status, MTP_ERR_ARG);
+    return;
+  }
+  const int64_t dst0 = static_cast<int64_t>(p.page) * 2 * a.c.heads * a.c.page + p.off;  // its first row in the page
+  for (int r0 = first; r0 - lane / kB < rows; r0 += parts * kR * kAhead) {
+    if (r0 != first) load(r0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int r = r0 + i * kR;
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsA
         const float r6 = rs >= kSmallRs ? recip(__fmul_rn(6.0f, rs)) : 0.0f;
         o = block_codes(u[i][0], u[i][1], rs, __fmul_rn(r6, kUp), __fmul_rn(r6, kDn));
       }
-      const int64_t dst = dst0 + static_cast<int64_t>(r) * a.c.page;
+      const int64_t dst = dst0 + r * a.c.page;
       *reinterpret_cast<uint2*>(a.c.q + dst * (D / 2) + j * 8) = make_uint2(o.c0, o.c1);
       a.c.bs[dst * kB + j] = static_cast<uint8_t>(o.sc);
       if (j == 0) a.c.rs[dst] = rs;
@@ -111,38 +116,37 @@ __global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsA
   }
 }
 
+// Eight columns a lane: 4 bytes of codes in, 16 bytes out, neighbouring lanes neighbouring columns.
 template <int D>
 __global__ void __launch_bounds__(kCThreads) cache_read_kernel(const CacheRowsArgs a, int parts) {
-  constexpr int kB = D / kFp4Block;
-  constexpr int kR = 32 / kB;
-  constexpr int kAhead = 4;
+  constexpr int kL = D / 8;    // lanes of a row
+  constexpr int kR = 32 / kL;  // rows of a warp at a time
+  constexpr int kAhead = 8;
   pdl_wait_prior_grid();
   const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCThreads + threadIdx.x) >> 5;
   const int t = static_cast<int>(wid / parts), part = static_cast<int>(wid % parts);
   if (t >= a.T) return;
-  const int lane = threadIdx.x & 31, j = lane % kB;
+  const int lane = threadIdx.x & 31, j = lane % kL;
   Place p{0, 0};
   const int found = find_place(a, t, p);
   if (found == -1) return;
   if (found == -2 && lane == 0) store_status(a.status, MTP_ERR_ARG);
   const int rows = 2 * a.c.heads;
-  uint16_t* k = a.k_out + t * a.ld_k + j * kFp4Block;
-  uint16_t* v = a.v_out + t * a.ld_v + j * kFp4Block;
+  uint16_t* k = a.k_out + t * a.ld_k + j * 8;
+  uint16_t* v = a.v_out + t * a.ld_v + j * 8;
   const int64_t src0 = static_cast<int64_t>(p.page) * 2 * a.c.heads * a.c.page + p.off;
-  for (int r0 = part * kR * kAhead + lane / kB; r0 < rows; r0 += parts * kR * kAhead) {
-    uint2 c[kAhead];
-    uint32_t sc[kAhead];
+  for (int r0 = part * kR * kAhead + lane / kL; r0 < rows; r0 += parts * kR * kAhead) {
+    uint32_t c[kAhead], sc[kAhead];
     float rs[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int r = r0 + i * kR;
-      const int64_t src = src0 + static_cast<int64_t>(r) * a.c.page;
-      c[i] = make_uint2(0u, 0u);  // (a row without a place: zeros)
-      sc[i] = 0u;
+      const int64_t src = src0 + r * a.c.page;
+      c[i] = sc[i] = 0u;  // (a row without a place: zeros)
       rs[i] = 0.0f;
       if (r < rows && found == 0) {
-        c[i] = __ldcs(reinterpret_cast<const uint2*>(a.c.q + src * (D / 2) + j * 8));
-        sc[i] = a.c.bs[src * kB + j];
+        c[i] = __ldcs(reinterpret_cast<const uint32_t*>(a.c.q + src * (D / 2)) + j);
+        sc[i] = a.c.bs[src * (D / kFp4Block) + (j >> 1)];
         rs[i] = a.c.rs[src];
       }
     }
@@ -152,20 +156,16 @@ __global__ void __launch_bounds__(kCThreads) cache_read_kernel(const CacheRowsAr
       if (r >= rows) continue;
       const RowOf ro(r, a.c.heads);
       const uint32_t s2 = e4m3x2_to_f16x2(sc[i] * 0x0101u);
-      uint4* dst = reinterpret_cast<uint4*>((ro.kind ? v : k) + ro.h * D);
+      uint32_t x[4], w[4];
+      e2m1x8_to_f16x2x4(c[i], x);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t x[4], w[4];
-        e2m1x8_to_f16x2x4(e == 0 ? c[i].x : c[i].y, x);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t y = f16x2_mul(x[n], s2);  // exact
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-              : "=r"(w[n])
-              : "f"(__fmul_rn(f16_hi(y), rs[i])), "f"(__fmul_rn(f16_lo(y), rs[i])));
-        }
-        __stcs(dst + e, make_uint4(w[0], w[1], w[2], w[3]));
+      for (int n = 0; n < 4; ++n) {
+        const uint32_t y = f16x2_mul(x[n], s2);  // exact
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+            : "=r"(w[n])
+            : "f"(__fmul_rn(f16_hi(y), rs[i])), "f"(__fmul_rn(f16_lo(y), rs[i])));
       }
+      __stcs(reinterpret_cast<uint4*>((ro.kind ? v : k) + ro.h * D), make_uint4(w[0], w[1], w[2], w[3]));
     }
   }
 }
@@ -194,7 +194,7 @@ cudaError_t launch_cache_write(const CacheRowsArgs& a, cudaStream_t stream) {
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t stream) {
   return launch_rows(a.c.D == 64 ? reinterpret_cast<const void*>(cache_read_kernel<64>)
                                  : reinterpret_cast<const void*>(cache_read_kernel<128>),
-                     4 * 512 / a.c.D, a, stream);
+                     8 * 256 / a.c.D, a, stream);
 }
 
 }  // namespace mtp

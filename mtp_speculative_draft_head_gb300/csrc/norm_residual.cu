@@ -93,15 +93,17 @@ constexpr int max_groups(int tpr, int p) { return tpr * p * 8 / kNormGroup + 2; 
 // multiple of 8. Otherwise pieces follow the arrays' 16-byte boundaries: a row's first and last may
 // be partial, and w, q and the scales' groups are not aligned with them.
 template <int TPR, int P, bool VEC>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(const NormResidualArgs a) {
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 256 && P <= 3 ? (VEC ? 5 : 4) : 1) norm_residual_kernel(const NormResidualArgs a) {
+  // sums of the threads, then (not VEC, group > 0) the groups' maxima [kRows][kMaxGroups]
+  extern __shared__ __align__(16) uint8_t dyn[];
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kWarpsHere = kThreads / 32;
   constexpr int kRows = kThreads / TPR;
   constexpr int kMaxGroups = max_groups(TPR, P);
   static_assert(TPR == 32 || kRows == 1, "a warp or a CTA per row");
-  __shared__ float red[2 * kWarpsHere + 2];
+  __shared__ float red[4];
   __shared__ uint32_t redm[kWarpsHere];
-  extern __shared__ uint32_t gmax[];  // not VEC, group > 0: [kRows][kMaxGroups]
+  float2* sums = reinterpret_cast<float2*>(dyn);  // TPR > 32: [kThreads]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = threadIdx.x % TPR;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
@@ -151,8 +153,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
   }
   if (a.y == nullptr && a.q == nullptr) return;
 
-  // ---- 1 / rms
-  auto sum_squares = [&]() -> DF {
+  // ---- 1 / rms. A CTA's sums go through shared memory to its first warp: adding double-floats across lanes costs a warp as
+  // much as ten elements a lane, so one warp does it for all (and with it the one fp64 reciprocal root of the row).
+  auto sum_squares = [&]() -> DF {  // TPR > 32: of warp 0 only
     DF2 acc{0ull, 0ull};
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -162,66 +165,92 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
         df2_add(acc, f2_mul(f, f));
       }
     DF v = df_add(df2_x(acc), df2_y(acc));
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) v = df_add(v, shfl_xor_df(v, m));
     if constexpr (TPR > 32) {
-      if (lane == 0) {
-        red[2 * warp] = v.hi;
-        red[2 * warp + 1] = v.lo;
-      }
+      sums[threadIdx.x] = make_float2(v.hi, v.lo);
       __syncthreads();
-      v = DF{red[0], red[1]};
-      for (int i = 1; i < kWarpsHere; ++i) v = df_add(v, DF{red[2 * i], red[2 * i + 1]});
+      if (warp == 0) {
+        for (int i = 1; i < kWarpsHere; ++i) {
+          const float2 u = sums[32 * i + lane];
+          v = df_add(v, DF{u.x, u.y});
+        }
+      }
+    }
+    if (TPR == 32 || warp == 0) {
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) v = df_add(v, shfl_xor_df(v, m));
     }
     return v;
   };
+  auto root = [&](const DF& v, double factor2) {  // 1 / sqrt(mean + eps) as two fp32 parts, within an ulp or two of fp64
+    const double ms = (static_cast<double>(v.hi) + static_cast<double>(v.lo)) * a.inv_h;
+    const double r = rsqrt(ms + static_cast<double>(a.eps) * factor2);
+    const float hi = static_cast<float>(r);
+    return make_float2(hi, isinf(hi) ? 0.0f : static_cast<float>(r - static_cast<double>(hi)));
+  };
+  auto ordinary = [](const DF& v) { return v.hi >= 0x1p-100f && v.hi < __int_as_float(0x7f800000); };
   DF tot = sum_squares();
-  double factor2 = 1.0;  // what eps is multiplied by: the square of the row's factor
-  if (!(tot.hi >= 0x1p-100f && tot.hi < __int_as_float(0x7f800000))) {  // (the whole row alike)
-    const bool big = !(tot.hi < 0x1p-100f);
-    const float f = big ? 0x1p-80f : 0x1p80f;
-    factor2 = big ? 0x1p-160 : 0x1p160;
-    uint32_t nan = 0u, inf = 0u;
+  float rh, rl;
+  bool good;
+  if constexpr (TPR == 32) {
+    good = ordinary(tot);
+    const float2 r = root(tot, 1.0);
+    rh = r.x, rl = r.y;
+  } else {
+    if (threadIdx.x == 0) {
+      const float2 r = root(tot, 1.0);
+      red[0] = r.x;
+      red[1] = r.y;
+      red[2] = ordinary(tot) ? 1.0f : 0.0f;
+    }
+    __syncthreads();
+    rh = red[0], rl = red[1];
+    good = red[2] != 0.0f;
+  }
+  if (!good) {  // (the whole row alike) squares beyond fp32, or infinities or NaN among them
+    uint32_t nan = 0u, inf = 0u, top = 0u;
 #pragma unroll
-    for (int i = 0; i < P; ++i)
+    for (int i = 0; i < P; ++i) {
+      top = mag_max(top, make_uint4(s[i][0], s[i][1], s[i][2], s[i][3]));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t lo = s[i][e] & 0x7FFFu, hi = (s[i][e] >> 16) & 0x7FFFu;
         nan |= (lo > 0x7F80u || hi > 0x7F80u) ? 1u : 0u;
         inf |= (lo == 0x7F80u || hi == 0x7F80u) ? 1u : 0u;
-        s[i][e] = scale_pair(s[i][e], f);
       }
-    if constexpr (TPR > 32) __syncthreads();  // red is read by all before it is written again
+    }
+    uint32_t flags = __reduce_or_sync(0xffffffffu, nan | (inf << 1));
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    if constexpr (TPR > 32) {
+      __syncthreads();  // red has been read
+      if (lane == 0) redm[warp] = flags | (top << 2);
+      __syncthreads();
+      flags = 0u, top = 0u;
+      for (int i = 0; i < kWarpsHere; ++i) {
+        flags |= redm[i] & 3u;
+        top = max(top, redm[i] >> 2);
+      }
+    }
+    const bool big = top >= 0x5000u;  // (2^33; squares of smaller rows do not overflow)
+    const float f = big ? 0x1p-80f : 0x1p80f;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = scale_pair(s[i][e], f);
     tot = sum_squares();
-    const uint32_t flags = __reduce_or_sync(0xffffffffu, nan | (inf << 1));
-    uint32_t all = flags;
-    if constexpr (TPR > 32) {
-      if (lane == 0) redm[warp] = flags;
-      __syncthreads();
-      for (int i = 0; i < kWarpsHere; ++i) all |= redm[i];
-      __syncthreads();
-    }
     // an infinity makes the mean infinite (finite columns become 0), a NaN makes it NaN
-    if (all != 0u) tot = DF{__int_as_float((all & 1u) ? 0x7fc00000 : 0x7f800000), 0.0f};
-  }
-  float rh, rl;
-  {
-    double r = 0.0;
-    if (t == 0 || TPR == 32) {
-      // (one fp64 reciprocal root a row, not one a thread: rsqrt is within an ulp or two)
-      const double ms = (static_cast<double>(tot.hi) + static_cast<double>(tot.lo)) * a.inv_h;
-      r = rsqrt(ms + static_cast<double>(a.eps) * factor2);
-    }
-    rh = static_cast<float>(r);
-    rl = isinf(rh) ? 0.0f : static_cast<float>(r - static_cast<double>(rh));
-    if constexpr (TPR > 32) {
-      if (t == 0) {
-        red[2 * kWarpsHere] = rh;
-        red[2 * kWarpsHere + 1] = rl;
+    if (flags != 0u) tot = DF{__int_as_float((flags & 1u) ? 0x7fc00000 : 0x7f800000), 0.0f};
+    const double factor2 = big ? 0x1p-160 : 0x1p160;
+    if constexpr (TPR == 32) {
+      const float2 r = root(tot, factor2);
+      rh = r.x, rl = r.y;
+    } else {
+      if (threadIdx.x == 0) {
+        const float2 r = root(tot, factor2);
+        red[0] = r.x;
+        red[1] = r.y;
       }
       __syncthreads();
-      rh = red[2 * kWarpsHere];
-      rl = red[2 * kWarpsHere + 1];
+      rh = red[0], rl = red[1];
     }
   }
 
@@ -252,12 +281,16 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
   if (a.q == nullptr) return;
 
   // ---- the 8-bit copy
+  // fp32( mx / 448 ), 0 for a NaN or Inf among the columns
+  auto scale_value = [](uint32_t mx) {
+    const float w = bf16_bits_to_f32(mx);
+    if (mx < 0x1000u) return __fdiv_rn(w, 448.0f);  // (below 2^-95)
+    const float q = __fmul_rn(w, 1.0f / 448.0f);    // one step from the product is the rounded quotient (codes.cuh)
+    return mx >= 0x7F80u ? 0.0f : __fmaf_rn(__fmaf_rn(-q, 448.0f, w), 1.0f / 448.0f, q);
+  };
   auto scale_of = [&](uint32_t mx) {
-    if (mx >= 0x7F80u) {  // a NaN or Inf among the columns
-      store_status(a.status, MTP_ERR_NONFINITE);
-      return 0.0f;
-    }
-    return __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+    if (mx >= 0x7F80u) store_status(a.status, MTP_ERR_NONFINITE);
+    return scale_value(mx);
   };
   auto store_codes = [&](int c0, uint2 c) {
     if constexpr (VEC) {
@@ -281,7 +314,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
 #pragma unroll
       for (int i = 0; i < kWarpsHere; ++i) mx = max(mx, redm[i]);
     }
-    const float sc = mx >= 0x7F80u ? 0.0f : __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+    const float sc = scale_value(mx);
     if (t == 0) a.q_scale[row] = scale_of(mx);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -302,7 +335,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
       uint32_t mx = max(m & 0xFFFFu, m >> 16);
 #pragma unroll
       for (int k = 8; k > 0; k >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-      const float sc = mx >= 0x7F80u ? 0.0f : __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+      const float sc = scale_value(mx);
       if (c0 < H) {
         if ((lane & 15) == 0) scales[c0 / kNormGroup] = scale_of(mx);
         store_codes(c0, codes_e4m3x8(s[i], sc));
@@ -310,7 +343,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
     }
   } else {
     // a piece meets at most two groups; the groups' maxima in shared memory
-    uint32_t* gm = gmax + (threadIdx.x / TPR) * kMaxGroups;
+    uint32_t* gm = reinterpret_cast<uint32_t*>(dyn + (TPR > 32 ? kThreads * 8 : 0)) + (threadIdx.x / TPR) * kMaxGroups;
     for (int g = t; g < groups; g += TPR) gm[g] = 0u;
     row_sync();
 #pragma unroll
@@ -333,8 +366,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_residual_kernel(co
     row_sync();
     for (int g = t; g < groups; g += TPR) scales[g] = scale_of(gm[g]);
     auto at_group = [&](int g) {
-      const uint32_t mx = g < groups ? gm[g] : 0u;
-      return mx >= 0x7F80u ? 0.0f : __fdiv_rn(bf16_bits_to_f32(mx), 448.0f);
+      return scale_value(g < groups ? gm[g] : 0u);
     };
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -361,7 +393,7 @@ cudaError_t launch_form(const NormResidualArgs& a, cudaStream_t stream) {
   const void* kern = vec ? reinterpret_cast<const void*>(norm_residual_kernel<TPR, P, true>)
                                   : reinterpret_cast<const void*>(norm_residual_kernel<TPR, P, false>);
   const int rows = kThreads / TPR;
-  const size_t smem = vec || a.group == 0 ? 0 : static_cast<size_t>(rows) * max_groups(TPR, P) * 4;
+  const size_t smem = (TPR > 32 ? kThreads * 8 : 0) + (vec || a.group == 0 ? 0 : static_cast<size_t>(rows) * max_groups(TPR, P) * 4);
   NormResidualArgs p = a;
   void* args[] = {&p};
   return launch_pdl(kern, dim3(static_cast<unsigned>((a.R + rows - 1) / rows)), dim3(kThreads), smem, stream, args);
