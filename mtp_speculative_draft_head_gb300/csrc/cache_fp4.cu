@@ -106,7 +106,13 @@ __global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsA
       BlockCodes o{0u, 0u, 0u};
       if (rs > 0.0f) {
         const float r6 = rs >= kSmallRs ? recip(__fmul_rn(6.0f, rs)) : 0.0f;
-        o = block_codes(u[i][0], u[i][1], rs, __fmul_rn(r6, kUp), __fmul_rn(r6, kDn));
+        const float off = __fmaf_rn(rs, 2688.0f, -bf16_bits_to_f32(mx));  // its sign is that of the scale's rounding
+        if (rs >= kSmallRs && off != 0.0f) {
+          const float side = off > 0.0f ? kDn : kUp;
+          o = block_codes_biased(u[i][0], u[i][1], rs, __fmul_rn(r6, side), side);
+        } else {
+          o = block_codes(u[i][0], u[i][1], rs, __fmul_rn(r6, kUp), __fmul_rn(r6, kDn));
+        }
       }
       const int64_t dst = dst0 + r * a.c.page;
       *reinterpret_cast<uint2*>(a.c.q + dst * (D / 2) + j * 8) = make_uint2(o.c0, o.c1);
@@ -118,10 +124,10 @@ __global__ void __launch_bounds__(kCThreads) cache_write_kernel(const CacheRowsA
 
 // Eight columns a lane: 4 bytes of codes in, 16 bytes out, neighbouring lanes neighbouring columns.
 template <int D>
-__global__ void __launch_bounds__(kCThreads) cache_read_kernel(const CacheRowsArgs a, int parts) {
+__global__ void __launch_bounds__(kCThreads, 6) cache_read_kernel(const CacheRowsArgs a, int parts) {
   constexpr int kL = D / 8;    // lanes of a row
   constexpr int kR = 32 / kL;  // rows of a warp at a time
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 4;
   pdl_wait_prior_grid();
   const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCThreads + threadIdx.x) >> 5;
   const int t = static_cast<int>(wid / parts), part = static_cast<int>(wid % parts);
@@ -194,7 +200,7 @@ cudaError_t launch_cache_write(const CacheRowsArgs& a, cudaStream_t stream) {
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t stream) {
   return launch_rows(a.c.D == 64 ? reinterpret_cast<const void*>(cache_read_kernel<64>)
                                  : reinterpret_cast<const void*>(cache_read_kernel<128>),
-                     8 * 256 / a.c.D, a, stream);
+                     4 * 256 / a.c.D, a, stream);
 }
 
 }  // namespace mtp
