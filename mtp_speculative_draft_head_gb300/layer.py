@@ -71,7 +71,12 @@ class DraftLayer:
             raise _lib.MTPError(int(st.item()), "DraftLayer")
         self.ws_qkv = _lib.linear_fp4_workspace(max_rows, width, self.H, dev)
         self.ws_o = _lib.linear_fp4_workspace(max_rows, self.H, q_heads * self.D, dev)
-        self.ws_step = None
+        self.ws_step = {1: self._step_workspace(1)}  # by the rows of a sequence
+
+    def _step_workspace(self, Q: int):
+        """For steps of Q rows of as many sequences as max_rows and the cache allow."""
+        return _lib.attention_fp4_workspace(min(self.cache.batch, self.max_rows // Q), Q, self.q_heads, self.kv_heads, self.D,
+                                            self.cache.max_len, self.device)
 
     def _project(self, x, status, stream):
         R = x.shape[0]
@@ -101,12 +106,19 @@ class DraftLayer:
     def step(self, x, length, status=None, stream=None):
         """The layer over the next rows of each sequence, in place: x [B Q, H] (Q rows of each of B sequences, the
         first B of the cache), length [B] int32 the tokens that the cache holds with them. Their keys and values are
-        written to the cache first."""
+        written to the cache first. The first step of another Q than 1 makes that Q's workspace and is not recorded into a
+        graph: its zero fill would only run with the graph."""
         B = length.numel()
-        if x.shape[0] % B != 0 or B > self.cache.batch:
+        if B < 1 or x.shape[0] < B or x.shape[0] % B != 0 or B > self.cache.batch:
             raise ValueError("x: an equal number of rows for each sequence of the cache")
         Q = x.shape[0] // B
+        if x.shape[0] > self.max_rows:
+            raise ValueError(f"{x.shape[0]} rows, made for {self.max_rows}")
         with torch.cuda.stream(stream):
+            if Q not in self.ws_step:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError(f"DraftLayer: make one step of {Q} rows before recording one")
+                self.ws_step[Q] = self._step_workspace(Q)
             q, k, v = self._project(x, status, stream)
             starts = torch.arange(0, (B + 1) * Q, Q, dtype=torch.int32, device=self.device)
             first = length - Q
@@ -114,11 +126,8 @@ class DraftLayer:
                 self.rotate(q, k, (first.view(-1, 1) + torch.arange(Q, dtype=torch.int32, device=self.device)).view(-1))
             table = self.cache.table[:B]
             _lib.mtp_head_cache_write_fp4(k, v, starts, first, table, *self.cache.arrays, status, stream)
-            if self.ws_step is None:
-                self.ws_step = _lib.attention_fp4_workspace(min(self.cache.batch, self.max_rows), self.max_rows, self.q_heads,
-                                                            self.kv_heads, self.D, self.cache.max_len, self.device)
             heads = torch.empty((B, Q, self.q_heads, self.D), dtype=torch.bfloat16, device=self.device)
-            _lib.mtp_head_attention_fp4(q.unflatten(0, (B, Q)), *self.cache.arrays, table, length, heads, self.ws_step,
+            _lib.mtp_head_attention_fp4(q.unflatten(0, (B, Q)), *self.cache.arrays, table, length, heads, self.ws_step[Q],
                                         status=status, stream=stream)
             return self._finish(x, heads, status, stream)
 

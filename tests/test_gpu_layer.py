@@ -804,3 +804,27 @@ def test_head_with_a_layer():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, x1)
+
+
+def test_layer_made_for_prompts_steps_too(monkeypatch):
+    """A layer made for the rows of long prompts takes steps of one and of three rows as one made for just those does; a
+    step whose workspace is not there yet is not recorded into a graph."""
+    H, hq, kv, D, B = 128, 4, 2, 64, 2
+    g = gen(42)
+    r = lambda *s: (torch.randn(s, generator=g, device=DEV) * 0.06).bfloat16()  # noqa: E731
+    w = (1 + r(H), r((hq + 2 * kv) * D, H), r(H, hq * D), hq, kv)
+    layers = [m.DraftLayer(*w, m.LayerCache(B, 64, kv, D, page=16, device=DEV), max_rows=n) for n in (2000, B * 3)]
+    n = 0
+    for Q in (1, 3, 1):
+        n += Q
+        x = r(B * Q, H)
+        a, b = (layer.step(x.clone(), i32([n, n])) for layer in layers)
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        layers[1].step(r(8, H), i32([n, n]))
+    with pytest.raises(ValueError):
+        layers[0].step(r(4, H), i32([]))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError):
+        layers[0].step(r(B * 2, H), i32([n + 2, n + 2]))
+    layers[0].step(r(B * 3, H), i32([n + 3, n + 3]))
