@@ -589,9 +589,10 @@ int mtp_head_cache_read_fp4(const uint8_t* q, const uint8_t* block_scale, const 
  *   workspace   at least mtp_head_attention_fp4_workspace_bytes(B, Q, q_heads, kv_heads, D, max_pages *
  *               page) bytes, zero-filled once before its first use (the kernel leaves its counters zero); all
  *               of workspace_bytes may be written. One workspace serves every call of no larger B, Q,
- *               head counts, D and max_pages * page. Two calls that may run at the same time need
- *               different ones.
- *   1 <= Q <= 1024, 1 <= B <= 65536, B * kv_heads * ceil(Q (q_heads / kv_heads) / 16) <= 2^23
+ *               kv_heads, q_heads / kv_heads, D and max_pages * page. Two calls that may run at the
+ *               same time need different ones.
+ *   1 <= Q <= 1024, 1 <= B <= 65536, n = B * kv_heads * ceil(Q (q_heads / kv_heads) / 16) <= 2^23,
+ *   n * ceil(max_pages * page / 128) <= 2^31
  * ---------------------------------------------------------------------------------------- */
 int mtp_head_attention_fp4(const uint16_t* query, int64_t ld_q, const uint8_t* q,
                            const uint8_t* block_scale, const float* row_scale,

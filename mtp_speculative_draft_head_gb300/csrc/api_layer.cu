@@ -103,9 +103,10 @@ bool bad_attention(int B, int Q, int q_heads, int kv_heads, int64_t max_len) {
   if (B < 1 || B > kMaxSequences || Q < 1 || Q > kMaxQueryRows || kv_heads < 1 || kv_heads > kMaxHeads || q_heads < 1 ||
       q_heads > kMaxHeads || q_heads % kv_heads != 0 || max_len < 1 || max_len > kMaxLength)
     return true;
-  // CTAs of a launch: at most 128 ranges of each (sequence, key head, 16 rows)
-  const int64_t groups = (static_cast<int64_t>(Q) * (q_heads / kv_heads) + 15) / 16;
-  return static_cast<int64_t>(B) * kv_heads * groups > (1 << 23);
+  // pieces of work, counted in 32 bits: rounds of 128 tokens for each (sequence, key head, 16 rows)
+  const int64_t groups = (static_cast<int64_t>(Q) * (q_heads / kv_heads) + 15) / 16, rounds = (max_len + 127) / 128;
+  const int64_t pairs = static_cast<int64_t>(B) * kv_heads * groups;
+  return pairs > (1 << 23) || pairs * rounds > (static_cast<int64_t>(1) << 31);
 }
 
 }  // namespace

@@ -417,6 +417,33 @@ def test_attention_long_and_many(B, Q, kv, G, D, lens):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("B,Q,kv,G,D,top", [(100, 1, 8, 2, 64, 700), (70, 3, 4, 4, 128, 900), (3, 1, 1, 1, 128, 100000),
+                                            (33, 1, 2, 1, 64, 300)])
+@pytest.mark.parametrize("some", [False, True])
+def test_attention_work_shared_out(B, Q, kv, G, D, top, some):
+    """Work that the CTAs share out in pieces that end inside sequences, over several of them, or (few long ones) in as many
+    pieces as are joined at once; sequences without rows in front, behind and in runs longer than a warp."""
+    lens = [(top * (i % 7 + 1)) // 7 - i % 5 for i in range(B)]
+    rows = [0 if i < B // 2 or i % 4 == 1 else i % (Q + 1) for i in range(B)] if some else None
+    cache, table = filled(lens, 64, kv, D, 31)
+    q = queries(B, Q, kv * G, D, 32, 1.5)
+    ws = m.attention_fp4_workspace(B, Q, kv * G, kv, D, table.shape[1] * 64, DEV)
+    first = attend(cache, table, lens, q, rows, ws=ws)
+    assert first[2] == 0
+    check_attention(cache, table, lens, q, rows, first[0], first[1], D ** -0.5)
+    again = attend(cache, table, lens, q, rows, ws=ws)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_attention_nothing_to_do():
+    cache, table = filled([20] * 40, 16, 2, 64, 33)
+    q = queries(40, 2, 4, 64, 34)
+    out, lse, st = attend(cache, table, [20] * 40, q, [0] * 40)
+    assert st == 0 and bool((out == 7.0).all()) and bool((lse == 7.0).all())
+    out, lse, st = attend(cache, table, [0] * 40, q)
+    assert st == 0 and not bool(out.any()) and bool((lse == float("-inf")).all())
+
+
 @pytest.mark.parametrize("kind", ["wide", "tiny", "huge", "ties"])
 def test_attention_values_of_any_size(kind):
     """Rows whose sizes differ by many orders of magnitude from token to token, queries to match (scores of order one)."""

@@ -159,6 +159,15 @@ def test_attention_fp4_workspace_serves_smaller_calls(lib):
                     assert 0 < f(b, q, kv, kv, 64, length) <= top
 
 
+def test_attention_fp4_refuses_more_rounds_than_it_counts(lib):
+    """2^31 rounds of 128 tokens over all sequences, key heads and groups of 16 rows."""
+    sizes = dict(spread(ATT), **dict(ATT_SIZES, B=65536, Q=1, hq=8, kv=8, ldq=512, ldo=512, pages=1 << 20, page=128, ws_bytes=0))
+    assert attend(lib, dict(sizes, mp=4096)) == m.ERR_WORKSPACE
+    assert attend(lib, dict(sizes, mp=4097)) == m.ERR_SHAPE
+    f = m.mtp_head_attention_fp4_workspace_bytes
+    assert f(65536, 1, 8, 8, 64, 4096 * 128) > 0 and f(65536, 1, 8, 8, 64, 4097 * 128) == 0
+
+
 PROMPT = ("q", "k", "v", "starts", "out", "lse", "status")
 PROMPT_SIZES = dict(T=9, B=2, hq=6, kv=3, D=64, ldq=384, ldk=192, ldv=200, ldo=392, scale=0.125)
 
