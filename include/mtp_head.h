@@ -577,7 +577,7 @@ int mtp_head_cache_read_fp4(const uint8_t* q, const uint8_t* block_scale, const 
  *   lse      [B, Q, q_heads] fp32      optional: ln sum_j exp(scale q . k_j)
  *   status   [1] int32   optional; MTP_ERR_ARG: a length outside 0 .. max_pages * page or rows outside
  *                        0 .. Q (that sequence's Q rows are zeros, their lse -Inf), or a page outside
- *                        0 .. pages (its tokens are left out); MTP_ERR_TIMEOUT: a wait ran out
+ *                        0 .. pages (its tokens are left out)
  *   cache, block_table, pages, page, max_pages   as above; q_heads a multiple of kv_heads (at most 1024
  *                        each): query head h reads key head h / (q_heads / kv_heads)
  *

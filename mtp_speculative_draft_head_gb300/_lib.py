@@ -582,6 +582,9 @@ def _cache(q, block_scale, row_scale):
 def _rows_of_heads(t, name, shape, dev):
     """The address and row stride of a BF16 tensor [..., heads, head_dim] whose rows may lie apart: its
     heads dense, the rows at equal distances."""
+    if (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr(), shape[-2] * shape[-1]
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if not t.is_cuda:

@@ -193,12 +193,12 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
     const int per_lane = (a.B + 31) / 32, b0 = min(lane * per_lane, a.B), b1 = min(b0 + per_lane, a.B);
     Sequence own{};  // the lane's first
     if (b0 < b1) own = sequence(b0);
-    uint32_t mine = own.rounds * own.groups;
+    uint32_t mine = static_cast<uint32_t>(own.rounds) * own.groups;
     int most = own.rounds;
 #pragma unroll 1
     for (int b = b0 + 1; b < b1; ++b) {
       const Sequence s = sequence(b);
-      mine += s.rounds * s.groups;
+      mine += static_cast<uint32_t>(s.rounds) * s.groups;
       most = max(most, s.rounds);
     }
     const uint32_t heads = a.c.heads;

@@ -17,6 +17,13 @@
 // 32 (w % 4) ..), 8 copies (2-D TMA, 128-byte swizzle), 9 tensor-memory allocation and MMA issue, 10 the next pieces, 11
 // only fills its warpgroup.
 // Every wait is bounded, as in context.cu.
+//
+// Measured at 48 query heads over 8 key heads, D = 128: 8 packed prompts of 16384 rows in all (0.52 TFLOP) 487 us, one prompt of
+// 16384 (3.3 TFLOP) 2.2 ms, 1.5 PFLOP/s; without the softmax, so as products and copies alone, they take 422 us and 1.9 ms. The
+// exponentials of a tile (eight a clock in a quarter of an SM) and its products run one under the other, with what both
+// wait for at a tile's ends on top. Slower: four softmax warpgroups, two threads a row (508 us, 2.33 ms), a second warp that
+// issues MMAs (509, 2.58), the next piece's first scores ahead of the last step (517 and up), a ring of 5 stages (492), 224
+// registers for the softmax (499), sleeping between polls (490).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

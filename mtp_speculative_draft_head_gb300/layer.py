@@ -105,7 +105,7 @@ class DraftLayer:
 
     def step(self, x, length, status=None, stream=None):
         """The layer over the next rows of each sequence, in place: x [B Q, H] (Q rows of each of B sequences, the
-        first B of the cache), length [B] int32 the tokens that the cache holds with them. Their keys and values are
+        first B of the cache), length [B] int32 (Q at least) the tokens that the cache holds with them. Their keys and values are
         written to the cache first. The first step of another Q than 1 makes that Q's workspace and is not recorded into a
         graph: its zero fill would only run with the graph."""
         B = length.numel()
@@ -133,10 +133,11 @@ class DraftLayer:
 
     def prompt(self, x, row_start, status=None, stream=None):
         """The layer over whole prompts, in place: x [T, H], sequence b's rows row_start[b] .. row_start[b + 1]
-        (row_start [B + 1] int32), from its first position on. Their keys and values fill the cache."""
+        (row_start [B + 1] int32), from its first position on. Their keys and values fill the cache. Rows of no sequence
+        attend to nothing."""
         B = row_start.numel() - 1
-        if B > self.cache.batch:
-            raise ValueError("more sequences than the cache has")
+        if B < 1 or B > self.cache.batch:
+            raise ValueError("row_start: one sequence at least, and no more than the cache has")
         with torch.cuda.stream(stream):
             q, k, v = self._project(x, status, stream)
             if self.rotate is not None:
