@@ -8,7 +8,7 @@
 // equal shares of all rounds, one after another: sequences differ in length, and a CTA that starts and one that
 // ends cost about 5 us together, so ranges cut sequence by sequence, in two waves of CTAs, took 93 and 143 us
 // where this takes 82 and 124 (the sizes below). Where it takes no more CTAs, every group of rows begins a share (16
-// instead of 20 us for 7 sequences of up to 5000 tokens). A group's ranges meet in the workspace, where the CTA
+// instead of 20 us for 7 sequences of up to 5000 tokens). Many short groups have CTAs of their own (see Plan). A group's ranges meet in the workspace, where the CTA
 // that finishes last joins them in order.
 //
 // Tokens are the M side of warp-level MMAs (m16n8k16, f16 operands, fp32 sums), rows the N side, eight a
@@ -56,7 +56,9 @@ constexpr int kRowTile = 8;                  // rows of an MMA
 constexpr int kMaxTiles = 2;                 // row tiles of a CTA
 constexpr int kAStages = 2;
 constexpr int kMaxRanges = 128;              // ranges that one sequence is cut into
-constexpr int kMaxCtas = 152 * 5;
+constexpr int kSms = 152;
+constexpr int kMaxCtas = kSms * 5;           // that share rounds out
+constexpr int kLongRange = 4096;
 
 template <int D>
 struct AStage {  // one warp's stage: keys and values of 32 tokens
@@ -84,17 +86,42 @@ struct Groups {
 constexpr int ctas_per_sm(int D, int tiles) { return tiles == 2 ? 3 : D == 64 ? 5 : 4; }
 inline int rows_kept(int Q, int G) { return Q * G < kMaxTiles * kRowTile ? Q * G : kMaxTiles * kRowTile; }
 inline size_t counters_bytes(int64_t pairs) { return (static_cast<size_t>(pairs) * 4 + 255) / 256 * 256; }
-// CTAs of a launch on as many as may run at once: no more than there are rounds.
-inline int ctas_of(int64_t pairs, int64_t max_len, int most) {
-  const int64_t rounds = pairs * ((max_len + kChunkTok - 1) / kChunkTok);
-  return static_cast<int>(rounds < most ? rounds : most);
-}
+// The CTAs of a launch. Either no more than run at once, which share the rounds out: the GPU is evenly busy to the end, but each
+// CTA first sums up all lengths, and groups of rows are cut where shares end. Or one for every range of at most
+// kLongRange tokens of every group: their starts hide under others' work, but the last ones run alone. The latter where there
+// are more groups than CTAs at once, and these too short for their number: us with shares and with ranges for 800 groups
+// of up to 500 tokens 24 and 20, of up to 3000 66 and 68, for 2048 groups of up to 500 61 and 38, 4000 169 and 159, 16000
+// 534 and 557.
+struct Plan {
+  int ctas, splits;  // splits: 0 where CTAs share rounds out, else ranges per group
+  Plan(int64_t pairs, int64_t max_len, int per_sm, int sms) {
+    const int64_t rounds = rounds_of(max_len), room = kSms * per_sm;
+    splits = pairs > room && rounds * room < 16 * pairs ? static_cast<int>(ranges_of(max_len)) : 0;
+    const int at_once = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+    ctas = static_cast<int>(splits > 0 ? pairs * splits : pairs * rounds < at_once ? pairs * rounds : at_once);
+  }
+  size_t parts() const { return splits == 0 ? 2 * static_cast<size_t>(ctas) : splits == 1 ? 0 : static_cast<size_t>(ctas); }
+  static int64_t rounds_of(int64_t max_len) { return (max_len + kChunkTok - 1) / kChunkTok; }
+  static int64_t ranges_of(int64_t max_len) {
+    const int64_t r = (max_len + kLongRange - 1) / kLongRange;
+    return r < kMaxRanges ? r : kMaxRanges;
+  }
+  // No fewer than the parts of any call of no more groups and no larger max_len: with ranges, their number is below
+  // groups / (2 CTAs at once) + 1.
+  static size_t most_parts(int64_t pairs, int64_t max_len) {
+    constexpr int64_t kFewest = kSms * ctas_per_sm(128, kMaxTiles);
+    const int64_t rounds = pairs * rounds_of(max_len), shares = 2 * (rounds < kMaxCtas ? rounds : kMaxCtas);
+    const int64_t ranges = ranges_of(max_len), top = pairs / (2 * kFewest) + 1, splits = ranges < top ? ranges : top;
+    const int64_t cut = pairs > kFewest && splits > 1 ? pairs * splits : 0;
+    return static_cast<size_t>(shares > cut ? shares : cut);
+  }
+};
 
 struct Params {
   AttentionFp4Args a;
-  int groups, kept, G;
-  float* part_o;     // [2 CTAs, kept, D]
-  float* part_stat;  // [2 CTAs, kept, 4]: m, l, m'
+  int groups, kept, G, splits;
+  float* part_o;     // [parts, kept, D]
+  float* part_stat;  // [parts, kept, 4]: m, l, m'
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -161,6 +188,7 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
   __shared__ struct {
     uint32_t share, unit, pos, pos_end;  // in rounds of the whole call
     uint32_t at, each, pair_at;          // sequence b's first, a group's number of them, this group's first
+    uint32_t cta0;                       // the CTA whose share begins with round 0
     int b, groups, h, grp, nrows, round1, active;
   } now_s;
   const AttentionFp4Args& a = p.a;
@@ -189,78 +217,104 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
     now_s.each = each;
     if (s.bad) store_status(a.status, MTP_ERR_ARG);
   };
-  if (warp == 0) {
-    const int per_lane = (a.B + 31) / 32, b0 = min(lane * per_lane, a.B), b1 = min(b0 + per_lane, a.B);
-    Sequence own{};  // the lane's first
-    if (b0 < b1) own = sequence(b0);
-    uint32_t mine = static_cast<uint32_t>(own.rounds) * own.groups;
-    int most = own.rounds;
-#pragma unroll 1
-    for (int b = b0 + 1; b < b1; ++b) {
-      const Sequence s = sequence(b);
-      mine += static_cast<uint32_t>(s.rounds) * s.groups;
-      most = max(most, s.rounds);
-    }
-    const uint32_t heads = a.c.heads;
-    // no sequence in more than kMaxRanges pieces, the two that are cut off at its ends among them
-    const uint32_t share = max((__reduce_add_sync(0xffffffffu, mine) * heads + gridDim.x - 1) / gridDim.x,
-                               (__reduce_max_sync(0xffffffffu, most) + kMaxRanges - 2u) / (kMaxRanges - 1u));
-    // whole shares for every group, where that takes no more CTAs
-    const uint32_t own_pieces = (own.rounds + share - 1) / share;
-    uint32_t pieces = own_pieces * own.groups, unit = 1, own_each = own.rounds;
-#pragma unroll 1
-    for (int b = b0 + 1; b < b1; ++b) {
-      const Sequence s = sequence(b);
-      pieces += (s.rounds + share - 1) / share * s.groups;
-    }
-    if (__reduce_add_sync(0xffffffffu, min(pieces, 4096u)) * heads <= gridDim.x) {
-      unit = share;
-      own_each = own_pieces * share;
-      mine = pieces * share;
-    }
-    mine *= heads;
-    uint32_t upto = mine;
-#pragma unroll 1
-    for (int k = 1; k < 32; k *= 2) {
-      const uint32_t other = __shfl_up_sync(0xffffffffu, upto, k);
-      if (lane >= k) upto += other;
-    }
-    const uint32_t pos = share * blockIdx.x;
-    if (lane == 31) {
+  int b;
+  uint32_t pos, pos_end, at, each;  // (of now_s)
+  Sequence seq;
+  if (p.splits > 0) {
+    const uint32_t sp = blockIdx.x % p.splits, pair = blockIdx.x / p.splits;
+    const int row_group = static_cast<int>(pair % p.groups), head = static_cast<int>(pair / p.groups % a.c.heads);
+    b = static_cast<int>(pair / p.groups / a.c.heads);
+    seq = sequence(b);
+    const uint32_t share = (seq.rounds + p.splits - 1u) / p.splits;
+    each = (seq.rounds + share - 1) / share * share;
+    if (row_group >= seq.groups || sp * share >= each) return;
+    pos = (head * seq.groups + row_group) * each + sp * share;
+    pos_end = pos + share;
+    at = 0;
+    if (threadIdx.x == 0) {
       now_s.share = share;
-      now_s.unit = unit;
       now_s.pos = pos;
-      now_s.pos_end = min(pos + share, upto);
-      now_s.b = -1;  // (no share: it stays so)
-    }
-    __syncwarp();
-    if (upto > pos && upto - mine <= pos) {
-      uint32_t at = upto - mine, each = own_each;
-      int b = b0;
-#pragma unroll 1
-      while (pos >= at + each * own.groups * heads && b + 1 < b1) {
-        at += each * own.groups * heads;
-        own = sequence(++b);
-        each = (own.rounds + unit - 1) / unit * unit;
-      }
+      now_s.pos_end = pos_end;
       now_s.at = at;
-      set_sequence(b, own, each);
+      now_s.cta0 = blockIdx.x - pos / share;
+      set_sequence(b, seq, each);
     }
+  } else {
+    if (warp == 0) {
+      const int per_lane = (a.B + 31) / 32, b0 = min(lane * per_lane, a.B), b1 = min(b0 + per_lane, a.B);
+      Sequence own{};  // the lane's first
+      if (b0 < b1) own = sequence(b0);
+      uint32_t mine = static_cast<uint32_t>(own.rounds) * own.groups;
+      int most = own.rounds;
+#pragma unroll 1
+      for (int b = b0 + 1; b < b1; ++b) {
+        const Sequence s = sequence(b);
+        mine += static_cast<uint32_t>(s.rounds) * s.groups;
+        most = max(most, s.rounds);
+      }
+      const uint32_t heads = a.c.heads;
+      // no sequence in more than kMaxRanges pieces, the two that are cut off at its ends among them
+      const uint32_t share = max((__reduce_add_sync(0xffffffffu, mine) * heads + gridDim.x - 1) / gridDim.x,
+                                 (__reduce_max_sync(0xffffffffu, most) + kMaxRanges - 2u) / (kMaxRanges - 1u));
+      // whole shares for every group, where that takes no more CTAs
+      const uint32_t own_pieces = (own.rounds + share - 1) / share;
+      uint32_t pieces = own_pieces * own.groups, unit = 1, own_each = own.rounds;
+#pragma unroll 1
+      for (int b = b0 + 1; b < b1; ++b) {
+        const Sequence s = sequence(b);
+        pieces += (s.rounds + share - 1) / share * s.groups;
+      }
+      if (__reduce_add_sync(0xffffffffu, min(pieces, 4096u)) * heads <= gridDim.x) {
+        unit = share;
+        own_each = own_pieces * share;
+        mine = pieces * share;
+      }
+      mine *= heads;
+      uint32_t upto = mine;
+#pragma unroll 1
+      for (int k = 1; k < 32; k *= 2) {
+        const uint32_t other = __shfl_up_sync(0xffffffffu, upto, k);
+        if (lane >= k) upto += other;
+      }
+      const uint32_t pos = share * blockIdx.x;
+      if (lane == 31) {
+        now_s.share = share;
+        now_s.unit = unit;
+        now_s.pos = pos;
+        now_s.pos_end = min(pos + share, upto);
+        now_s.cta0 = 0;
+        now_s.b = -1;  // (no share: it stays so)
+      }
+      __syncwarp();
+      if (upto > pos && upto - mine <= pos) {
+        uint32_t at = upto - mine, each = own_each;
+        int b = b0;
+#pragma unroll 1
+        while (pos >= at + each * own.groups * heads && b + 1 < b1) {
+          at += each * own.groups * heads;
+          own = sequence(++b);
+          each = (own.rounds + unit - 1) / unit * unit;
+        }
+        now_s.at = at;
+        set_sequence(b, own, each);
+      }
+    }
+    __syncthreads();
+    b = now_s.b;
+    if (b < 0) return;  // no share
+    pos = now_s.pos, pos_end = now_s.pos_end, at = now_s.at, each = now_s.each;
+    seq = sequence(b);
   }
-  __syncthreads();
-  if (now_s.b < 0) return;  // no share
 
   while (true) {
-    const int b = now_s.b;
-    const Sequence seq = sequence(b);
     const int n = seq.n, len = seq.len;
-    const uint32_t pair_b = (now_s.pos - now_s.at) / now_s.each, pair_at = now_s.at + pair_b * now_s.each;
+    const uint32_t pair_b = (pos - at) / each, pair_at = at + pair_b * each;
     const int h = static_cast<int>(pair_b) / seq.groups, grp = static_cast<int>(pair_b) % seq.groups;
     const int r0 = grp * kRows;
     const int nrows = min(n * p.G - r0, kRows);  // rows of this CTA
     const int seen = max(len - n + (r0 + nrows - 1) / p.G + 1, 0);  // tokens that its last row sees
-    const int begin = static_cast<int>(now_s.pos - pair_at) * kChunkTok;
-    const uint32_t round1 = min(now_s.each, now_s.pos_end - pair_at);
+    const int begin = static_cast<int>(pos - pair_at) * kChunkTok;
+    const uint32_t round1 = min(each, pos_end - pair_at);
     const int end = min(seen, min(static_cast<int>(round1), seq.rounds) * kChunkTok);
 
     // ---- copies: a warp's steps into its own ring
@@ -335,7 +389,7 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
       now_s.grp = grp;
       now_s.nrows = nrows;
       now_s.round1 = round1;
-      now_s.active = static_cast<int>((pair_at + now_s.each - 1) / now_s.share - pair_at / now_s.share) + 1;
+      now_s.active = static_cast<int>((pair_at + each - 1) / now_s.share - pair_at / now_s.share) + 1;
     }
 
     // ---- queries: row g of each tile as an f16 operand
@@ -672,7 +726,7 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
         v.w += u.w * k;
       }
     };
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (now_s.pos > now_s.share * blockIdx.x ? 1 : 0);
+    const int64_t slot = p.splits > 0 ? blockIdx.x : 2 * static_cast<int64_t>(blockIdx.x) + (now_s.pos > now_s.share * blockIdx.x ? 1 : 0);
     float* merge = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -735,10 +789,10 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
     }
     float4* stat = reinterpret_cast<float4*>(smem);  // [active][8]
     // the first range ends its CTA's share, and is that CTA's second unless it begins it too; the others begin theirs
-    const uint32_t cta0 = now_s.pair_at / now_s.share;
-    auto slot_of = [&](int s) {
-      return static_cast<int64_t>(2 * (cta0 + s) + (s == 0 && now_s.pair_at > cta0 * now_s.share ? 1 : 0));
-    };
+    const uint32_t first_cta = now_s.cta0 + now_s.pair_at / now_s.share;
+    const int64_t slot0 = p.splits > 0 ? first_cta : 2 * static_cast<int64_t>(first_cta);
+    const bool second = now_s.pair_at % now_s.share != 0u;
+    auto slot_of = [&](int s) { return p.splits > 0 ? slot0 + s : slot0 + 2 * s + (s == 0 && second ? 1 : 0); };
     for (int nt = 0; last && nt * kRowTile < rows_here; ++nt) {
       const int here = min(rows_here - nt * kRowTile, kRowTile);
       __syncthreads();
@@ -767,7 +821,7 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
     }
 
     // ---- on to the next group of rows, key head or sequence
-    const uint32_t pos = now_s.pair_at + now_s.round1;
+    pos = now_s.pair_at + now_s.round1;
     if (pos >= now_s.pos_end) return;
     __syncthreads();  // shared memory has been read
     if (warp == 0) {
@@ -796,7 +850,10 @@ __global__ void __launch_bounds__(kAThreads, ctas_per_sm(D, NT)) attention_fp4_k
       }
     }
     __syncthreads();
-    if (now_s.b < 0) return;  // (there is another with rows: pos_end is not behind the last)
+    b = now_s.b;
+    if (b < 0) return;  // (there is another with rows: pos_end is not behind the last)
+    pos_end = now_s.pos_end, at = now_s.at, each = now_s.each;
+    seq = sequence(b);
   }
 }
 
@@ -813,8 +870,7 @@ const void* kernel_of(int tiles) {
 size_t attention_fp4_workspace_bytes(int B, int Q, int q_heads, int kv_heads, int D, int64_t max_len) {
   const int G = q_heads / kv_heads;
   const int64_t pairs = static_cast<int64_t>(B) * kv_heads * Groups(Q, G).groups;
-  return counters_bytes(pairs) +
-         2 * static_cast<size_t>(ctas_of(pairs, max_len, kMaxCtas)) * rows_kept(Q, G) * (static_cast<size_t>(D) + 4) * 4;
+  return counters_bytes(pairs) + Plan::most_parts(pairs, max_len) * rows_kept(Q, G) * (static_cast<size_t>(D) + 4) * 4;
 }
 
 cudaError_t launch_attention_fp4(const AttentionFp4Args& a, cudaStream_t stream) {
@@ -827,15 +883,15 @@ cudaError_t launch_attention_fp4(const AttentionFp4Args& a, cudaStream_t stream)
   const Groups g(a.Q, p.G);
   p.groups = g.groups;
   p.kept = rows_kept(a.Q, p.G);
-  const int room = di.sm_count * ctas_per_sm(a.c.D, g.tiles);
-  const int ctas = ctas_of(static_cast<int64_t>(a.B) * a.c.heads * g.groups, static_cast<int64_t>(a.max_pages) * a.c.page,
-                           room < kMaxCtas ? room : kMaxCtas);
-  const size_t kept_rows = 2 * static_cast<size_t>(ctas) * p.kept;
+  const Plan plan(static_cast<int64_t>(a.B) * a.c.heads * g.groups, static_cast<int64_t>(a.max_pages) * a.c.page,
+                  ctas_per_sm(a.c.D, g.tiles), di.sm_count);
+  p.splits = plan.splits;
+  const size_t kept_rows = plan.parts() * p.kept;
   p.part_o = reinterpret_cast<float*>(a.ws + (a.ws_bytes / 16 * 16 - kept_rows * (a.c.D + 4) * 4));
   p.part_stat = p.part_o + kept_rows * a.c.D;
   void* args[] = {&p};
-  return launch_pdl(a.c.D == 64 ? kernel_of<64>(g.tiles) : kernel_of<128>(g.tiles), dim3(static_cast<unsigned>(ctas)), dim3(kAThreads),
-                    a.c.D == 64 ? AStage<64>::kSmem : AStage<128>::kSmem, stream, args);
+  return launch_pdl(a.c.D == 64 ? kernel_of<64>(g.tiles) : kernel_of<128>(g.tiles), dim3(static_cast<unsigned>(plan.ctas)),
+                    dim3(kAThreads), a.c.D == 64 ? AStage<64>::kSmem : AStage<128>::kSmem, stream, args);
 }
 
 }  // namespace mtp

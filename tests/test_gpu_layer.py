@@ -418,11 +418,12 @@ def test_attention_long_and_many(B, Q, kv, G, D, lens):
 
 
 @pytest.mark.parametrize("B,Q,kv,G,D,top", [(100, 1, 8, 2, 64, 700), (70, 3, 4, 4, 128, 900), (3, 1, 1, 1, 128, 100000),
-                                            (33, 1, 2, 1, 64, 300)])
+                                            (33, 1, 2, 1, 64, 300), (1500, 1, 1, 1, 64, 260), (200, 1, 8, 1, 64, 4200)])
 @pytest.mark.parametrize("some", [False, True])
 def test_attention_work_shared_out(B, Q, kv, G, D, top, some):
     """Work that the CTAs share out in pieces that end inside sequences, over several of them, or (few long ones) in as many
-    pieces as are joined at once; sequences without rows in front, behind and in runs longer than a warp."""
+    pieces as are joined at once, and work of so many sequences that each has its own; sequences without rows in front, behind
+    and in runs longer than a warp."""
     lens = [(top * (i % 7 + 1)) // 7 - i % 5 for i in range(B)]
     rows = [0 if i < B // 2 or i % 4 == 1 else i % (Q + 1) for i in range(B)] if some else None
     cache, table = filled(lens, 64, kv, D, 31)
