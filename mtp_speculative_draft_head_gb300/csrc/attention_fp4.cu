@@ -8,8 +8,8 @@
 // equal shares of all rounds, one after another: sequences differ in length, and a CTA that starts and one that
 // ends cost about 5 us together, so ranges cut sequence by sequence, in two waves of CTAs, took 93 and 143 us
 // where this takes 82 and 124 (the sizes below). Where it takes no more CTAs, every group of rows begins a share (16
-// instead of 20 us for 7 sequences of up to 5000 tokens). Many short groups have CTAs of their own (see Plan). A group's ranges meet in the workspace, where the CTA
-// that finishes last joins them in order.
+// instead of 20 us for 7 sequences of up to 5000 tokens). Many short groups, and a few very short ones, have CTAs of
+// their own (see Plan). A group's ranges meet in the workspace, where the CTA that finishes last joins them in order.
 //
 // Tokens are the M side of warp-level MMAs (m16n8k16, f16 operands, fp32 sums), rows the N side, eight a
 // tile: S^T = K Q^T, then O^T += V^T P^T with P^T out of S^T by a transposition within the warp. A step of one
@@ -30,7 +30,7 @@
 // took more instructions: their operands go through uniform registers, one lane after another.)
 //
 // Measured at 8 key heads of 6 query heads, D = 128: one row of each of 16 sequences of up to 32768 tokens (369 MB) 82 us,
-// 4.5 TB/s; five rows of each of 16 of up to 16384 (186 MB) 124 us; one sequence of 2048 tokens 15 us. Instructions
+// 4.5 TB/s; five rows of each of 16 of up to 16384 (186 MB) 124 us; one sequence of 2048 tokens 14 us. Instructions
 // bound it, not memory: a lane's word of eight codes with its conversions, scales and one row tile's MMA takes 18 cycles of an
 // SM's quarter, and a second tile of rows 8 more. Four row tiles a warp left too few warps (180 us for the five rows);
 // wide operands in shared memory for the larger tensor-core instructions took longer to write than they saved (187 us).
@@ -91,13 +91,18 @@ inline size_t counters_bytes(int64_t pairs) { return (static_cast<size_t>(pairs)
 // kLongRange tokens of every group: their starts hide under others' work, but the last ones run alone. The latter where there
 // are more groups than CTAs at once, and these too short for their number: us with shares and with ranges for 800 groups
 // of up to 500 tokens 24 and 20, of up to 3000 66 and 68, for 2048 groups of up to 500 61 and 38, 4000 169 and 159, 16000
-// 534 and 557.
+// 534 and 557. Or, where the whole call is no more than a round a CTA, one for every round (8 groups of 2048 tokens: 13.9 us,
+// 14.8 in shares).
 struct Plan {
   int ctas, splits;  // splits: 0 where CTAs share rounds out, else ranges per group
   Plan(int64_t pairs, int64_t max_len, int per_sm, int sms) {
     const int64_t rounds = rounds_of(max_len), room = kSms * per_sm;
-    splits = pairs > room && rounds * room < 16 * pairs ? static_cast<int>(ranges_of(max_len)) : 0;
     const int at_once = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+    splits = 0;
+    if (pairs * rounds <= at_once && rounds <= kMaxRanges)
+      splits = static_cast<int>(rounds);
+    else if (pairs > room && rounds * room < 16 * pairs)
+      splits = static_cast<int>(ranges_of(max_len));
     ctas = static_cast<int>(splits > 0 ? pairs * splits : pairs * rounds < at_once ? pairs * rounds : at_once);
   }
   size_t parts() const { return splits == 0 ? 2 * static_cast<size_t>(ctas) : splits == 1 ? 0 : static_cast<size_t>(ctas); }
@@ -107,7 +112,7 @@ struct Plan {
     return r < kMaxRanges ? r : kMaxRanges;
   }
   // No fewer than the parts of any call of no more groups and no larger max_len: with ranges, their number is below
-  // groups / (2 CTAs at once) + 1.
+  // groups / (2 CTAs at once) + 1; with a CTA a round there is a part for each, half of what shares take.
   static size_t most_parts(int64_t pairs, int64_t max_len) {
     constexpr int64_t kFewest = kSms * ctas_per_sm(128, kMaxTiles);
     const int64_t rounds = pairs * rounds_of(max_len), shares = 2 * (rounds < kMaxCtas ? rounds : kMaxCtas);
