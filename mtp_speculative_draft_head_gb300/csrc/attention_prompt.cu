@@ -186,7 +186,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int4* answer = reinterpret_cast<int4*>(full + TL::kBars);
   int4* work = answer + 1;             // [2]: first row of the sequence, its rows (0: no more work), pair of tiles, head
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(work + 2);
-  int* unusual = reinterpret_cast<int*>(tmem_slot + 1);  // [2]: a tile's own values hold infinities or NaN
+  // [4][2]: the piece (count + 1) in which a tile's own values last held infinities or NaN. A piece has the pair count & 3:
+  // no warp takes piece c + 4 before every warp has taken c + 2, and so has read the pair for c.
+  int* unusual = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -200,11 +202,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(smem_addr(&s_full[i]), 1);
       mbar_init(smem_addr(&p_full[i]), kTile);
       mbar_init(smem_addr(&p_full[2 + i]), kTile);
-      mbar_init(smem_addr(&o_full[i]), 1);
+      mbar_init(smem_addr(&o_full[i]), 2);  // the products, and the warp that has seen all weights come
       mbar_init(smem_addr(&work_full[i]), 1);
       mbar_init(smem_addr(&work_empty[i]), 10);  // the warps that work
-      unusual[i] = 0;
     }
+    for (int i = 0; i < 8; ++i) unusual[i] = 0;
     mbar_init(smem_addr(asked), 1);
     mbar_init(smem_addr(done), 1);
     fence_barrier_init();
@@ -406,6 +408,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
               if (j + 2 == of[tile]) commit(&q_empty[tile]);
             } else {
               commit(&o_full[tile]);
+              if (lead) mbar_arrive(smem_addr(&o_full[tile]));  // (with it the marks that came with the weights are seen)
+              __syncwarp();
             }
           }
           if (!ok) break;
@@ -456,8 +460,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (e > (row & 31)) s[k + e] = 0xFF800000u;
             }
           // A zero weight must not carry an infinity or a NaN of a row that is not seen into the sums: rows of V
-          // behind the sequence become zeros here, and so do such elements of the tile's own rows, which the
-          // epilogue gives back to the rows that see them.
+          // behind the sequence become zeros here, and so do such elements of the tile's own rows. The epilogue gives
+          // them back to the rows that see them: those of this tile, and of tile 1, whose products read tile 0's rows after this.
           const int left = w.n - i0, iv = base + 2 * j + 1;
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&full[iv % kStages]), static_cast<uint32_t>((iv / kStages) & 1)));
           if (!ok) break;
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 v[x] = make_uint4(0u, 0u, 0u, 0u);
               } else if (inf != 0u) {
                 v[x] = make_uint4(u.x & ~nonfinite(u.x), u.y & ~nonfinite(u.y), u.z & ~nonfinite(u.z), u.w & ~nonfinite(u.w));
-                unusual[tile] = 1;
+                unusual[2 * (count & 3) + tile] = count + 1;
               }
             }
             fence_proxy_async_smem();
@@ -544,15 +548,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
       uint16_t* dst = p.out + r * p.ld_out + w.h * D;
       named_barrier_sync(1 + tile, kTile);
-      const bool add = *reinterpret_cast<volatile int*>(&unusual[tile]) != 0;
+      const volatile int* marks = unusual + 2 * (count & 3);
+      // places in the tile of the rows whose elements were taken out and that this row sees
+      const int add0 = tile == 1 && marks[0] == count + 1 ? -kTile : 0, add1 = marks[tile] == count + 1 ? row + 1 : 0;
 #pragma unroll
       for (int k = 0; k < D; k += 32) {
         uint32_t o[32];
+        __syncwarp();  // (its rows went through loops of their own lengths)
         tmem_ld32_async(o_t + k, o);
         tmem_wait_ld();
         tmem_arrived(o);
-        if (in && add) {
-          for (int x = 0; x <= row; ++x) {
+        if (in) {
+          for (int x = add0; x < add1; ++x) {
             const uint16_t* v = p.v + (static_cast<int64_t>(w.s0) + i0 + x) * p.ld_v + w.h / p.G * D + k;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -576,11 +583,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       if (in && p.lse != nullptr)
         p.lse[r * p.q_heads + w.h] = l > 0.0f || l != l ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
-      if (add) {  // all have read the flag; it is down before one of them may raise it for the next piece
-        named_barrier_sync(1 + tile, kTile);
-        if (row == 0) unusual[tile] = 0;
-        named_barrier_sync(1 + tile, kTile);
-      }
     }
     if (!ok && lane == 0) give_up();
   }

@@ -1,0 +1,88 @@
+"""The attention half's operators where values, scales, streams and waits are out of the ordinary."""
+import numpy as np
+import pytest
+import torch
+
+import mtp_speculative_draft_head_gb300 as m
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, I32, F32, F64 = torch.bfloat16, torch.int32, torch.float32, torch.float64
+INF, NAN = float("inf"), float("nan")
+
+
+def i32(v):
+    return torch.tensor(v, dtype=I32, device=DEV)
+
+
+def status():
+    return torch.zeros(1, dtype=I32, device=DEV)
+
+
+def gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+# ------------------------------------------------------------------------------------- prompts
+def prompt(q, k, v, starts, st=None):
+    out = torch.full(q.shape, 7.0, dtype=BF, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    m.mtp_head_attention_prompt(q, k, v, i32(starts), out, lse, status=st)
+    return out, lse
+
+
+def with_values_planted(starts, good, v, plant):
+    """What the outputs `good` become when the elements {(row, key head, column): value} of v are infinite or NaN: a row that
+    sees infinities of one sign has them, one that sees a NaN or both signs has a NaN, and every other element stays."""
+    G = good.shape[1] // v.shape[1]
+    want = good.clone()
+    for (row, h, c), x in plant.items():
+        end = next(b for a, b in zip(starts[:-1], starts[1:]) if a <= row < b)
+        part = want[row:end, h * G:(h + 1) * G, c]
+        part.copy_(torch.where(torch.isfinite(part), torch.tensor(x, dtype=BF, device=DEV), part + x))
+    return want
+
+
+def same(a, b):
+    return bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [{0: INF, 5: NAN, 127: -INF}, {300: INF, 310: NAN}, {5: INF, 130: -INF, 255: NAN, 256: INF, 599: INF}])
+def test_prompt_carries_infinities_and_nan_of_every_place(D, rows):
+    """Non-finite values in the first and in the second 128 rows of each 256: every later row of the sequence has them, those
+    of the second 128 as well, whose products read the rows of the first after these were cleared."""
+    starts = [3, 303, 903, 1159]
+    g = gen(D)
+    q, k, v = (torch.randn((1164, n, D), generator=g, device=DEV).bfloat16() for n in (4, 2, 2))
+    good, good_lse = prompt(q, k, v, starts)
+    plant = {}
+    for s, (a, b) in enumerate(zip(starts[:-1], starts[1:])):
+        for i, (r, x) in enumerate(rows.items()):
+            if a + r < b:
+                plant[a + r, (s + i) % 2, (7 * i + 13 * s) % D] = x
+                plant[a + r, (s + i) % 2, D - 1] = x  # (a column where several meet)
+    for (r, h, c), x in plant.items():
+        v[r, h, c] = x
+    out, lse = prompt(q, k, v, starts)
+    assert same(out, with_values_planted(starts, good, v, plant))
+    assert torch.equal(lse, good_lse)
+
+
+def test_prompt_marks_of_one_piece_do_not_reach_the_next():
+    """Thousands of short pieces, one after another in the same CTAs, every third with an infinity among its values: one
+    and two tiles long by turns."""
+    lens = [(1, 100, 128, 129, 200, 256)[(i * i + i // 7) % 6] for i in range(600)]
+    starts = np.concatenate(([0], np.cumsum(lens))).tolist()
+    g = gen(3)
+    q, k, v = (torch.randn((starts[-1], n, 64), generator=g, device=DEV).bfloat16() for n in (4, 4, 4))
+    good, _ = prompt(q, k, v, starts)
+    plant = {}
+    for i, a in enumerate(starts[:-1]):
+        if i % 3 == 0:
+            plant[a + (37 * i) % lens[i], i % 4, i % 64] = INF if i % 2 else NAN
+    for (r, h, c), x in plant.items():
+        v[r, h, c] = x
+    want = with_values_planted(starts, good, v, plant)
+    for _ in range(5):
+        assert same(prompt(q, k, v, starts)[0], want)
