@@ -16,7 +16,8 @@
 // Warp roles: 0..3 and 4..7 softmax and epilogue of tile 0 and 1 (warp w reads TMEM lanes
 // 32 (w % 4) ..), 8 copies (2-D TMA, 128-byte swizzle), 9 tensor-memory allocation and MMA issue, 10 the next pieces, 11
 // only fills its warpgroup.
-// Every wait is bounded, as in context.cu.
+// Every wait is bounded, as in context.cu. A warp decides alone when it gives up, so between the start and the end of
+// the kernel nothing but these bounded waits joins several warps: no barrier of a warpgroup, which has no limit.
 //
 // Measured at 48 query heads over 8 key heads, D = 128: 8 packed prompts of 16384 rows in all (0.52 TFLOP) 487 us, one prompt of
 // 16384 (3.3 TFLOP) 2.2 ms, 1.5 PFLOP/s; without the softmax, so as products and copies alone, they take 422 us and 1.9 ms. The
@@ -547,7 +548,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int64_t r = static_cast<int64_t>(w.s0) + i0 + row;
       const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
       uint16_t* dst = p.out + r * p.ld_out + w.h * D;
-      named_barrier_sync(1 + tile, kTile);
       const volatile int* marks = unusual + 2 * (count & 3);
       // places in the tile of the rows whose elements were taken out and that this row sees
       const int add0 = tile == 1 && marks[0] == count + 1 ? -kTile : 0, add1 = marks[tile] == count + 1 ? row + 1 : 0;

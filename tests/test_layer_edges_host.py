@@ -1,0 +1,22 @@
+"""Properties of the attention half's sources, refusals and bookkeeping that need no GPU."""
+import os
+import re
+
+from mtp_speculative_draft_head_gb300 import build
+
+
+def source(name):
+    with open(os.path.join(build.CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_prompt_kernel_joins_its_warps_by_bounded_waits_only():
+    """A warp that gives up leaves its role at once: a barrier of several warps in front of the kernel's last one would hold
+    the others for ever. The whole CTA's barrier stands at the start and at the end, outside of every role."""
+    text = source("attention_prompt.cu")
+    assert "named_barrier" not in text and "bar.sync" not in text and "barrier.sync" not in text
+    kernel = text.split("attention_prompt_kernel(const __grid_constant__")[1].split("bool encode_rows")[0]
+    roles = kernel.index("if (warp >= 8) {"), kernel.rindex("give_up();")
+    at = [i.start() for i in re.finditer(r"__syncthreads\(\)", kernel)]
+    assert len(at) == 2 and at[0] < roles[0] and at[1] > roles[1]
+    assert "mbar_try_wait" not in kernel  # (mbar_wait_bounded alone)
