@@ -510,7 +510,7 @@ int mtp_head_verify(const float* target_probs, const float* draft_probs,
  * a paged cache of keys and values in four bits, attention over it for a step's rows, and attention
  * over whole prompts. In all of them an output or a workspace on an input that is still read, or on
  * another output, is MTP_ERR_ARG, but for what is stated. Their kernels wait for
- * their own copies and products only, 2 s at most.
+ * their own copies and products only, 2 s at most (the prompt attention: mtp_head_set_wait_limit_ns).
  *
  * Residual norm. For each of R rows of H columns:
  *   total = bf16( x + delta )              the real sum rounded once; x itself when delta is NULL
@@ -635,8 +635,8 @@ int mtp_head_attention_prompt(const uint16_t* q, int64_t ld_q, const uint16_t* k
  * never hang the GPU). Past the limit the kernel stores MTP_ERR_TIMEOUT in `status`, lets its own
  * copies in flight land, and returns; the draft and logits of that call are then undefined, and
  * the workspace is left ready for the next call. Default 2 s (2000000000 ns), far above any
- * real wait. The limit applies to the output-stage kernels (every batch size) and to the
- * single-sequence input stage, launched after this call (a CUDA graph keeps the limit it was
+ * real wait. The limit applies to the output-stage kernels (every batch size), to the
+ * single-sequence input stage and to the prompt attention, launched after this call (a CUDA graph keeps the limit it was
  * recorded with); the batched input stage, the context-row kernels and the FP4 linear always use 2 s, and so
  * does every wait for a kernel's own copies before it exits. Process-wide; returns the previous
  * limit. A short limit (a few ns: the device clock it is compared with advances about once a

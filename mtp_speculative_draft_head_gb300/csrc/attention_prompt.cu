@@ -66,6 +66,7 @@ struct PromptParams {
   int64_t ld_out;
   int T, B, q_heads, G, D;
   float c;  // scale * log2(e)
+  unsigned long long wait_ns;  // give-up time of the waits, but for those for the kernel's own copies and products at its end
 };
 
 // ------------------------------------------------------------------------------- PTX
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   };
   auto next_piece = [&](int count, bool& ok) {
     const int i = count & 1;
-    ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&work_full[i]), static_cast<uint32_t>((count >> 1) & 1)));
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&work_full[i]), static_cast<uint32_t>((count >> 1) & 1), p.wait_ns));
     Piece w{0, 0, 0, 0, 0, 0};
     if (!ok) return w;
     const int4 v = *const_cast<const int4*>(&work[i]);
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (more) w = find_work(p, item);
         if (more && w.y == 0) more = false;  // (pieces in front of the last sequence's end all exist)
         const int i = count & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&work_empty[i]), static_cast<uint32_t>(((count >> 1) & 1) ^ 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&work_empty[i]), static_cast<uint32_t>(((count >> 1) & 1) ^ 1), p.wait_ns));
         if (!ok) break;
         if (lane == 0) {
           work[i] = w;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
               : "memory");
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(asked), turn));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(asked), turn, p.wait_ns));
         turn ^= 1u;
         if (!ok) break;
         uint32_t got, x;
@@ -304,14 +305,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
       auto next = [&](const CUtensorMap* map, int x, int y) {
         if (!ok) return;
         const int s = used % kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[s]), static_cast<uint32_t>(((used / kStages) & 1) ^ 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[s]), static_cast<uint32_t>(((used / kStages) & 1) ^ 1), p.wait_ns));
         if (!ok) return;
         if (lead) load(ring + s * TL::kBytes, map, x, y, smem_addr(&full[s]));
         ++used;
       };
       auto next_q = [&](int tile, int x, int y) {
         if (!ok) return;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&q_empty[tile]), static_cast<uint32_t>((q_used[tile] & 1) ^ 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&q_empty[tile]), static_cast<uint32_t>((q_used[tile] & 1) ^ 1), p.wait_ns));
         if (!ok) return;
         if (lead) load(q_s + tile * TL::kBytes, &tm_q, x, y, smem_addr(&q_full[tile]));
         ++q_used[tile];
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const bool lead = elect_one();
       bool ok = true;
       auto wait = [&](uint64_t* bar, int phase) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), static_cast<uint32_t>(phase & 1)));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), static_cast<uint32_t>(phase & 1), p.wait_ns));
         tmem_fence_after_sync();
       };
       // item i of the ring: K of a step, or V
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int i0 = (2 * w.pair + tile) * kTile;  // first row of the tile in its sequence
       float m = -INFINITY, l = 0.0f;               // m in powers of two
       for (int j = 0; j < my_steps; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&s_full[tile]), static_cast<uint32_t>(s_seen++ & 1)));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&s_full[tile]), static_cast<uint32_t>(s_seen++ & 1), p.wait_ns));
         if (!ok) break;
         tmem_fence_after_sync();
         uint32_t s[kTile];
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // behind the sequence become zeros here, and so do such elements of the tile's own rows. The epilogue gives
           // them back to the rows that see them: those of this tile, and of tile 1, whose products read tile 0's rows after this.
           const int left = w.n - i0, iv = base + 2 * j + 1;
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&full[iv % kStages]), static_cast<uint32_t>((iv / kStages) & 1)));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&full[iv % kStages]), static_cast<uint32_t>((iv / kStages) & 1), p.wait_ns));
           if (!ok) break;
           uint4* v = reinterpret_cast<uint4*>(smem + (2 + iv % kStages) * TL::kBytes);
           uint32_t top = 0u;
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       base += 2 * w.steps();
       if (!ok || my_steps == 0) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&o_full[tile]), static_cast<uint32_t>(o_seen++ & 1)));
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&o_full[tile]), static_cast<uint32_t>(o_seen++ & 1), p.wait_ns));
       if (!ok) break;
       tmem_fence_after_sync();
       const bool in = i0 + row < w.n;
@@ -616,7 +617,7 @@ cudaError_t launch_attention_prompt(const AttentionPromptArgs& a, cudaStream_t s
       !encode_rows(enc, &tv, a.v, a.ld_v, a.T, a.kv_heads * a.D))
     return cudaErrorInvalidValue;
   PromptParams p{a.v, a.ld_v, a.row_start, a.out, a.lse, a.status, a.ld_out, a.T, a.B, a.q_heads, a.q_heads / a.kv_heads, a.D,
-                 a.scale * 1.44269504088896341f};
+                 a.scale * 1.44269504088896341f, stage_wait_ns()};
   // pairs of tiles: a sequence of n rows has at most n / 256 + 1
   const int64_t items = a.T / (2 * kTile) + a.B;
   void* args[] = {&tq, &tk, &tv, &p};

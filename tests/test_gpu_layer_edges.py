@@ -86,3 +86,28 @@ def test_prompt_marks_of_one_piece_do_not_reach_the_next():
     want = with_values_planted(starts, good, v, plant)
     for _ in range(5):
         assert same(prompt(q, k, v, starts)[0], want)
+
+
+def test_prompt_waits_that_give_up_return_and_leave_nothing_behind():
+    """A limit of 0: every wait gives up at once, the call says so and returns; with the old limit the same call is what it
+    was, and a recorded one keeps the limit of its recording."""
+    starts = [0, 300, 301, 1500]
+    g = gen(4)
+    q, k, v = (torch.randn((1500, n, 128), generator=g, device=DEV).bfloat16() for n in (4, 2, 2))
+    good, good_lse = prompt(q, k, v, starts)
+    at, out, st = i32(starts), torch.empty_like(good), status()
+    graph = m.MtpDraftHead.capture(lambda s: m.mtp_head_attention_prompt(q, k, v, at, out, status=st, stream=s))
+    old = m.mtp_head_set_wait_limit_ns(0)
+    try:
+        for _ in range(3):
+            none = status()
+            prompt(q, k, v, starts, none)
+            torch.cuda.synchronize()
+            assert int(none.item()) == m.ERR_TIMEOUT
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and torch.equal(out, good)
+    finally:
+        m.mtp_head_set_wait_limit_ns(old)
+    again, lse = prompt(q, k, v, starts, st)
+    assert int(st.item()) == 0 and torch.equal(again, good) and torch.equal(lse, good_lse)
