@@ -274,8 +274,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         __syncwarp();
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(asked), turn, p.wait_ns));
+        if (!ok) {
+          (void)mbar_wait_bounded(smem_addr(asked), turn);  // the answer lands before the shared memory goes away
+          break;
+        }
         turn ^= 1u;
-        if (!ok) break;
         uint32_t got, x;
         asm volatile(
             "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\tld.shared.b128 a, [%2];\n\t"

@@ -111,3 +111,30 @@ def test_prompt_waits_that_give_up_return_and_leave_nothing_behind():
         m.mtp_head_set_wait_limit_ns(old)
     again, lse = prompt(q, k, v, starts, st)
     assert int(st.item()) == 0 and torch.equal(again, good) and torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("starts,certain", [([0, 300, 301, 1500, 4000], False), ([0, 20000], True)])
+def test_prompt_waits_that_run_out_under_way(starts, certain):
+    """A limit of 1 ns: waits run out wherever their data is not there within the hardware's own polling time, in the
+    middle of pieces too. A call says so, or has the usual results; what was under way lands, and the next call is right.
+    In the second case a CTA has eight pieces one after another, the next but one of which waits for a whole piece (tens
+    of us): some wait runs out."""
+    g = gen(5)
+    q, k, v = (torch.randn((starts[-1], n, 64), generator=g, device=DEV).bfloat16() for n in (16, 2, 2))
+    good, good_lse = prompt(q, k, v, starts)
+    codes = []
+    old = m.mtp_head_set_wait_limit_ns(1)
+    try:
+        for _ in range(20):
+            st = status()
+            out, lse = prompt(q, k, v, starts, st)
+            codes.append(int(st.item()))
+            assert codes[-1] in (0, m.ERR_TIMEOUT)
+            if codes[-1] == 0:
+                assert torch.equal(out, good) and torch.equal(lse, good_lse)
+    finally:
+        m.mtp_head_set_wait_limit_ns(old)
+    assert not certain or m.ERR_TIMEOUT in codes
+    st = status()
+    out, lse = prompt(q, k, v, starts, st)
+    assert int(st.item()) == 0 and torch.equal(out, good) and torch.equal(lse, good_lse)

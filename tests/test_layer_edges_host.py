@@ -20,3 +20,13 @@ def test_prompt_kernel_joins_its_warps_by_bounded_waits_only():
     at = [i.start() for i in re.finditer(r"__syncthreads\(\)", kernel)]
     assert len(at) == 2 and at[0] < roles[0] and at[1] > roles[1]
     assert "mbar_try_wait" not in kernel  # (mbar_wait_bounded alone)
+
+
+def test_prompt_kernel_lets_an_answer_under_way_land():
+    """The answer about the next piece is written into shared memory by the hardware: a wait for it that runs out is
+    followed by one with the full limit before the warp leaves."""
+    text = source("attention_prompt.cu")
+    asked = text.split("clusterlaunchcontrol.try_cancel")[1].split("clusterlaunchcontrol.query_cancel")[0]
+    waits = re.findall(r"mbar_wait_bounded\(smem_addr\(asked\), turn(, p\.wait_ns)?\)", asked)
+    assert waits == [", p.wait_ns", ""]
+    assert asked.index("break;") > asked.rindex("mbar_wait_bounded")
