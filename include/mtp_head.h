@@ -582,7 +582,7 @@ int mtp_head_cache_read_fp4(const uint8_t* q, const uint8_t* block_scale, const 
  *                        each): query head h reads key head h / (q_heads / kv_heads)
  *
  * With n = rows[b], row i < n sees the first length[b] - n + i + 1 tokens:
- *   out = sum_j p_j v_j,  p = softmax_j( scale q . k_j ),  scale finite and > 0
+ *   out = sum_j p_j v_j,  p = softmax_j( scale q . k_j ),  0 < scale <= 2^60, |scale q . k_j| below 2^127
  * A row that sees no token gives zeros and lse -Inf. Rows i >= n are left as they were. What the pages hold
  * behind a sequence's tokens does not matter. Products take 16-bit operands (keys, values and query rows
  * exactly, weights in f16), sums are fp32; results do not vary from run to run.
@@ -621,7 +621,7 @@ size_t mtp_head_attention_fp4_workspace_bytes(int B, int Q, int q_heads, int kv_
  * Rows outside every sequence are left as they were, and what they hold does not matter. Weights are
  * BF16, sums fp32; results do not vary from run to run.
  *   1 <= T <= 2^22, 1 <= B <= 65536, q_heads a multiple of kv_heads (at most 1024 each), D 64 or 128 (others
- *   MTP_ERR_NOT_IMPLEMENTED), scale finite and > 0. No workspace.
+ *   MTP_ERR_NOT_IMPLEMENTED), 0 < scale <= 2^60, |scale q . k_j| below 2^127. No workspace.
  * ---------------------------------------------------------------------------------------- */
 int mtp_head_attention_prompt(const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k,
                               const uint16_t* v, int64_t ld_v, const int32_t* row_start,

@@ -24,7 +24,10 @@ bool bad4(const void* p) { return p && !aligned(p, 4); }
 // A row stride: dense heads fit, and rows start on 16-byte boundaries.
 bool bad_ld(int64_t ld, int64_t row) { return ld < row || ld > (static_cast<int64_t>(1) << 40); }
 size_t strided(int64_t rows, int64_t ld, int64_t row) { return (static_cast<size_t>(rows - 1) * ld + row) * 2; }
-bool bad_scale(float s) { return !(s > 0.0f) || isinf(s); }
+// With log2(e) and, over the cache, half of a query row's power of two (2^60 at most) it stays a number: an infinite factor
+// would make NaN of scores that are zero.
+constexpr float kMaxScale = 0x1p60f;
+bool bad_scale(float s) { return !(s > 0.0f && s <= kMaxScale); }
 
 int check_cache(const void* q, const void* bs, const void* rs, int heads, int D, int pages, int page, int max_pages) {
   if (!q || !bs || !rs) return MTP_ERR_ARG;

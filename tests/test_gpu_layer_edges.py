@@ -138,3 +138,35 @@ def test_prompt_waits_that_run_out_under_way(starts, certain):
     st = status()
     out, lse = prompt(q, k, v, starts, st)
     assert int(st.item()) == 0 and torch.equal(out, good) and torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 60, 2.0 ** -100])
+def test_scores_of_zero_stay_zero_at_any_scale(scale):
+    """Queries of 2^120 in a column where every key is zero: the weights are equal, so the outputs are the values' mean."""
+    n, D = 48, 64
+    g = gen(6)
+    q = torch.zeros((n, 2, D), dtype=BF, device=DEV)
+    q[..., 0] = 2.0 ** 120
+    k = torch.randn((n, 1, D), generator=g, device=DEV).bfloat16()
+    k[..., 0] = 0.0
+    v = torch.randint(-8, 9, (n, 1, D), generator=g, device=DEV).bfloat16()
+    v[:, :, ::16] = 8.0  # (blocks and rows whose FP4 copies hold these integers' multiples)
+    out, lse = torch.empty_like(q), torch.empty((n, 2), device=DEV)
+    m.mtp_head_attention_prompt(q, k, v, i32([0, n]), out, lse, scale)
+    mean = v[:, 0].double().cumsum(0) / torch.arange(1, n + 1, device=DEV).view(-1, 1)
+    # equal weights of 1: the sums are exact, their quotient rounds twice in fp32 and once to BF16
+    tol = mean.abs() * (2.0 ** -8 + 2.0 ** -21)
+    assert bool(((out.double() - mean.view(n, 1, D)).abs() <= tol.view(n, 1, D)).all())
+    cache, table = m.cache_empty(3, 16, 1, D, DEV), i32([[0, 1, 2]])
+    m.mtp_head_cache_write_fp4(k, v, i32([0, n]), i32([0]), table, *cache)
+    held = [torch.zeros((n, 1, D), dtype=BF, device=DEV) for _ in range(2)]
+    m.mtp_head_cache_read_fp4(*cache, i32([0, n]), i32([0]), table, *held)
+    assert not bool(held[0][..., 0].any())
+    one, ws = torch.empty((1, 1, 2, D), dtype=BF, device=DEV), m.attention_fp4_workspace(1, 1, 2, 1, D, 48, DEV)
+    m.mtp_head_attention_fp4(q[-1:].view(1, 1, 2, D), *cache, table, i32([n]), one, ws, scale=scale)
+    mean = held[1][:, 0].double().mean(0)
+    # the values read back are BF16 (2^-8 of each), the weights carry log2 of row scales near 8 / 2688 (8.4: an error of
+    # 3 * 8.4 * 2^-24 in the exponent) and round to f16 (2^-11); the result rounds to BF16
+    size = held[1][:, 0].double().abs().mean(0)
+    assert bool(((one.double() - mean).abs() <= size * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) + mean.abs() * 2.0 ** -8).all())
+    assert bool(((lse.double() - torch.arange(1, n + 1, device=DEV).double().log().view(-1, 1)).abs() <= 2.0 ** -20).all())

@@ -30,3 +30,16 @@ def test_prompt_kernel_lets_an_answer_under_way_land():
     waits = re.findall(r"mbar_wait_bounded\(smem_addr\(asked\), turn(, p\.wait_ns)?\)", asked)
     assert waits == [", p.wait_ns", ""]
     assert asked.index("break;") > asked.rindex("mbar_wait_bounded")
+
+
+def test_scales_that_leave_fp32_with_their_factors_are_refused():
+    """scale log2(e) and, over the cache, half of a query row's power of two are fp32 numbers: beyond 2^60 they need not be."""
+    import ctypes
+
+    import mtp_speculative_draft_head_gb300 as m
+    import test_layer_host as h
+    lib = m.load()
+    for scale in (2.0 ** 60 * (1 + 2.0 ** -23), 2.0 ** 100, 3.0e38):
+        assert ctypes.c_float(scale).value > 2.0 ** 60
+        assert h.attend(lib, dict(h.spread(h.ATT), **dict(h.ATT_SIZES, scale=scale))) == m.ERR_ARG
+        assert h.prompt(lib, dict(h.spread(h.PROMPT), **dict(h.PROMPT_SIZES, scale=scale))) == m.ERR_ARG
