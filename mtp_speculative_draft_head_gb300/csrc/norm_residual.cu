@@ -6,8 +6,9 @@
 // One read of x and delta: a row stays in the registers of the threads that share it, between the
 // sum of its squares and the results. Sums of squares are double-floats of exact squares, 1/rms is
 // formed in fp64, and y is rounded once from a double-float: y is the same whatever the number of
-// threads. A row's squares leave the fp32 range beyond 2^64 or below 2^-75; such a row is taken
-// once more at 2^-80 or 2^80 of its size, which the norm divides out again.
+// threads. A row's squares leave the fp32 range beyond 2^64 or below 2^-75; such a row's sum is taken
+// once more of 2^-80 or 2^80 of its elements, and its y is formed in fp64, as is an element's of any row
+// whose factors leave the normal fp32 range on the way.
 //
 // Measured: 4096 rows of 6144 columns with all three outputs (227 MB) 46 us, 4.9 TB/s where a copy makes 6.7; a row that is not
 // a multiple of 8 long costs its edges (1021 rows of 5003 columns without delta and codes, 20 MB: 10 us); 16 rows 5 us, a launch. Instructions bound
@@ -55,38 +56,87 @@ __device__ __forceinline__ uint32_t add_pair(uint32_t a, uint32_t b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(f2_hi(s)), "f"(f2_lo(s)));
   return o;
 }
-// A BF16 pair times a power of two (exact, but for results below the normal range).
-__device__ __forceinline__ uint32_t scale_pair(uint32_t a, float f) {
-  uint32_t o;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(__fmul_rn(bf16_hi(a), f)), "f"(__fmul_rn(bf16_lo(a), f)));
-  return o;
+// bf16( x w r ) in fp64: x w is exact, so the product is within two roundings of 2^-53 of the real one. Rounded to odd on the
+// way to fp32, so that the rounding to BF16 is that of the product. (A zero, the common case of such rows, costs nothing.)
+__device__ __forceinline__ uint32_t scaled_fp64(float x, float w, double r) {
+  if (x == 0.0f && fabsf(w) < __int_as_float(0x7f800000) && r < __longlong_as_double(0x7ff0000000000000ll))
+    return (__float_as_uint(x) ^ __float_as_uint(w)) >> 16 & 0x8000u;
+  const float f = to_odd(static_cast<double>(x) * static_cast<double>(w) * r);
+  return f != f ? 0x7FC0u : bf16_bits_rn(f);
 }
 
-// bf16( x w (rh + rl) ) of eight columns, as bf16x8_scaled_rne: the fp32 product x w rh decides unless its low half is within
-// two units of a BF16 midpoint; such a cell is redone as a whole from double-floats, out of line.
-static __device__ __noinline__ uint4 scaled_exact(uint4 x, uint4 w01, uint4 w23, float rh, float rl) {
-  const uint32_t xu[4] = {x.x, x.y, x.z, x.w};
-  const float wf[8] = {__uint_as_float(w01.x), __uint_as_float(w01.y), __uint_as_float(w01.z), __uint_as_float(w01.w),
-                       __uint_as_float(w23.x), __uint_as_float(w23.y), __uint_as_float(w23.z), __uint_as_float(w23.w)};
-  return bf16x8_scaled_rne(xu, wf, rh, rl);
+// 1 / rms of a row: up (rh + rl) with up a power of two and rh in [1, 2) where fp32 holds the sum of its squares, else up is 0 and
+// rh and rl are the upper and lower half of its bits in fp64.
+struct Root {
+  float rh, rl, up;
+};
+__device__ __forceinline__ Root root_fp64(double r) {
+  return Root{__int_as_float(__double2hiint(r)), __int_as_float(__double2loint(r)), 0.0f};
 }
-__device__ __forceinline__ uint4 scaled(const uint32_t (&x)[4], const uint64_t (&w)[4], float rh, float rl) {
-  const uint64_t r2 = f2_pack(rh, rh);
+// The eight anew.
+static __device__ __noinline__ uint4 scaled_exact(uint4 x, uint4 w, Root r) {
+  const uint32_t xu[4] = {x.x, x.y, x.z, x.w}, wu[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[4];
+  float lo = __int_as_float(0x7f800000), hi = 0.0f;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    uint32_t h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float p = __fmul_rn(__fmul_rn(e ? bf16_hi(xu[t]) : bf16_lo(xu[t]), r.up), e ? bf16_hi(wu[t]) : bf16_lo(wu[t]));
+      const float yh = __fmul_rn(p, r.rh), yl = __fmaf_rn(p, r.rl, __fmaf_rn(p, r.rh, -yh));
+      lo = fminf(lo, fabsf(yh)), hi = fmaxf(hi, fabsf(yh));
+      h[e] = bf16_rne_df(yh, yl);
+    }
+    o[t] = h[0] | (h[1] << 16);
+  }
+  // (double-floats hold it from 2^-101 on, where their parts are normal numbers)
+  if (r.up != 0.0f && lo >= 0x1p-101f && hi < __int_as_float(0x7f800000)) return make_uint4(o[0], o[1], o[2], o[3]);
+  const double d = r.up != 0.0f ? (static_cast<double>(r.rh) + static_cast<double>(r.rl)) * static_cast<double>(r.up)
+                                : __hiloint2double(__float_as_int(r.rh), __float_as_int(r.rl));
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    o[t] = scaled_fp64(bf16_lo(xu[t]), bf16_lo(wu[t]), d) | (scaled_fp64(bf16_hi(xu[t]), bf16_hi(wu[t]), d) << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Whether an x of the eight is not zero and x up is below 2^-142 (a power of two times eight bits from there on is exact).
+__device__ __forceinline__ bool tiny_among(const uint32_t (&x)[4], float up) {
+  bool some = false;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float v = fabsf(e ? bf16_hi(x[t]) : bf16_lo(x[t]));
+      some |= v != 0.0f && __fmul_rn(v, up) <= 0x1p-142f;  // (at it: rounded up, perhaps)
+    }
+  return some;
+}
+// bf16( x w up (rh + rl) ) of eight columns: the fp32 product yh = ((x up) w) rh decides unless its low half is within two units
+// of a BF16 midpoint; such a cell is redone as a whole, out of line. x up is at most sqrt(H) and p = (x up) w within a factor of
+// two of y, so each leaves the fp32 range only where y does: both are exact (8 and 16 bits) but for p below 2^-134, which
+// is off by half a unit of 2^-149, and yh is within 1.5 units of y. x up is not exact below 2^-142 (in rows with an rms of 2^9
+// or more only): such an x becomes 0 with a weight below 2, and is redone with others.
+__device__ __forceinline__ uint4 scaled(const uint32_t (&x)[4], const uint64_t (&w)[4], const Root& r) {
+  const uint64_t r2 = f2_pack(r.rh, r.rh), up2 = f2_pack(r.up, r.up);
   uint32_t o[4], near = 0xFFFFFFFFu;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const uint64_t y = f2_mul(f2_mul(bf16x2_to_f2(x[t]), w[t]), r2);
+    const uint64_t y = f2_mul(f2_mul(f2_mul(bf16x2_to_f2(x[t]), up2), w[t]), r2);
     const uint32_t lo = static_cast<uint32_t>(y), hi = static_cast<uint32_t>(y >> 32);
     near = min(near, min((lo - 0x7FFEu) << 16, (hi - 0x7FFEu) << 16));
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[t]) : "f"(f2_hi(y)), "f"(f2_lo(y)));
   }
-  if (near <= 0x40000u || !(rh >= 1.17549435e-38f))
-    return scaled_exact(make_uint4(x[0], x[1], x[2], x[3]),
-                        make_uint4(static_cast<uint32_t>(w[0]), static_cast<uint32_t>(w[0] >> 32), static_cast<uint32_t>(w[1]),
-                                   static_cast<uint32_t>(w[1] >> 32)),
-                        make_uint4(static_cast<uint32_t>(w[2]), static_cast<uint32_t>(w[2] >> 32), static_cast<uint32_t>(w[3]),
-                                   static_cast<uint32_t>(w[3] >> 32)),
-                        rh, rl);
+  bool redo = near <= 0x40000u;
+  if (r.up < 0x1p-9f) {  // (the whole row alike)
+    uint32_t any = 0u;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) any |= static_cast<uint32_t>(w[t]) | static_cast<uint32_t>(w[t] >> 32);
+    redo |= r.up == 0.0f || ((any & 0x40000000u) != 0u && tiny_among(x, r.up));  // (the bit of magnitudes from 2 on)
+  }
+  if (redo) {
+    auto pair = [](uint64_t v) { return __byte_perm(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), 0x7632); };
+    return scaled_exact(make_uint4(x[0], x[1], x[2], x[3]), make_uint4(pair(w[0]), pair(w[1]), pair(w[2]), pair(w[3])), r);
+  }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -159,13 +209,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 256 && P <= 3 ? 
 
   // ---- 1 / rms. A CTA's sums go through shared memory to its first warp: adding double-floats across lanes costs a warp as
   // much as ten elements a lane, so one warp does it for all (and with it the one fp64 reciprocal root of the row).
-  auto sum_squares = [&]() -> DF {  // TPR > 32: of warp 0 only
+  auto sum_squares = [&](float times) -> DF {  // of the elements times a power of two; TPR > 32: of warp 0 only
     DF2 acc{0ull, 0ull};
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint64_t f = bf16x2_to_f2(s[i][e]);
+        uint64_t f = bf16x2_to_f2(s[i][e]);
+        if (times != 1.0f) f = f2_mul(f, f2_pack(times, times));
         df2_add(acc, f2_mul(f, f));
       }
     DF v = df_add(df2_x(acc), df2_y(acc));
@@ -185,32 +236,33 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 256 && P <= 3 ? 
     }
     return v;
   };
-  auto root = [&](const DF& v, double factor2) {  // 1 / sqrt(mean + eps) as two fp32 parts, within an ulp or two of fp64
+  auto root64 = [&](const DF& v, double factor2) {  // 1 / sqrt(mean + eps factor2), within an ulp or two of fp64
     const double ms = (static_cast<double>(v.hi) + static_cast<double>(v.lo)) * a.inv_h;
-    const double r = rsqrt(ms + static_cast<double>(a.eps) * factor2);
-    const float hi = static_cast<float>(r);
-    return make_float2(hi, isinf(hi) ? 0.0f : static_cast<float>(r - static_cast<double>(hi)));
+    return rsqrt(ms + static_cast<double>(a.eps) * factor2);
   };
-  auto ordinary = [](const DF& v) { return v.hi >= 0x1p-100f && v.hi < __int_as_float(0x7f800000); };
-  DF tot = sum_squares();
-  float rh, rl;
-  bool good;
+  auto root = [&](const DF& v) {
+    if (!(v.hi >= 0x1p-100f && v.hi < __int_as_float(0x7f800000))) return Root{1.0f, 0.0f, 0.0f};
+    const double r = root64(v, 1.0);
+    const float hi = static_cast<float>(r);
+    const uint32_t e = __float_as_uint(hi) & 0x7F800000u;  // (2^-64 to 2^58)
+    const float down = __uint_as_float(0x7F000000u - e);
+    return Root{__fmul_rn(hi, down), __fmul_rn(static_cast<float>(r - static_cast<double>(hi)), down), __uint_as_float(e)};
+  };
+  DF tot = sum_squares(1.0f);
+  Root r;
   if constexpr (TPR == 32) {
-    good = ordinary(tot);
-    const float2 r = root(tot, 1.0);
-    rh = r.x, rl = r.y;
+    r = root(tot);
   } else {
     if (threadIdx.x == 0) {
-      const float2 r = root(tot, 1.0);
-      red[0] = r.x;
-      red[1] = r.y;
-      red[2] = ordinary(tot) ? 1.0f : 0.0f;
+      const Root of = root(tot);
+      red[0] = of.rh;
+      red[1] = of.rl;
+      red[2] = of.up;
     }
     __syncthreads();
-    rh = red[0], rl = red[1];
-    good = red[2] != 0.0f;
+    r = Root{red[0], red[1], red[2]};
   }
-  if (!good) {  // (the whole row alike) squares beyond fp32, or infinities or NaN among them
+  if (r.up == 0.0f) {  // (the whole row alike) squares beyond fp32, or infinities or NaN among them
     uint32_t nan = 0u, inf = 0u, top = 0u;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -225,7 +277,6 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 256 && P <= 3 ? 
     uint32_t flags = __reduce_or_sync(0xffffffffu, nan | (inf << 1));
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
     if constexpr (TPR > 32) {
-      __syncthreads();  // red has been read
       if (lane == 0) redm[warp] = flags | (top << 2);
       __syncthreads();
       flags = 0u, top = 0u;
@@ -236,26 +287,22 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 256 && P <= 3 ? 
     }
     const bool big = top >= 0x5000u;  // (2^33; squares of smaller rows do not overflow)
     const float f = big ? 0x1p-80f : 0x1p80f;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] = scale_pair(s[i][e], f);
-    tot = sum_squares();
+    tot = sum_squares(f);
     // an infinity makes the mean infinite (finite columns become 0), a NaN makes it NaN
     if (flags != 0u) tot = DF{__int_as_float((flags & 1u) ? 0x7fc00000 : 0x7f800000), 0.0f};
     const double factor2 = big ? 0x1p-160 : 0x1p160;
     if constexpr (TPR == 32) {
-      const float2 r = root(tot, factor2);
-      rh = r.x, rl = r.y;
+      r = root_fp64(root64(tot, factor2) * static_cast<double>(f));
     } else {
       if (threadIdx.x == 0) {
-        const float2 r = root(tot, factor2);
-        red[0] = r.x;
-        red[1] = r.y;
+        const Root of = root_fp64(root64(tot, factor2) * static_cast<double>(f));
+        red[0] = of.rh;
+        red[1] = of.rl;
       }
       __syncthreads();
-      rh = red[0], rl = red[1];
+      r = Root{red[0], red[1], 0.0f};
     }
+    if (flags == 0u && top == 0u && a.eps > 0.0f) r = Root{1.0f, 0.0f, 1.0f};  // a row of zeros stays one
   }
 
   // ---- y (in the place of s)
@@ -273,7 +320,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 256 && P <= 3 ? 
         w[e] = f2_pack(c0 + 2 * e >= 0 && c0 + 2 * e < H ? bf16_bits_to_f32(a.w[c0 + 2 * e]) : 0.0f,
                        c0 + 2 * e + 1 >= 0 && c0 + 2 * e + 1 < H ? bf16_bits_to_f32(a.w[c0 + 2 * e + 1]) : 0.0f);
     }
-    const uint4 o = scaled(s[i], w, rh, rl);
+    const uint4 o = scaled(s[i], w, r);
     s[i][0] = o.x, s[i][1] = o.y, s[i][2] = o.z, s[i][3] = o.w;
     if constexpr (!VEC) {  // (a NaN factor leaves a NaN in the columns that are not the row's)
 #pragma unroll

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import mtp_speculative_draft_head_gb300 as m
+import oracle
+import synth
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -170,3 +172,47 @@ def test_scores_of_zero_stay_zero_at_any_scale(scale):
     size = held[1][:, 0].double().abs().mean(0)
     assert bool(((one.double() - mean).abs() <= size * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) + mean.abs() * 2.0 ** -8).all())
     assert bool(((lse.double() - torch.arange(1, n + 1, device=DEV).double().log().view(-1, 1)).abs() <= 2.0 ** -20).all())
+
+
+# ------------------------------------------------------------------------------------- residual norm
+def bf16(a):
+    return torch.from_numpy(oracle.f64_to_bf16(a).view(np.int16).copy()).view(BF).to(DEV)
+
+
+def vals(t):
+    return oracle.bf16_to_f64(synth.bits(t))
+
+
+def norm_is_rounded_once(x, w, eps, delta=None):
+    """y, bit for bit, against the formula in 64 bits, whatever its factors' sizes; zeros of either sign are alike."""
+    t = vals(x) if delta is None else oracle.bf16_to_f64(oracle.f64_to_bf16(vals(x) + vals(delta)))
+    with np.errstate(over="ignore"):
+        want = oracle.bf16_to_f64(oracle.f64_to_bf16(t * (vals(w)[None] / np.sqrt((t * t).mean(1, keepdims=True) + eps))))
+    y = torch.empty_like(x)
+    m.mtp_head_norm_residual(x, w, delta, y=y, eps=eps)
+    assert np.array_equal(vals(y), want)
+
+
+@pytest.mark.parametrize("H", [200, 1003, 2048, 6144, 9000])
+@pytest.mark.parametrize("xs,ws", [(2.0 ** 60, 2.0 ** 70), (2.0 ** 30, 2.0 ** 110), (2.0 ** -20, 2.0 ** -115), (2.0 ** -49, 2.0 ** -80),
+                                   (2.0 ** 100, 2.0 ** 90), (2.0 ** -100, 2.0 ** 90), (2.0 ** -100, 2.0 ** -60)])
+def test_norm_weights_of_any_size(xs, ws, H):
+    """x w beyond the fp32 range on either side, where x w / rms is within it."""
+    r = np.random.default_rng(H)
+    x, w = bf16(r.standard_normal((5, H)) * xs), bf16(r.standard_normal(H) * ws)
+    for eps in (0.0, 1e-6):
+        norm_is_rounded_once(x, w, eps)
+
+
+@pytest.mark.parametrize("H", [200, 1003, 4096, 6144, 9000])
+@pytest.mark.parametrize("top", [2.0 ** 90, 2.0 ** 40, 1.0, 2.0 ** -45, 2.0 ** -70])
+def test_norm_rows_of_elements_far_apart(top, H):
+    """Elements down to 2^-133 beside the row's largest, zeros among them, with weights that bring them back."""
+    r = np.random.default_rng(H + 1)
+    x = r.standard_normal((6, H)) * top * 2.0 ** -r.uniform(0, 160, (6, H))
+    x[:, ::5] = 0.0
+    x[:, 3] = top
+    w = r.standard_normal(H) * 2.0 ** r.uniform(-60, 120, H)
+    w[2::7] = 0.0
+    norm_is_rounded_once(bf16(x), bf16(w), 0.0)
+    norm_is_rounded_once(bf16(x), bf16(w), 1e-6, bf16(r.standard_normal((6, H)) * top * 2.0 ** -r.uniform(0, 160, (6, H))))
