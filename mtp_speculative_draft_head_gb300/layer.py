@@ -14,6 +14,12 @@ import torch
 from . import _lib
 
 
+def _filled(device) -> None:
+    """Waits for the fills of new buffers: calls on any stream may use them from here on."""
+    if device.type == "cuda":
+        torch.cuda.current_stream(device).synchronize()
+
+
 class LayerCache:
     """A paged FP4 cache of keys and values for ``batch`` sequences of up to ``max_len`` tokens: the three
     arrays, and a table that gives every sequence pages of its own (``table`` may be replaced by one that
@@ -26,6 +32,7 @@ class LayerCache:
         self.arrays = _lib.cache_empty(batch * self.max_pages, page, kv_heads, head_dim, device)
         self.device = self.arrays[0].device
         self.table = torch.arange(batch * self.max_pages, dtype=torch.int32, device=self.device).view(batch, -1)
+        _filled(self.device)
 
     def write(self, k, v, row_start, position, status=None, stream=None) -> None:
         """Packed rows k, v [T, kv_heads, head_dim] to the sequences' places, as mtp_head_cache_write_fp4."""
@@ -46,7 +53,10 @@ class DraftLayer:
     projections are copied to FP4 here. ``rotate(q, k, positions)``, if given, rotates the views q
     [R, q_heads, head_dim] and k [R, kv_heads, head_dim] in place (positions [R] int32). ``mlp(y, q, q_scale)``, with
     ``mlp_norm_w`` [H], takes the normalised rows in BF16 and in E4M3 (a scale per 128 columns) and returns what is
-    added to x. ``max_rows``: rows of a call at most."""
+    added to x. ``max_rows``: rows of a call at most.
+
+    Its workspaces serve one call at a time: calls of one layer (and replays of graphs that recorded some) follow one
+    another, on one stream or ordered by events."""
 
     def __init__(self, norm_w, qkv_proj, o_proj, q_heads: int, kv_heads: int, cache: LayerCache, eps: float = 1e-6,
                  max_rows: int = 16, rotate=None, mlp=None, mlp_norm_w=None):
@@ -71,12 +81,14 @@ class DraftLayer:
             raise _lib.MTPError(int(st.item()), "DraftLayer")
         self.ws_qkv = _lib.linear_fp4_workspace(max_rows, width, self.H, dev)
         self.ws_o = _lib.linear_fp4_workspace(max_rows, self.H, q_heads * self.D, dev)
-        self.ws_step = {1: self._step_workspace(1)}  # by the rows of a sequence
+        self.ws_step = {1: self._step_workspace(1)}  # by the rows of a sequence (waits for all fills up to here)
 
     def _step_workspace(self, Q: int):
         """For steps of Q rows of as many sequences as max_rows and the cache allow."""
-        return _lib.attention_fp4_workspace(min(self.cache.batch, self.max_rows // Q), Q, self.q_heads, self.kv_heads, self.D,
-                                            self.cache.max_len, self.device)
+        ws = _lib.attention_fp4_workspace(min(self.cache.batch, self.max_rows // Q), Q, self.q_heads, self.kv_heads, self.D,
+                                          self.cache.max_len, self.device)
+        _filled(self.device)
+        return ws
 
     def _project(self, x, status, stream):
         R = x.shape[0]
@@ -106,8 +118,8 @@ class DraftLayer:
     def step(self, x, length, status=None, stream=None):
         """The layer over the next rows of each sequence, in place: x [B Q, H] (Q rows of each of B sequences, the
         first B of the cache), length [B] int32 (Q at least) the tokens that the cache holds with them. Their keys and values are
-        written to the cache first. The first step of another Q than 1 makes that Q's workspace and is not recorded into a
-        graph: its zero fill would only run with the graph."""
+        written to the cache first. The first step of another Q than 1 makes that Q's workspace, waits for its zero fill and is
+        not recorded into a graph: the fill would only run with the graph."""
         B = length.numel()
         if B < 1 or x.shape[0] < B or x.shape[0] % B != 0 or B > self.cache.batch:
             raise ValueError("x: an equal number of rows for each sequence of the cache")

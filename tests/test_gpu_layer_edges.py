@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import mtp_speculative_draft_head_gb300 as m
+from mtp_speculative_draft_head_gb300 import _lib
 import oracle
 import synth
 
@@ -216,3 +217,41 @@ def test_norm_rows_of_elements_far_apart(top, H):
     w[2::7] = 0.0
     norm_is_rounded_once(bf16(x), bf16(w), 0.0)
     norm_is_rounded_once(bf16(x), bf16(w), 1e-6, bf16(r.standard_normal((6, H)) * top * 2.0 ** -r.uniform(0, 160, (6, H))))
+
+
+# ------------------------------------------------------------------------------------- the layer and its cache
+H, HQ, KV, D = 128, 4, 2, 64
+
+
+def layer_weights(seed=50):
+    g = gen(seed)
+    r = lambda *s: (torch.randn(s, generator=g, device=DEV) * 0.06).bfloat16()  # noqa: E731
+    return 1 + r(H), r((HQ + 2 * KV) * D, H), r(H, HQ * D), HQ, KV
+
+
+def rows(n, seed):
+    return torch.randn((n, H), generator=gen(seed), device=DEV).bfloat16()
+
+
+def test_layer_buffers_are_filled_before_another_stream_may_use_them(monkeypatch):
+    """Zero fills run on the stream of the construction, or of a step's first number of rows. They are over when the call
+    returns: nothing orders them before a call on another stream."""
+    late = torch.cuda.Stream()
+    with torch.cuda.stream(late):
+        torch.cuda._sleep(100_000_000)
+        cache = m.LayerCache(2, 64, KV, D, page=16, device=DEV)
+        assert late.query()
+        real = _lib.attention_fp4_workspace
+
+        def slow(*args):
+            torch.cuda._sleep(100_000_000)
+            return real(*args)
+
+        monkeypatch.setattr(_lib, "attention_fp4_workspace", slow)
+        layer = m.DraftLayer(*layer_weights(), cache, max_rows=6)
+        assert late.query()
+        calls = []
+        monkeypatch.setattr(_lib, "mtp_head_norm_residual", lambda *a, **k: calls.append(late.query()))
+        layer.step(rows(6, 1), i32([3, 3]))
+        assert calls[0]
+    torch.cuda.synchronize()
