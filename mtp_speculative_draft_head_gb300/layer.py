@@ -20,6 +20,14 @@ def _filled(device) -> None:
         torch.cuda.current_stream(device).synchronize()
 
 
+def _on(stream, device):
+    """The context of a stream as the binding takes it: a torch.cuda.Stream, a raw handle or None (the current one)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 class LayerCache:
     """A paged FP4 cache of keys and values for ``batch`` sequences of up to ``max_len`` tokens: the three
     arrays, and a table that gives every sequence pages of its own (``table`` may be replaced by one that
@@ -40,8 +48,9 @@ class LayerCache:
 
     def read(self, row_start, position, rows: int, status=None, stream=None):
         """``rows`` packed rows (k, v) back as BF16, as mtp_head_cache_read_fp4 (rows of no sequence: zeros)."""
-        k, v = (torch.zeros((rows, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
-                for _ in range(2))
+        with _on(stream, self.device):  # (the fills too)
+            k, v = (torch.zeros((rows, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+                    for _ in range(2))
         _lib.mtp_head_cache_read_fp4(*self.arrays, row_start, position, self.table, k, v, status, stream)
         return k, v
 

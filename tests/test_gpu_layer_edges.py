@@ -255,3 +255,19 @@ def test_layer_buffers_are_filled_before_another_stream_may_use_them(monkeypatch
         layer.step(rows(6, 1), i32([3, 3]))
         assert calls[0]
     torch.cuda.synchronize()
+
+
+def test_cache_read_fills_its_rows_on_the_stream_that_reads():
+    cache = m.LayerCache(1, 64, KV, D, page=16, device=DEV)
+    k, v = (torch.randn((20, KV, D), generator=gen(i), device=DEV).bfloat16() for i in (51, 52))
+    starts, at = i32([0, 20]), i32([0])
+    cache.write(k, v, starts, at)
+    good = cache.read(starts, at, 22)
+    assert bool(good[0][:20].any()) and not bool(good[0][20:].any())
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # the current stream is busy
+    got = cache.read(starts, at, 22, stream=other)
+    raw = cache.read(starts, at, 22, stream=other.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((*got, *raw), (*good, *good)))
