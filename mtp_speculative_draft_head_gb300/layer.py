@@ -135,7 +135,7 @@ class DraftLayer:
         Q = x.shape[0] // B
         if x.shape[0] > self.max_rows:
             raise ValueError(f"{x.shape[0]} rows, made for {self.max_rows}")
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device):
             if Q not in self.ws_step:
                 if torch.cuda.is_current_stream_capturing():
                     raise RuntimeError(f"DraftLayer: make one step of {Q} rows before recording one")
@@ -159,7 +159,7 @@ class DraftLayer:
         B = row_start.numel() - 1
         if B < 1 or B > self.cache.batch:
             raise ValueError("row_start: one sequence at least, and no more than the cache has")
-        with torch.cuda.stream(stream):
+        with _on(stream, self.device):
             q, k, v = self._project(x, status, stream)
             if self.rotate is not None:
                 row = torch.arange(x.shape[0], dtype=torch.int32, device=self.device)

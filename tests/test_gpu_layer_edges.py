@@ -271,3 +271,28 @@ def test_cache_read_fills_its_rows_on_the_stream_that_reads():
     raw = cache.read(starts, at, 22, stream=other.cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((*got, *raw), (*good, *good)))
+
+
+def test_layer_takes_the_streams_that_the_binding_takes():
+    """A torch.cuda.Stream, its raw handle, the default stream's handle (0), or none; also through the head's forward."""
+    x0, x1 = rows(5, 53), rows(2, 54)
+    starts, length = i32([0, 3, 5]), i32([4, 3])
+    head_w = synth.make_weights(H, 512, 0, "cpu")
+    gw = {k: t.to(DEV) for k, t in head_w.as_dict().items()}
+    head = m.MtpDraftHead(gw["embed"], gw["lm_head"], gw["eh_proj"], gw["enorm_w"], gw["hnorm_w"], gw["final_norm_w"], max_batch=2)
+    tokens, hidden = (t.to(DEV) for t in synth.make_step_inputs(H, 512, 2, 0, "cpu"))
+    layer = m.DraftLayer(*layer_weights(), m.LayerCache(2, 64, KV, D, page=16, device=DEV), max_rows=5)
+    other = torch.cuda.Stream()
+    seen = []
+    for stream in (None, other, other.cuda_stream, 0):
+        a, b = x0.clone(), x1.clone()
+        torch.cuda.synchronize()
+        layer.prompt(a, starts, stream=stream)
+        torch.cuda.synchronize()
+        layer.step(b, length, stream=stream)
+        torch.cuda.synchronize()
+        x, _, draft = head.forward(tokens, hidden, stream=stream, layer=lambda x, **kw: layer.step(x, length, **kw))
+        torch.cuda.synchronize()
+        seen.append((a, b, x, draft))
+    for s in seen[1:]:
+        assert all(torch.equal(t, u) for t, u in zip(s, seen[0]))
