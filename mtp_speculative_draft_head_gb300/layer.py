@@ -64,6 +64,9 @@ class DraftLayer:
     ``mlp_norm_w`` [H], takes the normalised rows in BF16 and in E4M3 (a scale per 128 columns) and returns what is
     added to x. ``max_rows``: rows of a call at most.
 
+    ``status`` [1] int32 takes the errors of calls that are given none (a length or a prompt that the cache does not hold, a
+    page that is not there, a NaN or Inf in what is copied): it keeps the first until the caller sets it to 0.
+
     Its workspaces serve one call at a time: calls of one layer (and replays of graphs that recorded some) follow one
     another, on one stream or ordered by events."""
 
@@ -88,6 +91,7 @@ class DraftLayer:
         _lib.mtp_head_quantize_fp4(o_proj, *self.o_fp4, st)
         if int(st.item()) != 0:
             raise _lib.MTPError(int(st.item()), "DraftLayer")
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.ws_qkv = _lib.linear_fp4_workspace(max_rows, width, self.H, dev)
         self.ws_o = _lib.linear_fp4_workspace(max_rows, self.H, q_heads * self.D, dev)
         self.ws_step = {1: self._step_workspace(1)}  # by the rows of a sequence (waits for all fills up to here)
@@ -118,8 +122,6 @@ class DraftLayer:
         y = torch.empty_like(x)
         q = torch.empty(x.shape, dtype=torch.uint8, device=self.device)
         scale = torch.empty((x.shape[0], -(-self.H // 128)), dtype=torch.float32, device=self.device)
-        if status is None:
-            status = torch.zeros(1, dtype=torch.int32, device=self.device)
         _lib.mtp_head_norm_residual(x, self.mlp_norm_w, delta, x, y, q, scale, status, 128, self.eps, stream)
         _lib.mtp_head_norm_residual(x, self.mlp_norm_w, self.mlp(y, q, scale), total=x, eps=self.eps, stream=stream)
         return x
@@ -135,6 +137,7 @@ class DraftLayer:
         Q = x.shape[0] // B
         if x.shape[0] > self.max_rows:
             raise ValueError(f"{x.shape[0]} rows, made for {self.max_rows}")
+        status = self.status if status is None else status
         with _on(stream, self.device):
             if Q not in self.ws_step:
                 if torch.cuda.is_current_stream_capturing():
@@ -159,6 +162,7 @@ class DraftLayer:
         B = row_start.numel() - 1
         if B < 1 or B > self.cache.batch:
             raise ValueError("row_start: one sequence at least, and no more than the cache has")
+        status = self.status if status is None else status
         with _on(stream, self.device):
             q, k, v = self._project(x, status, stream)
             if self.rotate is not None:

@@ -296,3 +296,37 @@ def test_layer_takes_the_streams_that_the_binding_takes():
         seen.append((a, b, x, draft))
     for s in seen[1:]:
         assert all(torch.equal(t, u) for t, u in zip(s, seen[0]))
+
+
+@pytest.mark.parametrize("mlp", [False, True])
+def test_layer_keeps_the_errors_of_calls_without_a_status(mlp):
+    cache = m.LayerCache(2, 32, KV, D, page=16, device=DEV)
+    half = dict(mlp=lambda y, q, s: y, mlp_norm_w=layer_weights()[0]) if mlp else {}
+    layer = m.DraftLayer(*layer_weights(), cache, max_rows=80, **half)
+
+    def code():
+        c = int(layer.status.item())
+        layer.status.zero_()
+        return c
+
+    layer.prompt(rows(30, 55), i32([0, 20, 30]))
+    layer.step(rows(2, 56), i32([21, 11]))
+    assert code() == 0
+    layer.step(rows(2, 57), i32([33, 12]))  # a place behind the cache
+    assert code() == m.ERR_ARG
+    layer.prompt(rows(50, 58), i32([0, 40, 50]))  # more rows than the cache holds
+    assert code() == m.ERR_ARG
+    bad = rows(2, 59)
+    bad[1, 3] = NAN
+    layer.step(bad, i32([21, 11]))
+    assert code() == m.ERR_NONFINITE
+    own = status()
+    layer.step(rows(2, 60), i32([33, 12]), own)
+    assert int(own.item()) == m.ERR_ARG and code() == 0
+    table = cache.table.clone()
+    cache.table[1, 0] = 99
+    layer.step(rows(2, 61), i32([21, 11]))
+    assert code() == m.ERR_ARG
+    cache.table.copy_(table)
+    layer.step(rows(2, 62), i32([21, 11]))
+    assert code() == 0
