@@ -60,7 +60,8 @@ class DraftLayer:
 
     ``norm_w`` [H], ``qkv_proj`` [(q_heads + 2 kv_heads) head_dim, H], ``o_proj`` [H, q_heads head_dim] BF16: the
     projections are copied to FP4 here. ``rotate(q, k, positions)``, if given, rotates the views q
-    [R, q_heads, head_dim] and k [R, kv_heads, head_dim] in place (positions [R] int32). ``mlp(y, q, q_scale)``, with
+    [R, q_heads, head_dim] and k [R, kv_heads, head_dim] in place (positions [R] int32, never negative and always
+    below cache.max_len: rows that have no place there, which the status tells, and rows of no sequence are given the nearest). ``mlp(y, q, q_scale)``, with
     ``mlp_norm_w`` [H], takes the normalised rows in BF16 and in E4M3 (a scale per 128 columns) and returns what is
     added to x. ``max_rows``: rows of a call at most.
 
@@ -147,7 +148,8 @@ class DraftLayer:
             starts = torch.arange(0, (B + 1) * Q, Q, dtype=torch.int32, device=self.device)
             first = length - Q
             if self.rotate is not None:
-                self.rotate(q, k, (first.view(-1, 1) + torch.arange(Q, dtype=torch.int32, device=self.device)).view(-1))
+                at = (first.view(-1, 1) + torch.arange(Q, dtype=torch.int32, device=self.device)).view(-1)
+                self.rotate(q, k, at.clamp_(0, self.cache.max_len - 1))
             table = self.cache.table[:B]
             _lib.mtp_head_cache_write_fp4(k, v, starts, first, table, *self.cache.arrays, status, stream)
             heads = torch.empty((B, Q, self.q_heads, self.D), dtype=torch.bfloat16, device=self.device)
@@ -168,7 +170,7 @@ class DraftLayer:
             if self.rotate is not None:
                 row = torch.arange(x.shape[0], dtype=torch.int32, device=self.device)
                 which = torch.bucketize(row, row_start[1:], out_int32=True, right=True).clamp_(max=B - 1)
-                self.rotate(q, k, row - row_start[which.long()])
+                self.rotate(q, k, (row - row_start[which.long()]).clamp_(0, self.cache.max_len - 1))
             first = torch.zeros(B, dtype=torch.int32, device=self.device)
             _lib.mtp_head_cache_write_fp4(k, v, row_start, first, self.cache.table[:B], *self.cache.arrays, status, stream)
             heads = torch.zeros((x.shape[0], self.q_heads, self.D), dtype=torch.bfloat16, device=self.device)

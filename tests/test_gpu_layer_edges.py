@@ -330,3 +330,23 @@ def test_layer_keeps_the_errors_of_calls_without_a_status(mlp):
     cache.table.copy_(table)
     layer.step(rows(2, 62), i32([21, 11]))
     assert code() == 0
+
+
+def test_layer_rotates_at_places_of_the_cache_only():
+    """Rows of no sequence, lengths below the step's rows or past the cache: the positions that a rotation may look up in a
+    table of max_len rows stay within it, and those of rows that have a place are theirs."""
+    cache = m.LayerCache(3, 48, KV, D, page=16, device=DEV)
+    seen = []
+    layer = m.DraftLayer(*layer_weights(), cache, max_rows=200, rotate=lambda q, k, p: seen.append(p.clone()))
+    layer.prompt(rows(200, 63), i32([4, 24, 24, 60]))
+    p = seen.pop()
+    assert p.dtype == I32 and int(p.min()) >= 0 and int(p.max()) < cache.max_len
+    assert torch.equal(p[4:24], torch.arange(20, dtype=I32, device=DEV))
+    assert torch.equal(p[24:60], torch.arange(36, dtype=I32, device=DEV))
+    layer.prompt(rows(100, 64), i32([0, 100]))
+    p = seen.pop()
+    assert torch.equal(p, torch.arange(100, dtype=I32, device=DEV).clamp_(max=cache.max_len - 1))
+    layer.step(rows(6, 65), i32([0, 21, 60]))
+    assert seen.pop().tolist() == [0, 0, 19, 20, 47, 47]
+    layer.step(rows(3, 66), i32([1, 48, 22]))
+    assert seen.pop().tolist() == [0, 47, 21]
