@@ -121,11 +121,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // All ones in the halves of a BF16 pair that are infinite or NaN.
 __device__ __forceinline__ uint32_t nonfinite(uint32_t pair) { return __vcmpeq2(pair & 0x7F807F80u, 0x7F807F80u); }
 

@@ -166,6 +166,13 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b16) { return __uint_
 __device__ __forceinline__ float bf16_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t pair) { return __uint_as_float(pair & 0xFFFF0000u); }
 
+// 2^x (the hardware's approximation, subnormals flushed): a weight of the attentions, which 16 bits hold.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // s + e == a + b exactly (Knuth's TwoSum; no ordering requirement on |a|, |b|).
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = __fadd_rn(a, b);
