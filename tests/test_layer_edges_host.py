@@ -19,7 +19,9 @@ def test_prompt_kernel_joins_its_warps_by_bounded_waits_only():
     roles = kernel.index("if (warp >= 8) {"), kernel.rindex("give_up();")
     at = [i.start() for i in re.finditer(r"__syncthreads\(\)", kernel)]
     assert len(at) == 2 and at[0] < roles[0] and at[1] > roles[1]
-    assert "mbar_try_wait" not in kernel  # (mbar_wait_bounded alone)
+    wait = kernel[kernel.index("auto come ="):]  # polls stand in the bounded wait alone
+    wait = wait[:wait.index("};")]
+    assert kernel.count("mbar_try_wait") == wait.count("mbar_try_wait") and "<= p.wait_ns" in wait
 
 
 def test_prompt_kernel_lets_an_answer_under_way_land():
@@ -27,8 +29,8 @@ def test_prompt_kernel_lets_an_answer_under_way_land():
     followed by one with the full limit before the warp leaves."""
     text = source("attention_prompt.cu")
     asked = text.split("clusterlaunchcontrol.try_cancel")[1].split("clusterlaunchcontrol.query_cancel")[0]
-    waits = re.findall(r"mbar_wait_bounded\(smem_addr\(asked\), turn(, p\.wait_ns)?\)", asked)
-    assert waits == [", p.wait_ns", ""]
+    waits = re.findall(r"(come|mbar_wait_bounded)\(smem_addr\(asked\), turn\)", asked)
+    assert waits == ["come", "mbar_wait_bounded"]
     assert asked.index("break;") > asked.rindex("mbar_wait_bounded")
 
 
