@@ -12,7 +12,7 @@
 //
 // Measured: 4096 rows of 6144 columns with all three outputs (227 MB) 46 us, 4.9 TB/s where a copy makes 6.7; a row that is not
 // a multiple of 8 long costs its edges (1021 rows of 5003 columns without delta and codes, 20 MB: 10 us); 16 rows 5 us, a launch. Instructions bound
-// the long rows (issue slots 64 % busy): the exact squares' double-floats are a third of them.
+// the long rows (issue slots 64 % busy), the double-floats of exact squares among them, and the barriers between a row's phases.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -73,31 +73,47 @@ struct Root {
 __device__ __forceinline__ Root root_fp64(double r) {
   return Root{__int_as_float(__double2hiint(r)), __int_as_float(__double2loint(r)), 0.0f};
 }
-// The eight anew.
+// a + b (|b| below a few units of a) rounded to odd: the neighbour nearer zero, its last bit set where that is not the sum. A
+// following rounding to BF16 is that of the sum, without a branch.
+__device__ __forceinline__ float sum_to_odd(float a, float b) {
+  float s, err;
+  two_sum(a, b, s, err);
+  const uint32_t u = __float_as_uint(s);
+  const uint32_t back = err != 0.0f && ((__float_as_uint(err) ^ u) >> 31) != 0u ? 1u : 0u;
+  return __uint_as_float((u - back) | (err != 0.0f ? 1u : 0u));
+}
+// Eight columns by fp64; out of line, as it is long.
+static __device__ __noinline__ uint4 scaled8_fp64(uint4 x, uint4 w, double d) {
+  const uint32_t xu[4] = {x.x, x.y, x.z, x.w}, wu[4] = {w.x, w.y, w.z, w.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    o[t] = scaled_fp64(bf16_lo(xu[t]), bf16_lo(wu[t]), d) | (scaled_fp64(bf16_hi(xu[t]), bf16_hi(wu[t]), d) << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// The eight anew. (Without a branch, and the fp64 part apart from it: a CTA waits for its slowest warp, and one in fifty comes
+// here. With both in one place, 4096 rows of 6144 columns took 48 us, and 46 so.)
 static __device__ __noinline__ uint4 scaled_exact(uint4 x, uint4 w, Root r) {
   const uint32_t xu[4] = {x.x, x.y, x.z, x.w}, wu[4] = {w.x, w.y, w.z, w.w};
   uint32_t o[4];
   float lo = __int_as_float(0x7f800000), hi = 0.0f;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    uint32_t h[2];
+    float z[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float p = __fmul_rn(__fmul_rn(e ? bf16_hi(xu[t]) : bf16_lo(xu[t]), r.up), e ? bf16_hi(wu[t]) : bf16_lo(wu[t]));
       const float yh = __fmul_rn(p, r.rh), yl = __fmaf_rn(p, r.rl, __fmaf_rn(p, r.rh, -yh));
       lo = fminf(lo, fabsf(yh)), hi = fmaxf(hi, fabsf(yh));
-      h[e] = bf16_rne_df(yh, yl);
+      z[e] = sum_to_odd(yh, yl);
     }
-    o[t] = h[0] | (h[1] << 16);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[t]) : "f"(z[1]), "f"(z[0]));
   }
   // (double-floats hold it from 2^-101 on, where their parts are normal numbers)
-  if (r.up != 0.0f && lo >= 0x1p-101f && hi < __int_as_float(0x7f800000)) return make_uint4(o[0], o[1], o[2], o[3]);
+  if (r.up != 0.0f && lo >= 0x1p-101f && hi < 0x1p127f) return make_uint4(o[0], o[1], o[2], o[3]);
   const double d = r.up != 0.0f ? (static_cast<double>(r.rh) + static_cast<double>(r.rl)) * static_cast<double>(r.up)
                                 : __hiloint2double(__float_as_int(r.rh), __float_as_int(r.rl));
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-    o[t] = scaled_fp64(bf16_lo(xu[t]), bf16_lo(wu[t]), d) | (scaled_fp64(bf16_hi(xu[t]), bf16_hi(wu[t]), d) << 16);
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  return scaled8_fp64(x, w, d);
 }
 // Whether an x of the eight is not zero and x up is below 2^-142 (a power of two times eight bits from there on is exact).
 __device__ __forceinline__ bool tiny_among(const uint32_t (&x)[4], float up) {
