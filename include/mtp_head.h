@@ -584,8 +584,11 @@ int mtp_head_cache_read_fp4(const uint8_t* q, const uint8_t* block_scale, const 
  * With n = rows[b], row i < n sees the first length[b] - n + i + 1 tokens:
  *   out = sum_j p_j v_j,  p = softmax_j( scale q . k_j ),  0 < scale <= 2^60, |scale q . k_j| below 2^127
  * A row that sees no token gives zeros and lse -Inf. Rows i >= n are left as they were. What the pages hold
- * behind a sequence's tokens does not matter. Products take 16-bit operands (keys, values and query rows
- * exactly, weights in f16), sums are fp32; results do not vary from run to run.
+ * behind a sequence's tokens does not matter. Products take 16-bit operands (keys and values exactly, query
+ * elements to 2^-32 of their row's largest, weights in f16: one below 2^-25 of the heaviest that the same warp has
+ * met, 32 of 128 tokens at a time, is in the sum but not in the output), sums are fp32; results do not
+ * vary from run to run. How the work is cut up goes by max_pages * page, not by the lengths, which the host does
+ * not know: one short sequence, or many, are slower in a table that is much wider than they are.
  *   workspace   at least mtp_head_attention_fp4_workspace_bytes(B, Q, q_heads, kv_heads, D, max_pages *
  *               page) bytes, zero-filled once before its first use (the kernel leaves its counters zero); all
  *               of workspace_bytes may be written. One workspace serves every call of no larger B, Q,

@@ -30,7 +30,8 @@
 // took more instructions: their operands go through uniform registers, one lane after another.)
 //
 // Measured at 8 key heads of 6 query heads, D = 128: one row of each of 16 sequences of up to 32768 tokens (369 MB) 82 us,
-// 4.5 TB/s; five rows of each of 16 of up to 16384 (186 MB) 124 us; one sequence of 2048 tokens 14 us. Instructions
+// 4.5 TB/s; five rows of each of 16 of up to 16384 (186 MB) 124 us; one sequence of 2048 tokens 14 us (block tables as
+// wide as the longest sequence, here and below). Instructions
 // bound it, not memory: a lane's word of eight codes with its conversions, scales and one row tile's MMA takes 18 cycles of an
 // SM's quarter, and a second tile of rows 8 more. Four row tiles a warp left too few warps (180 us for the five rows);
 // wide operands in shared memory for the larger tensor-core instructions took longer to write than they saved (187 us).
@@ -89,10 +90,11 @@ inline size_t counters_bytes(int64_t pairs) { return (static_cast<size_t>(pairs)
 // The CTAs of a launch. Either no more than run at once, which share the rounds out: the GPU is evenly busy to the end, but each
 // CTA first sums up all lengths, and groups of rows are cut where shares end. Or one for every range of at most
 // kLongRange tokens of every group: their starts hide under others' work, but the last ones run alone. The latter where there
-// are more groups than CTAs at once, and these too short for their number: us with shares and with ranges for 800 groups
+// are more groups than CTAs at once, and tables too narrow for their number: us with shares and with ranges for 800 groups
 // of up to 500 tokens 24 and 20, of up to 3000 66 and 68, for 2048 groups of up to 500 61 and 38, 4000 169 and 159, 16000
 // 534 and 557. Or, where the whole call is no more than a round a CTA, one for every round (8 groups of 2048 tokens: 13.9 us,
-// 14.8 in shares).
+// 14.8 in shares). The host knows the table's width only: with lengths well below it the last two are not taken (in a table of 32768
+// tokens the 8 groups of 2048 take 16 to 17 us and the 2048 groups of up to 500 take 59).
 struct Plan {
   int ctas, splits;  // splits: 0 where CTAs share rounds out, else ranges per group
   Plan(int64_t pairs, int64_t max_len, int per_sm, int sms) {

@@ -7,7 +7,7 @@
 // shuffles and a warp's loads and stores are contiguous over whole heads. Reading takes D / 8 lanes a row. Bound by
 // bytes in principle: 4 D in and 2 (D/2 + D/16 + 4) out for a token's key and value of one head, or the other way round.
 // Measured at 16384 tokens of 8 heads, D = 128 (87 MB each way): 36 us for a write and the read after it, 4.8 TB/s;
-// writing is as much bound by its arithmetic (issue slots 58 % busy: correctly rounded quotients), reading by
+// writing is as much bound by its arithmetic (issue slots 56 % busy: correctly rounded quotients), reading by
 // the latency of small pieces (a row is 64, 8 and 4 bytes in three places). Few tokens: a launch each.
 #include <cuda_runtime.h>
 #include <stdint.h>

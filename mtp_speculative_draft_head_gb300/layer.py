@@ -130,7 +130,7 @@ class DraftLayer:
     def step(self, x, length, status=None, stream=None):
         """The layer over the next rows of each sequence, in place: x [B Q, H] (Q rows of each of B sequences, the
         first B of the cache), length [B] int32 (Q at least) the tokens that the cache holds with them. Their keys and values are
-        written to the cache first. The first step of another Q than 1 makes that Q's workspace, waits for its zero fill and is
+        written to the cache first. Every sequence has Q rows (mtp_head_attention_fp4 itself takes fewer of some). The first step of another Q than 1 makes that Q's workspace, waits for its zero fill and is
         not recorded into a graph: the fill would only run with the graph."""
         B = length.numel()
         if B < 1 or x.shape[0] < B or x.shape[0] % B != 0 or B > self.cache.batch:
@@ -159,8 +159,9 @@ class DraftLayer:
 
     def prompt(self, x, row_start, status=None, stream=None):
         """The layer over whole prompts, in place: x [T, H], sequence b's rows row_start[b] .. row_start[b + 1]
-        (row_start [B + 1] int32), from its first position on. Their keys and values fill the cache. Rows of no sequence
-        attend to nothing."""
+        (row_start [B + 1] int32), from its first position on. Their keys and values fill the cache. The rows attend to them in
+        BF16, as they are; steps attend to the cache's FP4 copies, so a row is not quite the same through either. Rows of
+        no sequence attend to nothing, but are projected all the same (the status tells a NaN in one)."""
         B = row_start.numel() - 1
         if B < 1 or B > self.cache.batch:
             raise ValueError("row_start: one sequence at least, and no more than the cache has")
